@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import (POINTER, byref, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t,
+from ctypes import (POINTER, byref, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t,
                     c_uint32, c_void_p)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -46,6 +46,8 @@ EXPORTS = [
     "fno_tucker_keep_intermediates", "fno_tucker_save_bytes",
     "fno_tucker_block_fwd", "fno_tucker_block_bwd", "fno_tucker_spectral_conv_fwd",
     "fno_tucker_spectral_conv_bwd", "fno_tucker_block_fwd_mse", "fno_tucker_block_bwd_preact",
+    "fno_layer_norm_fwd", "fno_layer_norm_workspace_bytes", "fno_layer_norm_bwd",
+    "fno_grad_norm_workspace_bytes", "fno_grad_norm", "fno_clip_grad_norm", "fno_adamw",
     "fno_timing_enable", "fno_timing_select",
     "fno_timing_reset", "fno_timing_count", "fno_timing_get", "fno_status_string",
     "fno_last_error_message",
@@ -56,6 +58,22 @@ class fno_plan_desc(ctypes.Structure):
     _fields_ = [("ndim", c_int32), ("spectral_dtype", c_int32), ("flags", c_uint32),
                 ("reserved", c_int32), ("batch", c_int64), ("c_in", c_int64),
                 ("c_out", c_int64), ("n", c_int64 * 4), ("modes", c_int64 * 4)]
+
+
+class fno_layer_norm_desc(ctypes.Structure):
+    _fields_ = [("dtype", c_int32), ("reserved", c_int32), ("batch", c_int64),
+                ("channels", c_int64), ("npts", c_int64), ("x_stride", c_int64),
+                ("y_stride", c_int64), ("grad_x_stride", c_int64), ("eps", c_double)]
+
+
+class fno_tensor(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("elems", c_int64), ("dtype", c_int32),
+                ("reserved", c_int32)]
+
+
+class fno_adamw_desc(ctypes.Structure):
+    _fields_ = [("lr", c_double), ("beta1", c_double), ("beta2", c_double), ("eps", c_double),
+                ("weight_decay", c_double), ("step", c_int64)]
 
 
 class FnoError(RuntimeError):
@@ -113,6 +131,15 @@ def _load():
                                              P, P, P, c_size_t, P]),
         "fno_tucker_block_bwd_preact": (c_int, [P, P, P, POINTER(c_void_p), P, P, P, P, P, P,
                                                 POINTER(c_void_p), P, P, P, c_size_t, P]),
+        "fno_layer_norm_fwd": (c_int, [POINTER(fno_layer_norm_desc), P, P, P, P, P, P]),
+        "fno_layer_norm_workspace_bytes": (c_int, [POINTER(fno_layer_norm_desc),
+                                                   POINTER(c_size_t)]),
+        "fno_layer_norm_bwd": (c_int, [POINTER(fno_layer_norm_desc), P, P, P, P, P, P, P, P,
+                                       c_size_t, P]),
+        "fno_grad_norm_workspace_bytes": (c_int, [c_int64, POINTER(c_size_t)]),
+        "fno_grad_norm": (c_int, [c_int64, P, c_float, c_float, P, P, c_size_t, P]),
+        "fno_clip_grad_norm": (c_int, [c_int64, P, P, c_float, c_float, P, P, c_size_t, P]),
+        "fno_adamw": (c_int, [c_int64, P, P, P, P, POINTER(fno_adamw_desc), P, P]),
         "fno_timing_enable": (c_int, [c_int]),
         "fno_timing_select": (c_int, [c_char_p]),
         "fno_timing_reset": (c_int, []),
@@ -250,6 +277,45 @@ def fno_mse_grad(n, y, t, grad, loss, ws, ws_bytes, stream):
 def fno_mse_grad_scaled(n, y, t, grad, loss, grad_scale, ws, ws_bytes, stream):
     _check(_lib.fno_mse_grad_scaled(n, y, t, grad, loss, grad_scale, ws, ws_bytes, stream),
            "fno_mse_grad_scaled")
+
+
+def fno_layer_norm_fwd(desc, x, gamma, beta, y, stats, stream):
+    _check(_lib.fno_layer_norm_fwd(byref(desc), x, gamma, beta, y, stats, stream),
+           "fno_layer_norm_fwd")
+
+
+def fno_layer_norm_workspace_bytes(desc) -> int:
+    b = c_size_t()
+    _check(_lib.fno_layer_norm_workspace_bytes(byref(desc), byref(b)),
+           "fno_layer_norm_workspace_bytes")
+    return b.value
+
+
+def fno_layer_norm_bwd(desc, x, gamma, stats, grad_y, grad_x, grad_gamma, grad_beta, ws, ws_bytes,
+                       stream):
+    _check(_lib.fno_layer_norm_bwd(byref(desc), x, gamma, stats, grad_y, grad_x, grad_gamma,
+                                   grad_beta, ws, ws_bytes, stream), "fno_layer_norm_bwd")
+
+
+def fno_grad_norm_workspace_bytes(count: int) -> int:
+    b = c_size_t()
+    _check(_lib.fno_grad_norm_workspace_bytes(count, byref(b)), "fno_grad_norm_workspace_bytes")
+    return b.value
+
+
+def fno_grad_norm(count, grads, max_norm, grad_scale, record, ws, ws_bytes, stream):
+    _check(_lib.fno_grad_norm(count, grads, max_norm, grad_scale, record, ws, ws_bytes, stream),
+           "fno_grad_norm")
+
+
+def fno_clip_grad_norm(count, grads, out, max_norm, grad_scale, record, ws, ws_bytes, stream):
+    _check(_lib.fno_clip_grad_norm(count, grads, out, max_norm, grad_scale, record, ws, ws_bytes,
+                                   stream), "fno_clip_grad_norm")
+
+
+def fno_adamw(count, params, grads, exp_avg, exp_avg_sq, desc, record, stream):
+    _check(_lib.fno_adamw(count, params, grads, exp_avg, exp_avg_sq, byref(desc), record, stream),
+           "fno_adamw")
 
 
 def fno_timing_enable(enable: bool) -> None:
@@ -704,3 +770,229 @@ def mse_grad(y, t, grad=None, loss=None, ws=None, grad_scale=1.0):
         fno_mse_grad_scaled(n, y.data_ptr(), t.data_ptr(), g.data_ptr(), lo.data_ptr(),
                             float(grad_scale), w.data_ptr(), w.numel(), stream)
     return lo, g
+
+
+# ---- training operators -----------------------------------------------------------------------
+def _data_dtype(t):
+    """fno_dtype of a tensor's elements (complex64 counts as pairs of float32)."""
+    import torch
+    kinds = {torch.float32: FNO_DTYPE_F32, torch.complex64: FNO_DTYPE_F32,
+             torch.bfloat16: FNO_DTYPE_BF16, torch.float16: FNO_DTYPE_F16}
+    if t.dtype not in kinds:
+        raise ValueError(f"float32, bfloat16 or float16 data expected, not {t.dtype}")
+    return kinds[t.dtype]
+
+
+class _Call:
+    """The current stream of a device, with the device current while the call is made."""
+
+    def __init__(self, device):
+        import torch
+        if device.type != "cuda":
+            raise ValueError(f"tensors on the GPU expected, not on {device}")
+        self._guard = None
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(device)
+        self.stream = torch.cuda.current_stream(device).cuda_stream
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _batch_stride(t, name):
+    """Elements between the batch entries of a field whose entries are packed."""
+    if t.is_contiguous():
+        return t[0].numel() if t.shape[0] else 0
+    if t.shape[0] and not t[0].is_contiguous():
+        raise ValueError(f"{name}: its batch entries must be packed (call .contiguous())")
+    return t.stride(0)
+
+
+def _like_x(t, x, name):
+    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
+        raise ValueError(f"{name}: needs x's shape, dtype and device, {tuple(x.shape)} "
+                         f"{x.dtype} on {x.device}")
+    return t
+
+
+def _float_vector(t, shape, x, name):
+    import torch
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != torch.float32
+                          or t.device != x.device or not t.is_contiguous()):
+        raise ValueError(f"{name}: needs packed float32 {tuple(shape)} on {x.device}")
+    return t
+
+
+def _norm_desc(x, eps):
+    if x.dim() < 2:
+        raise ValueError("layer norm: x is [batch, channels, *grid]")
+    d = fno_layer_norm_desc()
+    d.dtype = _data_dtype(x)
+    if x.is_complex():
+        raise ValueError("layer norm: x must be real")
+    d.batch, d.channels = x.shape[0], x.shape[1]
+    npts = 1
+    for n in x.shape[2:]:
+        npts *= n
+    d.npts = npts
+    d.x_stride = _batch_stride(x, "x")
+    d.eps = eps
+    return d
+
+
+def layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, out=None, stats=None, want_stats=True):
+    """Layer norm of a field [B, C, *grid] over its channels at each point ([rows, C]: over each
+    row), times gamma plus beta (float32 [C]; None: 1 and 0).  Returns (y, stats); stats, float32
+    [2, B, *grid], holds the means and the reciprocal deviations for layer_norm_bwd (None without
+    want_stats)."""
+    import torch
+    d = _norm_desc(x, eps)
+    y = _like_x(out, x, "out") if out is not None else torch.empty(x.shape, dtype=x.dtype,
+                                                                   device=x.device)
+    d.y_stride = _batch_stride(y, "out")
+    _float_vector(gamma, x.shape[1:2], x, "gamma")
+    _float_vector(beta, x.shape[1:2], x, "beta")
+    shape = (2, x.shape[0]) + tuple(x.shape[2:])
+    if stats is not None:
+        _float_vector(stats, shape, x, "stats")
+    elif want_stats:
+        stats = torch.empty(shape, dtype=torch.float32, device=x.device)
+    with _Call(x.device) as stream:
+        fno_layer_norm_fwd(d, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), _ptr(stats),
+                           stream)
+    return y, stats
+
+
+def layer_norm_bwd(x, gamma, stats, grad_y, want=("x", "gamma", "beta"), out=None, ws=None):
+    """Gradients of layer_norm_fwd from its x and stats: dict(x, gamma, beta), None where not
+    asked.  out: tensors to write instead of new ones (out["x"] may be grad_y itself).  ws: uint8
+    workspace of fno_layer_norm_workspace_bytes (allocated when None)."""
+    import torch
+    d = _norm_desc(x, 0.0)
+    d.y_stride = _batch_stride(_like_x(grad_y, x, "grad_y"), "grad_y")
+    _float_vector(gamma, x.shape[1:2], x, "gamma")
+    _float_vector(stats, (2, x.shape[0]) + tuple(x.shape[2:]), x, "stats")
+    o = out or {}
+    c = x.shape[1]
+    gx = o["x"] if "x" in o else (torch.empty(x.shape, dtype=x.dtype, device=x.device)
+                                  if "x" in want else None)
+    gg, gb = (o[k] if k in o else (torch.empty(c, dtype=torch.float32, device=x.device)
+                                   if k in want else None) for k in ("gamma", "beta"))
+    if gx is not None:
+        d.grad_x_stride = _batch_stride(_like_x(gx, x, "grad_x"), "grad_x")
+    _float_vector(gg, (c,), x, "grad_gamma")
+    _float_vector(gb, (c,), x, "grad_beta")
+    if ws is None and (gg is not None or gb is not None):
+        ws = torch.empty(max(fno_layer_norm_workspace_bytes(d), 16), dtype=torch.uint8,
+                         device=x.device)
+    with _Call(x.device) as stream:
+        fno_layer_norm_bwd(d, x.data_ptr(), _ptr(gamma), stats.data_ptr(), grad_y.data_ptr(),
+                           _ptr(gx), _ptr(gg), _ptr(gb), _ptr(ws),
+                           0 if ws is None else ws.numel() * ws.element_size(), stream)
+    return {"x": gx, "gamma": gg, "beta": gb}
+
+
+class TensorList:
+    """Tensors that one call goes over (gradients, parameters, moments): packed float32,
+    bfloat16, float16 or complex64 tensors on one GPU.  Holds the tensors and their addresses, so
+    it is made once for buffers that stay; functions that take one also take a plain sequence."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        flat = []
+        self.device = None
+        for i, t in enumerate(self.tensors):
+            if not t.is_contiguous() or t.is_conj() or t.is_neg():
+                raise ValueError(f"tensor {i} of the list is not packed (call .contiguous())")
+            if self.device is None:
+                self.device = t.device
+            elif t.device != self.device:
+                raise ValueError("the tensors of a list are on one device")
+            flat += (t.data_ptr(), t.numel() * (2 if t.is_complex() else 1), _data_dtype(t))
+        self.count = len(self.tensors)
+        self.array = (c_int64 * max(len(flat), 1))(*flat)  # fno_tensor[count], reserved = 0
+        self.ptr = ctypes.addressof(self.array)
+
+    def __len__(self):
+        return self.count
+
+
+def _tensor_list(ts):
+    ts = ts if isinstance(ts, TensorList) else TensorList(ts)
+    if ts.device is None:
+        import torch
+        ts.device = torch.device("cuda", torch.cuda.current_device())
+    return ts
+
+
+def _same_device(device, *others):
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"everything must be on {device}")
+
+
+def _record(record, device):
+    import torch
+    if record is None:
+        return torch.empty(2, dtype=torch.float32, device=device)
+    if record.numel() != 2 or record.dtype != torch.float32 or not record.is_contiguous():
+        raise ValueError("record: two packed float32")
+    return record
+
+
+def _norm_workspace(gl):
+    import torch
+    return torch.empty(fno_grad_norm_workspace_bytes(gl.count), dtype=torch.uint8,
+                       device=gl.device)
+
+
+def grad_norm(grads, max_norm=float("inf"), grad_scale=1.0, record=None, ws=None):
+    """The global norm of a list of gradients, which carry the loss scale grad_scale, and what
+    clipping to max_norm multiplies them by: a device tensor record = [norm, factor] (see
+    fno_grad_norm)."""
+    gl = _tensor_list(grads)
+    record = _record(record, gl.device)
+    ws = ws if ws is not None else _norm_workspace(gl)
+    _same_device(gl.device, record, ws)
+    with _Call(gl.device) as stream:
+        fno_grad_norm(gl.count, gl.ptr, max_norm, grad_scale, record.data_ptr(), ws.data_ptr(),
+                      ws.numel() * ws.element_size(), stream)
+    return record
+
+
+def clip_grad_norm(grads, max_norm, grad_scale=1.0, out=None, record=None, ws=None):
+    """grad_norm, and every gradient times the factor, in place or into the tensors of `out` (of
+    the gradient's dtype or float32).  Returns the record [norm, factor]."""
+    gl = _tensor_list(grads)
+    ol = gl if out is None else _tensor_list(out)
+    if ol.count != gl.count:
+        raise ValueError("out lists another number of tensors")
+    record = _record(record, gl.device)
+    ws = ws if ws is not None else _norm_workspace(gl)
+    _same_device(gl.device, record, ws, ol)
+    with _Call(gl.device) as stream:
+        fno_clip_grad_norm(gl.count, gl.ptr, ol.ptr, max_norm, grad_scale, record.data_ptr(),
+                           ws.data_ptr(), ws.numel() * ws.element_size(), stream)
+    return record
+
+
+def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps=1e-8,
+          weight_decay=0.01, record=None):
+    """One AdamW update, number `step` (from 1), of float32 (or complex64, as pairs) parameters in
+    place, from gradients times the factor of `record` (grad_norm's; None: as they are).  A factor
+    that is not finite leaves parameters and moments as they are."""
+    pl, gl, ml, vl = (_tensor_list(t) for t in (params, grads, exp_avg, exp_avg_sq))
+    if not pl.count == gl.count == ml.count == vl.count:
+        raise ValueError("the four lists need the same number of tensors")
+    d = fno_adamw_desc(lr, betas[0], betas[1], eps, weight_decay, step)
+    if record is not None:
+        _record(record, pl.device)
+    _same_device(pl.device, gl, ml, vl, record)
+    with _Call(pl.device) as stream:
+        fno_adamw(pl.count, pl.ptr, gl.ptr, ml.ptr, vl.ptr, d, _ptr(record), stream)

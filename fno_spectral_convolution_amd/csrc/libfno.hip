@@ -4,12 +4,14 @@
 // static scratch array of fno_block_fwd_static (the runtime places it when it loads the
 // library's code on a device).
 #include "fno_internal.h"
+#include "train_ops.h"
 
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 #include <new>
 #include <cmath>
@@ -1752,3 +1754,300 @@ fno_status fno_timing_get(int index, const char** name, int64_t* launches, doubl
 
 }  // extern "C"
 
+// ---- training operators ------------------------------------------------------------------
+namespace {
+
+bool aligned_to(const void* p, size_t n) {
+  return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+size_t dtype_bytes(int32_t dtype) { return dtype == FNO_DTYPE_F32 ? 4 : 2; }
+bool known_dtype(int32_t d) {
+  return d == FNO_DTYPE_F32 || d == FNO_DTYPE_BF16 || d == FNO_DTYPE_F16;
+}
+
+// a data pointer that has to be there, at a multiple of `bytes`
+#define REQ_AT(ptr, name, bytes)                                                     \
+  do {                                                                               \
+    if (!(ptr)) return fail(FNO_ERR_INVALID_ARGUMENT, "%s is NULL", name);           \
+    if (!aligned_to(ptr, bytes))                                                     \
+      return fail(FNO_ERR_INVALID_ARGUMENT, "%s is not %d-byte aligned", name, (int)(bytes)); \
+  } while (0)
+
+#define OPT_AT(ptr, name, bytes) \
+  do {                           \
+    if (ptr) REQ_AT(ptr, name, bytes); \
+  } while (0)
+
+fno_status norm_args(const fno_layer_norm_desc* d, fno::NormArgs* a) {
+  if (!d) return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm descriptor is NULL");
+  if (!known_dtype(d->dtype)) return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: unknown dtype");
+  if (d->reserved != 0) return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: reserved must be 0");
+  if (d->batch < 0 || d->npts < 0 || d->channels < 1)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: batch, npts >= 0 and channels >= 1");
+  if (d->x_stride < 0 || d->y_stride < 0 || d->grad_x_stride < 0)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: strides must be >= 0");
+  if (!(d->eps >= 0.0) || !std::isfinite(d->eps))
+    return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: eps must be finite and >= 0");
+  if (d->channels >= (int64_t)1 << 31)
+    return fail(FNO_ERR_UNSUPPORTED, "layer norm: channels >= 2^31");
+  // every byte offset into every operand fits 62 bits
+  const int64_t lim = (int64_t)1 << 60;
+  int64_t per, rows, span;
+  const int64_t st = std::max(std::max(d->x_stride, d->y_stride), d->grad_x_stride);
+  if (__builtin_mul_overflow(d->channels, d->npts, &per) || per > lim ||
+      __builtin_mul_overflow(d->batch, d->npts, &rows) || rows > lim ||
+      __builtin_mul_overflow(d->batch, st, &span) || span > lim)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: sizes overflow");
+  a->batch = d->batch;
+  a->npts = d->npts;
+  a->channels = (int)d->channels;
+  a->x_stride = d->x_stride;
+  a->y_stride = d->y_stride;
+  a->gx_stride = d->grad_x_stride;
+  a->eps = (float)d->eps;
+  return FNO_OK;
+}
+
+bool norm_writes_overlap(const fno::NormArgs& a, int64_t stride) {
+  return a.batch > 1 && stride < (int64_t)a.channels * a.npts;
+}
+
+size_t norm_workspace(const fno::NormArgs& a, int32_t dtype) {
+  return align_up(sizeof(float) * 2 * (size_t)a.channels * (size_t)fno::layer_norm_parts(a, dtype));
+}
+
+// elements of one tensor: a table's chunk numbers then stay below 2^31
+constexpr int64_t kMaxElems = (int64_t)1 << 36;
+
+fno_status check_list(int64_t count, const fno_tensor* t, const char* name) {
+  if (count < 0) return fail(FNO_ERR_INVALID_ARGUMENT, "count < 0");
+  if (count > 0 && !t) return fail(FNO_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+  for (int64_t i = 0; i < count; ++i) {
+    const fno_tensor& e = t[i];
+    if (!known_dtype(e.dtype) || e.reserved != 0 || e.elems < 0 || e.elems > kMaxElems)
+      return fail(FNO_ERR_INVALID_ARGUMENT, "%s[%lld]: bad dtype, reserved or elems", name,
+                  (long long)i);
+    if (e.elems > 0 && (!e.data || !aligned_to(e.data, dtype_bytes(e.dtype))))
+      return fail(FNO_ERR_INVALID_ARGUMENT, "%s[%lld]: NULL or not aligned to its elements", name,
+                  (long long)i);
+  }
+  return FNO_OK;
+}
+
+// Calls flush(table, groups) with tables of up to Cap of the lists' tensors that have elements,
+// each with at most `most` work-groups.
+template <typename Table, int Lists, int Cap, typename Flush>
+fno_status walk_lists(int64_t count, const fno_tensor* const (&lists)[Lists], int most,
+                             Flush&& flush) {
+  Table t;
+  t.count = 0;
+  t.first[0] = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const int64_t n = lists[0][i].elems;
+    if (n > 0) {
+      const int k = t.count++;
+      for (int l = 0; l < Lists; ++l) t.ptr[l][k] = lists[l][i].data;
+      t.elems[k] = n;
+      t.dtype[k] = (uint8_t)(lists[0][i].dtype | (lists[1][i].dtype << 4));
+      t.first[k + 1] = t.first[k] + (uint32_t)((n + fno::kChunk - 1) / fno::kChunk);
+    }
+    if (t.count > 0 && (t.count == Cap || i == count - 1)) {
+      const uint32_t chunks = t.first[t.count];
+      const fno_status st = flush(t, (int)(chunks < (uint32_t)most ? chunks : (uint32_t)most));
+      if (st != FNO_OK) return st;
+      t.count = 0;
+    }
+  }
+  return FNO_OK;
+}
+
+size_t norm_parts_bytes(int64_t count) {
+  const int64_t tables = count / fno::kNormTensors + 1;
+  return sizeof(double) * (size_t)tables * fno::kNormParts;
+}
+
+fno_status grad_norm_impl(int64_t count, const fno_tensor* grads, float max_norm,
+                                 float grad_scale, float* record, void* ws, size_t ws_bytes,
+                                 hipStream_t s) {
+  fno_status st = check_list(count, grads, "grads");
+  if (st != FNO_OK) return st;
+  if (!(max_norm > 0.0f)) return fail(FNO_ERR_INVALID_ARGUMENT, "max_norm must be > 0");
+  if (!(grad_scale > 0.0f) || !std::isfinite(grad_scale))
+    return fail(FNO_ERR_INVALID_ARGUMENT, "grad_scale must be finite and > 0");
+  REQ_AT(record, "record", sizeof(float));
+  REQ(ws, "workspace");
+  if (ws_bytes < norm_parts_bytes(count))
+    return fail(FNO_ERR_INVALID_ARGUMENT, "workspace too small");
+  double* part = static_cast<double*>(ws);
+  int nparts = 0;
+  const fno_tensor* const lists[2] = {grads, grads};
+  st = walk_lists<fno::NormTable, 2, fno::kNormTensors>(
+      count, lists, fno::kNormParts, [&](const fno::NormTable& t, int groups) -> fno_status {
+        LAUNCH("grad_norm", s, fno::launch_norm_part(t, groups, part + nparts, s));
+        nparts += groups;
+        return FNO_OK;
+      });
+  if (st != FNO_OK) return st;
+  LAUNCH("grad_norm_finish", s,
+         fno::launch_norm_finish(part, nparts, max_norm, grad_scale, record, s));
+  return FNO_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fno_status fno_layer_norm_fwd(const fno_layer_norm_desc* desc, const void* x, const float* gamma,
+                              const float* beta, void* y, float* stats, void* stream) {
+  fno::NormArgs a;
+  fno_status st = norm_args(desc, &a);
+  if (st != FNO_OK) return st;
+  if (norm_writes_overlap(a, a.y_stride))
+    return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: y_stride < channels * npts");
+  if (a.batch == 0 || a.npts == 0) return FNO_OK;
+  const size_t w = dtype_bytes(desc->dtype);
+  REQ_AT(x, "x", w);
+  REQ_AT(y, "y", w);
+  OPT_AT(gamma, "gamma", sizeof(float));
+  OPT_AT(beta, "beta", sizeof(float));
+  OPT_AT(stats, "stats", sizeof(float));
+  if (x == y && a.batch > 1 && a.x_stride != a.y_stride)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm in place needs x_stride == y_stride");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LAUNCH("layer_norm_fwd", s,
+         fno::launch_layer_norm_fwd(a, desc->dtype, x, gamma, beta, y, stats, s));
+  return FNO_OK;
+}
+
+fno_status fno_layer_norm_workspace_bytes(const fno_layer_norm_desc* desc, size_t* bytes) {
+  if (!bytes) return fail(FNO_ERR_INVALID_ARGUMENT, "bytes is NULL");
+  fno::NormArgs a;
+  fno_status st = norm_args(desc, &a);
+  if (st != FNO_OK) return st;
+  *bytes = norm_workspace(a, desc->dtype);
+  return FNO_OK;
+}
+
+fno_status fno_layer_norm_bwd(const fno_layer_norm_desc* desc, const void* x, const float* gamma,
+                              const float* stats, const void* grad_y, void* grad_x,
+                              float* grad_gamma, float* grad_beta, void* ws, size_t ws_bytes,
+                              void* stream) {
+  fno::NormArgs a;
+  fno_status st = norm_args(desc, &a);
+  if (st != FNO_OK) return st;
+  if (grad_x && norm_writes_overlap(a, a.gx_stride))
+    return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: grad_x_stride < channels * npts");
+  OPT_AT(grad_gamma, "grad_gamma", sizeof(float));
+  OPT_AT(grad_beta, "grad_beta", sizeof(float));
+  const bool weights = grad_gamma || grad_beta, none = a.batch == 0 || a.npts == 0;
+  if (!none) {
+    const size_t w = dtype_bytes(desc->dtype);
+    REQ_AT(x, "x", w);
+    REQ_AT(grad_y, "grad_y", w);
+    REQ_AT(stats, "stats", sizeof(float));
+    OPT_AT(gamma, "gamma", sizeof(float));
+    OPT_AT(grad_x, "grad_x", w);
+    if (a.batch > 1 && ((grad_x == x && a.gx_stride != a.x_stride) ||
+                        (grad_x == grad_y && a.gx_stride != a.y_stride)))
+      return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm in place needs equal strides");
+    if (weights) {
+      REQ(ws, "workspace");
+      if (ws_bytes < norm_workspace(a, desc->dtype))
+        return fail(FNO_ERR_INVALID_ARGUMENT, "workspace too small");
+    }
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  float* part = weights ? static_cast<float*>(ws) : nullptr;
+  if (!none && (weights || grad_x))
+    LAUNCH("layer_norm_bwd", s,
+           fno::launch_layer_norm_bwd(a, desc->dtype, x, gamma, stats, grad_y, grad_x, part, s));
+  if (weights)
+    LAUNCH("layer_norm_finish", s,
+           fno::launch_layer_norm_finish(a, none ? 0 : fno::layer_norm_parts(a, desc->dtype),
+                                         part, grad_gamma, grad_beta, s));
+  return FNO_OK;
+}
+
+fno_status fno_grad_norm_workspace_bytes(int64_t count, size_t* bytes) {
+  if (count < 0 || count > (int64_t)1 << 40 || !bytes)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "bad gradient norm workspace query");
+  *bytes = norm_parts_bytes(count);
+  return FNO_OK;
+}
+
+fno_status fno_grad_norm(int64_t count, const fno_tensor* grads, float max_norm,
+                         float grad_scale, float* record, void* ws, size_t ws_bytes,
+                         void* stream) {
+  return grad_norm_impl(count, grads, max_norm, grad_scale, record, ws, ws_bytes,
+                        static_cast<hipStream_t>(stream));
+}
+
+fno_status fno_clip_grad_norm(int64_t count, const fno_tensor* grads, const fno_tensor* out,
+                              float max_norm, float grad_scale, float* record, void* ws,
+                              size_t ws_bytes, void* stream) {
+  fno_status st = check_list(count, grads, "grads");
+  if (st == FNO_OK) st = check_list(count, out, "out");
+  if (st != FNO_OK) return st;
+  for (int64_t i = 0; i < count; ++i) {
+    if (out[i].elems != grads[i].elems)
+      return fail(FNO_ERR_INVALID_ARGUMENT, "out[%lld]: another number of elements",
+                  (long long)i);
+    if (out[i].dtype != grads[i].dtype &&
+        (out[i].dtype != FNO_DTYPE_F32 || (out[i].elems > 0 && out[i].data == grads[i].data)))
+      return fail(FNO_ERR_INVALID_ARGUMENT,
+                  "out[%lld]: not its gradient's dtype, nor float32 apart from it", (long long)i);
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  st = grad_norm_impl(count, grads, max_norm, grad_scale, record, ws, ws_bytes, s);
+  if (st != FNO_OK) return st;
+  const fno_tensor* const lists[2] = {grads, out};
+  return walk_lists<fno::NormTable, 2, fno::kNormTensors>(
+      count, lists, 2048, [&](const fno::NormTable& t, int groups) -> fno_status {
+        LAUNCH("grad_clip", s, fno::launch_clip(t, groups, record, s));
+        return FNO_OK;
+      });
+}
+
+fno_status fno_adamw(int64_t count, const fno_tensor* params, const fno_tensor* grads,
+                     const fno_tensor* exp_avg, const fno_tensor* exp_avg_sq,
+                     const fno_adamw_desc* d, const float* record, void* stream) {
+  if (!d) return fail(FNO_ERR_INVALID_ARGUMENT, "AdamW descriptor is NULL");
+  if (!std::isfinite(d->lr) || !std::isfinite(d->weight_decay) || !(d->eps >= 0.0) ||
+      !std::isfinite(d->eps) || !(d->beta1 >= 0.0 && d->beta1 < 1.0) ||
+      !(d->beta2 >= 0.0 && d->beta2 < 1.0) || d->step < 1)
+    return fail(FNO_ERR_INVALID_ARGUMENT,
+                "AdamW: lr, weight_decay finite, eps >= 0, betas in [0, 1), step >= 1");
+  fno_status st = check_list(count, params, "params");
+  if (st == FNO_OK) st = check_list(count, grads, "grads");
+  if (st == FNO_OK) st = check_list(count, exp_avg, "exp_avg");
+  if (st == FNO_OK) st = check_list(count, exp_avg_sq, "exp_avg_sq");
+  if (st != FNO_OK) return st;
+  for (int64_t i = 0; i < count; ++i) {
+    const int64_t n = params[i].elems;
+    if (grads[i].elems != n || exp_avg[i].elems != n || exp_avg_sq[i].elems != n)
+      return fail(FNO_ERR_INVALID_ARGUMENT, "AdamW: tensor %lld has different elems in its lists",
+                  (long long)i);
+    if (params[i].dtype != FNO_DTYPE_F32 || exp_avg[i].dtype != FNO_DTYPE_F32 ||
+        exp_avg_sq[i].dtype != FNO_DTYPE_F32)
+      return fail(FNO_ERR_UNSUPPORTED, "AdamW: parameters and moments are float32");
+  }
+  OPT_AT(record, "record", sizeof(float));
+  fno::AdamArgs a;
+  a.beta1 = (float)d->beta1;
+  a.beta2 = (float)d->beta2;
+  a.one_minus_beta1 = (float)(1.0 - d->beta1);
+  a.one_minus_beta2 = (float)(1.0 - d->beta2);
+  a.decay = (float)(1.0 - d->lr * d->weight_decay);
+  a.step_size = (float)(d->lr / (1.0 - std::pow(d->beta1, (double)d->step)));
+  a.inv_bias2 = (float)(1.0 / std::sqrt(1.0 - std::pow(d->beta2, (double)d->step)));
+  a.eps = (float)d->eps;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const fno_tensor* const lists[4] = {params, grads, exp_avg, exp_avg_sq};
+  return walk_lists<fno::AdamTable, 4, fno::kAdamTensors>(
+      count, lists, 2048, [&](const fno::AdamTable& t, int groups) -> fno_status {
+        LAUNCH("adamw", s, fno::launch_adamw(t, groups, a, record, s));
+        return FNO_OK;
+      });
+}
+
+}  // extern "C"

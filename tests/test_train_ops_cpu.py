@@ -1,0 +1,168 @@
+"""Argument checks of the training operators (layer norm, gradient norm and clipping, AdamW) that
+the library makes on the host before any HIP call, and the binding's own."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from fno_spectral_convolution_amd import binding as L
+
+BAD = L.FNO_ERR_INVALID_ARGUMENT
+P = 1 << 20  # an aligned address that no call gets as far as reading
+
+
+def _desc(**kw):
+    base = dict(dtype=0, reserved=0, batch=4, channels=8, npts=3, x_stride=24, y_stride=24,
+                grad_x_stride=24, eps=1e-5)
+    base.update(kw)
+    d = L.fno_layer_norm_desc()
+    for k, v in base.items():
+        setattr(d, k, v)
+    return d
+
+
+def _fwd(d, x=P, gamma=P, beta=P, y=P, stats=P):
+    return L._lib.fno_layer_norm_fwd(d, x, gamma, beta, y, stats, None)
+
+
+def _bwd(d, x=P, gamma=P, stats=P, gy=P, gx=P, gg=P, gb=P, ws=P, ws_bytes=1 << 30):
+    return L._lib.fno_layer_norm_bwd(d, x, gamma, stats, gy, gx, gg, gb, ws, ws_bytes, None)
+
+
+def test_struct_layouts():
+    assert ctypes.sizeof(L.fno_layer_norm_desc) == 8 + 3 * 8 + 3 * 8 + 8
+    assert ctypes.sizeof(L.fno_tensor) == 24
+    assert ctypes.sizeof(L.fno_adamw_desc) == 48
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=3), BAD), (dict(reserved=1), BAD), (dict(batch=-1), BAD), (dict(npts=-1), BAD),
+    (dict(channels=0), BAD), (dict(x_stride=-1), BAD), (dict(eps=-1e-9), BAD),
+    (dict(eps=math.nan), BAD), (dict(eps=math.inf), BAD), (dict(npts=1 << 62), BAD),
+    (dict(batch=1 << 50, x_stride=1 << 40), BAD),
+    (dict(channels=1 << 31), L.FNO_ERR_UNSUPPORTED),
+])
+def test_layer_norm_descriptor_refused(kw, status):
+    d = _desc(**kw)
+    assert _fwd(d) == status and L.last_error_message()
+    assert _bwd(d) == status
+    n = ctypes.c_size_t()
+    assert L._lib.fno_layer_norm_workspace_bytes(d, ctypes.byref(n)) == status
+
+
+def test_layer_norm_pointers_refused():
+    d = _desc()
+    assert L._lib.fno_layer_norm_fwd(None, P, P, P, P, P, None) == BAD
+    for kw in (dict(x=None), dict(y=None), dict(x=P + 2), dict(y=P + 1), dict(gamma=P + 2),
+               dict(beta=P + 2), dict(stats=P + 1)):
+        assert _fwd(d, **kw) == BAD, kw
+    assert _fwd(_desc(dtype=1), x=P + 1) == BAD
+    assert _fwd(_desc(y_stride=23)) == BAD            # outputs would overlap
+    assert _fwd(_desc(x_stride=30)) == BAD            # in place with another stride
+    for kw in (dict(x=None), dict(gy=None), dict(stats=None), dict(gx=P + 2), dict(gg=P + 2),
+               dict(gb=P + 1), dict(ws=None), dict(ws=P + 8), dict(ws_bytes=0)):
+        assert _bwd(d, **kw) == BAD, kw
+    assert _bwd(_desc(grad_x_stride=23)) == BAD
+    assert _bwd(_desc(y_stride=30)) == BAD            # grad_x is grad_y with another stride
+    assert L._lib.fno_layer_norm_workspace_bytes(d, None) == BAD
+
+
+def test_layer_norm_without_rows_needs_no_pointers():
+    for kw in (dict(batch=0), dict(npts=0)):
+        assert _fwd(_desc(**kw), None, None, None, None, None) == L.FNO_OK
+        assert _bwd(_desc(**kw), None, None, None, None, None, None, None, None, 0) == L.FNO_OK
+
+
+def _list(*entries):
+    a = (L.fno_tensor * max(len(entries), 1))()
+    for e, (data, n, dt) in zip(a, entries):
+        e.data, e.elems, e.dtype, e.reserved = data, n, dt, 0
+    return a
+
+
+def _norm(n, g, max_norm=1.0, scale=1.0, record=P, ws=P, ws_bytes=1 << 30):
+    return L._lib.fno_grad_norm(n, g, max_norm, scale, record, ws, ws_bytes, None)
+
+
+def test_tensor_lists_refused():
+    ok = _list((P, 4, 0))
+    for n, g in ((-1, ok), (1, None), (1, _list((None, 4, 0))), (1, _list((P + 2, 4, 0))),
+                 (1, _list((P, -1, 0))), (1, _list((P, 4, 9))), (1, _list((P, 1 << 37, 0)))):
+        assert _norm(n, g) == BAD
+        assert L._lib.fno_clip_grad_norm(n, g, g, 1.0, 1.0, P, P, 1 << 30, None) == BAD
+    odd = _list((P, 4, 0))
+    odd[0].reserved = 1
+    assert _norm(1, odd) == BAD
+    for kw in (dict(max_norm=0.0), dict(max_norm=-1.0), dict(max_norm=math.nan), dict(scale=0.0),
+               dict(scale=math.inf), dict(scale=math.nan), dict(record=None), dict(record=P + 2),
+               dict(ws=None), dict(ws=P + 4), dict(ws_bytes=0)):
+        assert _norm(1, ok, **kw) == BAD, kw
+    n = ctypes.c_size_t()
+    assert L._lib.fno_grad_norm_workspace_bytes(-1, ctypes.byref(n)) == BAD
+    assert L._lib.fno_grad_norm_workspace_bytes(1, None) == BAD
+
+
+def test_clip_outputs_refused():
+    half = _list((P, 4, 1))
+    for out in (_list((P, 5, 1)), _list((P, 4, 0)), _list((P, 4, 2)), _list((2 * P, 4, 2))):
+        assert L._lib.fno_clip_grad_norm(1, half, out, 1.0, 1.0, P, P, 1 << 30, None) == BAD
+    full = _list((P, 4, 0))
+    assert L._lib.fno_clip_grad_norm(1, full, _list((2 * P, 4, 1)), 1.0, 1.0, P, P, 1 << 30,
+                                     None) == BAD
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lr=math.nan), dict(lr=math.inf), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0),
+    dict(beta2=math.nan), dict(eps=-1.0), dict(eps=math.inf), dict(weight_decay=math.nan),
+    dict(step=0),
+])
+def test_adamw_descriptor_refused(kw):
+    base = dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, weight_decay=0.0, step=1)
+    base.update(kw)
+    t = _list((P, 4, 0))
+    assert L._lib.fno_adamw(1, t, t, t, t, L.fno_adamw_desc(**base), None, None) == BAD
+
+
+def test_adamw_lists_refused():
+    d = L.fno_adamw_desc(1e-3, 0.9, 0.99, 1e-8, 0.0, 1)
+    t, more, half = _list((P, 4, 0)), _list((P, 5, 0)), _list((P, 4, 1))
+    assert L._lib.fno_adamw(1, t, t, t, t, None, None, None) == BAD
+    for lists in ((t, more, t, t), (t, t, more, t), (t, t, t, more), (None, t, t, t)):
+        assert L._lib.fno_adamw(1, *lists, d, None, None) == BAD
+    assert L._lib.fno_adamw(1, t, t, t, t, d, P + 2, None) == BAD
+    for lists in ((half, t, t, t), (t, t, half, t), (t, t, t, half)):
+        assert L._lib.fno_adamw(1, *lists, d, None, None) == L.FNO_ERR_UNSUPPORTED
+    assert L._lib.fno_adamw(0, None, None, None, None, d, None, None) == L.FNO_OK
+
+
+def test_binding_refuses():
+    x = torch.zeros(4, 8, 6)
+    with pytest.raises(ValueError, match="GPU"):
+        L.layer_norm_fwd(x)
+    with pytest.raises(ValueError, match="float32"):
+        L.layer_norm_fwd(x.double())
+    with pytest.raises(ValueError, match="batch, channels"):
+        L.layer_norm_fwd(x[0, 0])
+    with pytest.raises(ValueError, match="packed"):
+        L.layer_norm_fwd(x.transpose(1, 2))
+    with pytest.raises(ValueError, match="real"):
+        L.layer_norm_fwd(x.to(torch.complex64))
+    with pytest.raises(ValueError, match="gamma"):
+        L.layer_norm_fwd(x, torch.ones(7))
+    with pytest.raises(ValueError, match="out"):
+        L.layer_norm_fwd(x, out=x[:2])
+    with pytest.raises(ValueError, match="stats"):
+        L.layer_norm_bwd(x, None, torch.zeros(2, 4), x)
+    with pytest.raises(ValueError, match="grad_y"):
+        L.layer_norm_bwd(x, None, torch.zeros(2, 4, 6), x.bfloat16())
+    with pytest.raises(ValueError, match="packed"):
+        L.TensorList([x, x.transpose(0, 1)])
+    with pytest.raises(ValueError, match="float32"):
+        L.TensorList([x.double()])
+    with pytest.raises(ValueError, match="GPU"):
+        L.grad_norm([x], record=torch.zeros(2), ws=torch.zeros(64, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="record"):
+        L.grad_norm([x], record=torch.zeros(3))
+    with pytest.raises(ValueError, match="same number"):
+        L.adamw([x], [x, x], [x], [x], 1, 1e-3)
