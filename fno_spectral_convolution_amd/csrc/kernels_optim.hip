@@ -1,4 +1,5 @@
 // The global gradient norm over a list of tensors, clipping, and the AdamW update.
+#include "train_device.h"
 #include "train_ops.h"
 
 namespace fno {

@@ -1,0 +1,83 @@
+// Device helpers of the training operators: element types, unaligned vectors, wave sums.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fno {
+
+// ---- element types ---------------------------------------------------------------------------
+// float32, bfloat16 and IEEE half data as float; half results are rounded to nearest-even.
+template <typename T>
+__device__ __forceinline__ float to_float(T v) {
+  return (float)v;
+}
+template <typename T>
+__device__ __forceinline__ T from_float(float v) {
+  return (T)v;
+}
+
+// `N` packed elements at any multiple of the element size, as one load or store of N * sizeof(T)
+// bytes: the global memory instructions take 16 bytes at any address (gfx950 runs in unaligned
+// access mode), so odd row lengths and views need no code of their own.
+template <typename T, int N>
+struct __attribute__((packed, aligned(sizeof(T)))) Pack {
+  T v[N];
+};
+template <typename T, int N>
+__device__ __forceinline__ void load_pack(const T* p, float (&f)[N]) {
+  const Pack<T, N> q = *reinterpret_cast<const Pack<T, N>*>(p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = to_float(q.v[i]);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_pack(T* p, const float (&f)[N]) {
+  Pack<T, N> q;
+#pragma unroll
+  for (int i = 0; i < N; ++i) q.v[i] = from_float<T>(f[i]);
+  *reinterpret_cast<Pack<T, N>*>(p) = q;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const Pack<T, N>& q, float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = to_float(q.v[i]);
+}
+
+// ---- sums over lanes ---------------------------------------------------------------------------
+template <int Ctrl>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), Ctrl, 0xf, 0xf, true));
+}
+// v of lane ^ 16 (ROW 16) or lane ^ 32 (ROW 32) added to v; both lanes add the same two numbers
+template <int Row>
+__device__ __forceinline__ float add_across(float v) {
+  const unsigned u = __float_as_uint(v);
+  const auto r = Row == 16 ? __builtin_amdgcn_permlane16_swap(u, u, false, false)
+                           : __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Sum over the aligned groups of N lanes (8, 16, 32 or 64), the same bits in every lane: six
+// vector instructions for a wave and no trip through LDS.  Quad permutes reach lanes ^ 1 and ^ 2;
+// with whole quads equal the half-row mirror stands for lane ^ 4, then the row mirror for ^ 8.
+template <int N>
+__device__ __forceinline__ float lane_sum(float v) {
+  v += dpp<0xb1>(v);
+  v += dpp<0x4e>(v);
+  v += dpp<0x141>(v);
+  if (N >= 16) v += dpp<0x140>(v);
+  if (N >= 32) v = add_across<16>(v);
+  if (N >= 64) v = add_across<32>(v);
+  return v;
+}
+// Sum over the lanes of a wave that share lane % N (N = 8, 16, 32; 64: v itself).
+template <int N>
+__device__ __forceinline__ float stride_sum(float v) {
+  if (N <= 8) v += dpp<0x128>(v);  // rotation of the row by 8
+  if (N <= 16) v = add_across<16>(v);
+  if (N <= 32) v = add_across<32>(v);
+  return v;
+}
+
+}  // namespace fno

@@ -9,38 +9,6 @@
 
 namespace fno {
 
-// ---- element types ---------------------------------------------------------------------------
-// float32, bfloat16 and IEEE half data as float; half results are rounded to nearest-even.
-template <typename T>
-__device__ __forceinline__ float to_float(T v) {
-  return (float)v;
-}
-template <typename T>
-__device__ __forceinline__ T from_float(float v) {
-  return (T)v;
-}
-
-// `N` packed elements at any multiple of the element size, as one load or store of N * sizeof(T)
-// bytes: the global memory instructions take 16 bytes at any address (gfx950 runs in unaligned
-// access mode), so odd row lengths and views need no code of their own.
-template <typename T, int N>
-struct __attribute__((packed, aligned(sizeof(T)))) Pack {
-  T v[N];
-};
-template <typename T, int N>
-__device__ __forceinline__ void load_pack(const T* p, float (&f)[N]) {
-  const Pack<T, N> q = *reinterpret_cast<const Pack<T, N>*>(p);
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = to_float(q.v[i]);
-}
-template <typename T, int N>
-__device__ __forceinline__ void store_pack(T* p, const float (&f)[N]) {
-  Pack<T, N> q;
-#pragma unroll
-  for (int i = 0; i < N; ++i) q.v[i] = from_float<T>(f[i]);
-  *reinterpret_cast<Pack<T, N>*>(p) = q;
-}
-
 // ---- layer norm (kernels_layernorm.hip) ------------------------------------------------------
 struct NormArgs {
   int64_t batch, npts;
@@ -50,7 +18,7 @@ struct NormArgs {
 };
 hipError_t launch_layer_norm_fwd(const NormArgs& a, int dtype, const void* x, const float* gamma,
                                  const float* beta, void* y, float* stats, hipStream_t s);
-// rows of partial sums that the weight gradients' reduction has, each [2][channels] floats
+// rows of partial sums that the backward writes for the weight gradients, each [2][channels] floats
 int layer_norm_parts(const NormArgs& a, int dtype);
 // part: layer_norm_parts rows (unused when both weight gradients are NULL)
 hipError_t launch_layer_norm_bwd(const NormArgs& a, int dtype, const void* x, const float* gamma,
