@@ -47,6 +47,7 @@ EXPORTS = [
     "fno_tucker_block_fwd", "fno_tucker_block_bwd", "fno_tucker_spectral_conv_fwd",
     "fno_tucker_spectral_conv_bwd", "fno_tucker_block_fwd_mse", "fno_tucker_block_bwd_preact",
     "fno_layer_norm_fwd", "fno_layer_norm_workspace_bytes", "fno_layer_norm_bwd",
+    "fno_tensor_list_bytes", "fno_tensor_list_create", "fno_tensor_list_destroy",
     "fno_grad_norm_workspace_bytes", "fno_grad_norm", "fno_clip_grad_norm", "fno_adamw",
     "fno_timing_enable", "fno_timing_select",
     "fno_timing_reset", "fno_timing_count", "fno_timing_get", "fno_status_string",
@@ -136,10 +137,13 @@ def _load():
                                                    POINTER(c_size_t)]),
         "fno_layer_norm_bwd": (c_int, [POINTER(fno_layer_norm_desc), P, P, P, P, P, P, P, P,
                                        c_size_t, P]),
-        "fno_grad_norm_workspace_bytes": (c_int, [c_int64, POINTER(c_size_t)]),
-        "fno_grad_norm": (c_int, [c_int64, P, c_float, c_float, P, P, c_size_t, P]),
-        "fno_clip_grad_norm": (c_int, [c_int64, P, P, c_float, c_float, P, P, c_size_t, P]),
-        "fno_adamw": (c_int, [c_int64, P, P, P, P, POINTER(fno_adamw_desc), P, P]),
+        "fno_tensor_list_bytes": (c_int, [c_int64, P, POINTER(c_size_t)]),
+        "fno_tensor_list_create": (c_int, [c_int64, P, P, c_size_t, P, POINTER(c_void_p)]),
+        "fno_tensor_list_destroy": (c_int, [P]),
+        "fno_grad_norm_workspace_bytes": (c_int, [P, POINTER(c_size_t)]),
+        "fno_grad_norm": (c_int, [P, c_float, c_float, P, P, c_size_t, P]),
+        "fno_clip_grad_norm": (c_int, [P, P, c_float, c_float, P, P, c_size_t, P]),
+        "fno_adamw": (c_int, [P, P, P, P, POINTER(fno_adamw_desc), P, P]),
         "fno_timing_enable": (c_int, [c_int]),
         "fno_timing_select": (c_int, [c_char_p]),
         "fno_timing_reset": (c_int, []),
@@ -157,6 +161,8 @@ def _load():
 
 
 _lib = _load()
+
+import torch as _torch  # noqa: E402  (after libfno: _load has imported it)
 
 
 def status_string(status: int) -> str:
@@ -297,24 +303,41 @@ def fno_layer_norm_bwd(desc, x, gamma, stats, grad_y, grad_x, grad_gamma, grad_b
                                    grad_beta, ws, ws_bytes, stream), "fno_layer_norm_bwd")
 
 
-def fno_grad_norm_workspace_bytes(count: int) -> int:
+def fno_tensor_list_bytes(count, tensors) -> int:
     b = c_size_t()
-    _check(_lib.fno_grad_norm_workspace_bytes(count, byref(b)), "fno_grad_norm_workspace_bytes")
+    _check(_lib.fno_tensor_list_bytes(count, tensors, byref(b)), "fno_tensor_list_bytes")
     return b.value
 
 
-def fno_grad_norm(count, grads, max_norm, grad_scale, record, ws, ws_bytes, stream):
-    _check(_lib.fno_grad_norm(count, grads, max_norm, grad_scale, record, ws, ws_bytes, stream),
+def fno_tensor_list_create(count, tensors, table, table_bytes, stream) -> int:
+    out = c_void_p()
+    _check(_lib.fno_tensor_list_create(count, tensors, table, table_bytes, stream, byref(out)),
+           "fno_tensor_list_create")
+    return out.value
+
+
+def fno_tensor_list_destroy(handle) -> None:
+    _check(_lib.fno_tensor_list_destroy(handle), "fno_tensor_list_destroy")
+
+
+def fno_grad_norm_workspace_bytes(grads) -> int:
+    b = c_size_t()
+    _check(_lib.fno_grad_norm_workspace_bytes(grads, byref(b)), "fno_grad_norm_workspace_bytes")
+    return b.value
+
+
+def fno_grad_norm(grads, max_norm, grad_scale, record, ws, ws_bytes, stream):
+    _check(_lib.fno_grad_norm(grads, max_norm, grad_scale, record, ws, ws_bytes, stream),
            "fno_grad_norm")
 
 
-def fno_clip_grad_norm(count, grads, out, max_norm, grad_scale, record, ws, ws_bytes, stream):
-    _check(_lib.fno_clip_grad_norm(count, grads, out, max_norm, grad_scale, record, ws, ws_bytes,
+def fno_clip_grad_norm(grads, out, max_norm, grad_scale, record, ws, ws_bytes, stream):
+    _check(_lib.fno_clip_grad_norm(grads, out, max_norm, grad_scale, record, ws, ws_bytes,
                                    stream), "fno_clip_grad_norm")
 
 
-def fno_adamw(count, params, grads, exp_avg, exp_avg_sq, desc, record, stream):
-    _check(_lib.fno_adamw(count, params, grads, exp_avg, exp_avg_sq, byref(desc), record, stream),
+def fno_adamw(params, grads, exp_avg, exp_avg_sq, desc, record, stream):
+    _check(_lib.fno_adamw(params, grads, exp_avg, exp_avg_sq, byref(desc), record, stream),
            "fno_adamw")
 
 
@@ -773,42 +796,40 @@ def mse_grad(y, t, grad=None, loss=None, ws=None, grad_scale=1.0):
 
 
 # ---- training operators -----------------------------------------------------------------------
-def _data_dtype(t):
-    """fno_dtype of a tensor's elements (complex64 counts as pairs of float32)."""
-    import torch
-    kinds = {torch.float32: FNO_DTYPE_F32, torch.complex64: FNO_DTYPE_F32,
-             torch.bfloat16: FNO_DTYPE_BF16, torch.float16: FNO_DTYPE_F16}
-    if t.dtype not in kinds:
+# These are small next to a launch, so their argument checks are kept cheap: one dictionary, one
+# attribute or one comparison each.
+_KINDS = {_torch.float32: FNO_DTYPE_F32, _torch.bfloat16: FNO_DTYPE_BF16,
+          _torch.float16: FNO_DTYPE_F16}
+_LIST_KINDS = {**_KINDS, _torch.complex64: FNO_DTYPE_F32}  # as pairs of float32
+
+
+def _kind(t, kinds):
+    k = kinds.get(t.dtype)
+    if k is None:
         raise ValueError(f"float32, bfloat16 or float16 data expected, not {t.dtype}")
-    return kinds[t.dtype]
+    return k
 
 
-class _Call:
-    """The current stream of a device, with the device current while the call is made."""
-
-    def __init__(self, device):
-        import torch
-        if device.type != "cuda":
-            raise ValueError(f"tensors on the GPU expected, not on {device}")
-        self._guard = None
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(device)
-        self.stream = torch.cuda.current_stream(device).cuda_stream
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+# The handle of a device's current stream, without the Stream object that the public call makes
+# (0.1 us against 1.9, next to 3.3 for a launch); the public call where torch has no such function.
+_stream_handle = getattr(_torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: _torch.cuda.current_stream(index).cuda_stream)
 
 
-def _batch_stride(t, name):
-    """Elements between the batch entries of a field whose entries are packed."""
+def _on_stream(device, fn, *args):
+    """fn(*args, current stream of `device`), with the device current."""
+    current = _torch.cuda.current_device()
+    index = current if device.index is None else device.index
+    if index == current:
+        return fn(*args, _stream_handle(index))
+    with _torch.cuda.device(index):
+        return fn(*args, _stream_handle(index))
+
+
+def _batch_stride(t, packed, name):
+    """Elements between the batch entries of a field whose entries, `packed` elements, are packed."""
     if t.is_contiguous():
-        return t[0].numel() if t.shape[0] else 0
+        return packed
     if t.shape[0] and not t[0].is_contiguous():
         raise ValueError(f"{name}: its batch entries must be packed (call .contiguous())")
     return t.stride(0)
@@ -821,29 +842,29 @@ def _like_x(t, x, name):
     return t
 
 
-def _float_vector(t, shape, x, name):
-    import torch
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != torch.float32
-                          or t.device != x.device or not t.is_contiguous()):
-        raise ValueError(f"{name}: needs packed float32 {tuple(shape)} on {x.device}")
-    return t
+def _vector(t, shape, device, name):
+    """The address of packed float32 values of a shape (None: none given)."""
+    if t is None:
+        return None
+    if t.dtype != _torch.float32 or t.shape != shape or t.device != device \
+            or not t.is_contiguous():
+        raise ValueError(f"{name}: needs packed float32 {tuple(shape)} on {device}")
+    return t.data_ptr()
 
 
 def _norm_desc(x, eps):
-    if x.dim() < 2:
+    shape = x.shape
+    if len(shape) < 2:
         raise ValueError("layer norm: x is [batch, channels, *grid]")
-    d = fno_layer_norm_desc()
-    d.dtype = _data_dtype(x)
-    if x.is_complex():
-        raise ValueError("layer norm: x must be real")
-    d.batch, d.channels = x.shape[0], x.shape[1]
     npts = 1
-    for n in x.shape[2:]:
+    for n in shape[2:]:
         npts *= n
-    d.npts = npts
-    d.x_stride = _batch_stride(x, "x")
-    d.eps = eps
-    return d
+    packed = shape[1] * npts
+    d = fno_layer_norm_desc(_kind(x, _KINDS), 0, shape[0], shape[1], npts,
+                            _batch_stride(x, packed, "x"), packed, packed, eps)
+    if not x.is_cuda:
+        raise ValueError(f"tensors on the GPU expected, not on {x.device}")
+    return d, packed
 
 
 def layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, out=None, stats=None, want_stats=True):
@@ -851,105 +872,114 @@ def layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, out=None, stats=None, wan
     row), times gamma plus beta (float32 [C]; None: 1 and 0).  Returns (y, stats); stats, float32
     [2, B, *grid], holds the means and the reciprocal deviations for layer_norm_bwd (None without
     want_stats)."""
-    import torch
-    d = _norm_desc(x, eps)
-    y = _like_x(out, x, "out") if out is not None else torch.empty(x.shape, dtype=x.dtype,
-                                                                   device=x.device)
-    d.y_stride = _batch_stride(y, "out")
-    _float_vector(gamma, x.shape[1:2], x, "gamma")
-    _float_vector(beta, x.shape[1:2], x, "beta")
-    shape = (2, x.shape[0]) + tuple(x.shape[2:])
-    if stats is not None:
-        _float_vector(stats, shape, x, "stats")
-    elif want_stats:
-        stats = torch.empty(shape, dtype=torch.float32, device=x.device)
-    with _Call(x.device) as stream:
-        fno_layer_norm_fwd(d, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), _ptr(stats),
-                           stream)
-    return y, stats
+    d, packed = _norm_desc(x, eps)
+    device, shape = x.device, x.shape
+    if out is None:
+        out = x.new_empty(shape)
+    else:
+        d.y_stride = _batch_stride(_like_x(out, x, "out"), packed, "out")
+    of_stats = (2, shape[0]) + shape[2:]
+    if stats is None and want_stats:
+        stats = x.new_empty(of_stats, dtype=_torch.float32)
+    _on_stream(device, fno_layer_norm_fwd, d, x.data_ptr(),
+               _vector(gamma, shape[1:2], device, "gamma"),
+               _vector(beta, shape[1:2], device, "beta"), out.data_ptr(),
+               _vector(stats, of_stats, device, "stats"))
+    return out, stats
 
 
 def layer_norm_bwd(x, gamma, stats, grad_y, want=("x", "gamma", "beta"), out=None, ws=None):
     """Gradients of layer_norm_fwd from its x and stats: dict(x, gamma, beta), None where not
     asked.  out: tensors to write instead of new ones (out["x"] may be grad_y itself).  ws: uint8
     workspace of fno_layer_norm_workspace_bytes (allocated when None)."""
-    import torch
-    d = _norm_desc(x, 0.0)
-    d.y_stride = _batch_stride(_like_x(grad_y, x, "grad_y"), "grad_y")
-    _float_vector(gamma, x.shape[1:2], x, "gamma")
-    _float_vector(stats, (2, x.shape[0]) + tuple(x.shape[2:]), x, "stats")
-    o = out or {}
-    c = x.shape[1]
-    gx = o["x"] if "x" in o else (torch.empty(x.shape, dtype=x.dtype, device=x.device)
-                                  if "x" in want else None)
-    gg, gb = (o[k] if k in o else (torch.empty(c, dtype=torch.float32, device=x.device)
-                                   if k in want else None) for k in ("gamma", "beta"))
+    d, packed = _norm_desc(x, 0.0)
+    device, shape = x.device, x.shape
+    d.y_stride = _batch_stride(_like_x(grad_y, x, "grad_y"), packed, "grad_y")
+    channels = shape[1:2]
+    got = {}
+    for k in ("x", "gamma", "beta"):
+        if out is not None and k in out:
+            got[k] = out[k]
+        elif k not in want:
+            got[k] = None
+        else:
+            got[k] = x.new_empty(shape) if k == "x" else x.new_empty(channels,
+                                                                    dtype=_torch.float32)
+    gx = got["x"]
     if gx is not None:
-        d.grad_x_stride = _batch_stride(_like_x(gx, x, "grad_x"), "grad_x")
-    _float_vector(gg, (c,), x, "grad_gamma")
-    _float_vector(gb, (c,), x, "grad_beta")
-    if ws is None and (gg is not None or gb is not None):
-        ws = torch.empty(max(fno_layer_norm_workspace_bytes(d), 16), dtype=torch.uint8,
-                         device=x.device)
-    with _Call(x.device) as stream:
-        fno_layer_norm_bwd(d, x.data_ptr(), _ptr(gamma), stats.data_ptr(), grad_y.data_ptr(),
-                           _ptr(gx), _ptr(gg), _ptr(gb), _ptr(ws),
-                           0 if ws is None else ws.numel() * ws.element_size(), stream)
-    return {"x": gx, "gamma": gg, "beta": gb}
+        d.grad_x_stride = _batch_stride(_like_x(gx, x, "grad_x"), packed, "grad_x")
+    gamma, gg, gb = (_vector(t, channels, device, name) for t, name in
+                     ((gamma, "gamma"), (got["gamma"], "grad_gamma"), (got["beta"], "grad_beta")))
+    stats = _vector(stats, (2, shape[0]) + shape[2:], device, "stats")
+    if ws is None and not (gg is None and gb is None):
+        ws = x.new_empty(max(fno_layer_norm_workspace_bytes(d), 16), dtype=_torch.uint8)
+    _on_stream(device, fno_layer_norm_bwd, d, x.data_ptr(), gamma, stats, grad_y.data_ptr(),
+               _ptr(gx), gg, gb, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+    return got
 
 
 class TensorList:
     """Tensors that one call goes over (gradients, parameters, moments): packed float32,
-    bfloat16, float16 or complex64 tensors on one GPU.  Holds the tensors and their addresses, so
-    it is made once for buffers that stay; functions that take one also take a plain sequence."""
+    bfloat16, float16 or complex64 tensors on one GPU.  Made once for buffers that stay: it holds
+    the tensors, and uploads the table of their addresses on the current stream.  Functions that
+    take a TensorList also take a plain sequence, and make a list for the one call."""
 
     def __init__(self, tensors):
+        self.handle = None
         self.tensors = list(tensors)
-        flat = []
-        self.device = None
+        self.device = self.tensors[0].device if self.tensors else \
+            _torch.device("cuda", _torch.cuda.current_device())
+        entries = (fno_tensor * max(len(self.tensors), 1))()
         for i, t in enumerate(self.tensors):
             if not t.is_contiguous() or t.is_conj() or t.is_neg():
                 raise ValueError(f"tensor {i} of the list is not packed (call .contiguous())")
-            if self.device is None:
-                self.device = t.device
-            elif t.device != self.device:
-                raise ValueError("the tensors of a list are on one device")
-            flat += (t.data_ptr(), t.numel() * (2 if t.is_complex() else 1), _data_dtype(t))
-        self.count = len(self.tensors)
-        self.array = (c_int64 * max(len(flat), 1))(*flat)  # fno_tensor[count], reserved = 0
-        self.ptr = ctypes.addressof(self.array)
+            if t.device != self.device or not t.is_cuda:
+                raise ValueError("the tensors of a list are on one GPU")
+            e = entries[i]
+            e.data, e.dtype = t.data_ptr(), _kind(t, _LIST_KINDS)
+            e.elems = 2 * t.numel() if t.is_complex() else t.numel()
+        count = len(self.tensors)
+        ptr = ctypes.addressof(entries)
+        self.table = _torch.empty(max(fno_tensor_list_bytes(count, ptr), 16), dtype=_torch.uint8,
+                                  device=self.device)
+
+        def create(stream):
+            return fno_tensor_list_create(count, ptr, self.table.data_ptr(), self.table.numel(),
+                                          stream)
+
+        self.handle = _on_stream(self.device, create)
+        self.norm_ws_bytes = fno_grad_norm_workspace_bytes(self.handle)
 
     def __len__(self):
-        return self.count
+        return len(self.tensors)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            fno_tensor_list_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 def _tensor_list(ts):
-    ts = ts if isinstance(ts, TensorList) else TensorList(ts)
-    if ts.device is None:
-        import torch
-        ts.device = torch.device("cuda", torch.cuda.current_device())
-    return ts
+    return ts if isinstance(ts, TensorList) else TensorList(ts)
 
 
-def _same_device(device, *others):
-    for t in others:
-        if t is not None and t.device != device:
-            raise ValueError(f"everything must be on {device}")
-
-
-def _record(record, device):
-    import torch
+def _norm_buffers(gl, record, ws):
     if record is None:
-        return torch.empty(2, dtype=torch.float32, device=device)
-    if record.numel() != 2 or record.dtype != torch.float32 or not record.is_contiguous():
-        raise ValueError("record: two packed float32")
-    return record
-
-
-def _norm_workspace(gl):
-    import torch
-    return torch.empty(fno_grad_norm_workspace_bytes(gl.count), dtype=torch.uint8,
-                       device=gl.device)
+        record = gl.table.new_empty(2, dtype=_torch.float32)
+    elif record.device != gl.device or record.numel() != 2 or record.dtype != _torch.float32 \
+            or not record.is_contiguous():
+        raise ValueError(f"record: needs two packed float32 on {gl.device}")
+    if ws is None:
+        ws = gl.table.new_empty(gl.norm_ws_bytes)
+    elif ws.device != gl.device or not ws.is_contiguous():
+        raise ValueError(f"ws: needs packed memory on {gl.device}")
+    return record, ws
 
 
 def grad_norm(grads, max_norm=float("inf"), grad_scale=1.0, record=None, ws=None):
@@ -957,12 +987,9 @@ def grad_norm(grads, max_norm=float("inf"), grad_scale=1.0, record=None, ws=None
     clipping to max_norm multiplies them by: a device tensor record = [norm, factor] (see
     fno_grad_norm)."""
     gl = _tensor_list(grads)
-    record = _record(record, gl.device)
-    ws = ws if ws is not None else _norm_workspace(gl)
-    _same_device(gl.device, record, ws)
-    with _Call(gl.device) as stream:
-        fno_grad_norm(gl.count, gl.ptr, max_norm, grad_scale, record.data_ptr(), ws.data_ptr(),
-                      ws.numel() * ws.element_size(), stream)
+    record, ws = _norm_buffers(gl, record, ws)
+    _on_stream(gl.device, fno_grad_norm, gl.handle, max_norm, grad_scale, record.data_ptr(),
+               ws.data_ptr(), ws.numel() * ws.element_size())
     return record
 
 
@@ -971,14 +998,9 @@ def clip_grad_norm(grads, max_norm, grad_scale=1.0, out=None, record=None, ws=No
     the gradient's dtype or float32).  Returns the record [norm, factor]."""
     gl = _tensor_list(grads)
     ol = gl if out is None else _tensor_list(out)
-    if ol.count != gl.count:
-        raise ValueError("out lists another number of tensors")
-    record = _record(record, gl.device)
-    ws = ws if ws is not None else _norm_workspace(gl)
-    _same_device(gl.device, record, ws, ol)
-    with _Call(gl.device) as stream:
-        fno_clip_grad_norm(gl.count, gl.ptr, ol.ptr, max_norm, grad_scale, record.data_ptr(),
-                           ws.data_ptr(), ws.numel() * ws.element_size(), stream)
+    record, ws = _norm_buffers(gl, record, ws)
+    _on_stream(gl.device, fno_clip_grad_norm, gl.handle, ol.handle, max_norm, grad_scale,
+               record.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return record
 
 
@@ -988,11 +1010,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps=
     place, from gradients times the factor of `record` (grad_norm's; None: as they are).  A factor
     that is not finite leaves parameters and moments as they are."""
     pl, gl, ml, vl = (_tensor_list(t) for t in (params, grads, exp_avg, exp_avg_sq))
-    if not pl.count == gl.count == ml.count == vl.count:
-        raise ValueError("the four lists need the same number of tensors")
     d = fno_adamw_desc(lr, betas[0], betas[1], eps, weight_decay, step)
-    if record is not None:
-        _record(record, pl.device)
-    _same_device(pl.device, gl, ml, vl, record)
-    with _Call(pl.device) as stream:
-        fno_adamw(pl.count, pl.ptr, gl.ptr, ml.ptr, vl.ptr, d, _ptr(record), stream)
+    if record is not None and (record.device != pl.device or record.numel() != 2
+                               or record.dtype != _torch.float32 or not record.is_contiguous()):
+        raise ValueError(f"record: needs two packed float32 on {pl.device}")
+    _on_stream(pl.device, fno_adamw, pl.handle, gl.handle, ml.handle, vl.handle, d, _ptr(record))

@@ -7,18 +7,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// the tensor that holds chunk `c` of the list: the last k with first[k] <= c
-template <int Lists, int Cap>
-__device__ __forceinline__ int tensor_of(const TensorTable<Lists, Cap>& t, uint32_t c) {
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.first[mid] <= c) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-
 // fixed-order sum of one double per thread; every thread gets it
 __device__ __forceinline__ double group_sum(double v, double* s_red) {
   const int tid = threadIdx.x;
@@ -32,28 +20,83 @@ __device__ __forceinline__ double group_sum(double v, double* s_red) {
   return s_red[0];
 }
 
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return __builtin_amdgcn_readfirstlane(v);
+}
 template <typename T>
-__device__ __forceinline__ double sum_squares(const T* p, int n) {
-  double a = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const double g = (double)to_float(p[i]);
-    a += g * g;
-  }
-  return a;
+__device__ __forceinline__ Global<T> data_of(const TensorTable& t, uint32_t k, int64_t at) {
+  const uint64_t v = reinterpret_cast<uint64_t>(t.entry[k].data);
+  const uint64_t u = (uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v);
+  return (Global<T>)u + at;
 }
 
-__global__ __launch_bounds__(kThreads) void k_norm_part(NormTable t, double* part) {
+// Calls f(entry number, first element, elements) for the spans of this work-group's share of the
+// chunks: neighbours, so that a work-group meets few tensors.  A span has at most 2^28 elements,
+// so that offsets inside it fit 32 bits; where it lies in its tensor is 64 bits.
+template <typename F>
+__device__ __forceinline__ void each_span(const TensorTable& t, F&& f) {
+  const uint64_t total = t.chunks;
+  uint32_t c = (uint32_t)(total * blockIdx.x / gridDim.x);
+  const uint32_t end = (uint32_t)(total * (blockIdx.x + 1) / gridDim.x);
+  while (c < end) {
+    const uint32_t k = uniform(t.of_chunk[c]), first = uniform(t.entry[k].first);
+    const int64_t elems = (int64_t)((uint64_t)uniform((uint32_t)(t.entry[k].elems >> 32)) << 32 |
+                                    uniform((uint32_t)t.entry[k].elems));
+    const int64_t at = (int64_t)(c - first) * kChunk;
+    const uint32_t most = end - c < (1u << 28) / kChunk ? end - c : (1u << 28) / kChunk;
+    const int64_t n = elems - at < most * kChunk ? elems - at : most * kChunk;
+    f(k, at, (int)n);
+    c += (uint32_t)((n + kChunk - 1) / kChunk);
+  }
+}
+
+constexpr int kAhead = 4;  // vectors that a thread has in flight of each operand
+
+template <typename T>
+__device__ __forceinline__ double sum_squares(Global<const T> p, int n) {
+  constexpr int V = 16 / (int)sizeof(T);
+  double a[kAhead] = {};
+  const int nv = n / V;
+  int i = threadIdx.x;
+  for (; i + (kAhead - 1) * kThreads < nv; i += kAhead * kThreads) {
+    Pack<T, V> q[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      q[u] = load_global<T, V>(p + (i + u * kThreads) * V);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const double g = (double)to_float(q[u].v[e]);
+        a[u] += g * g;
+      }
+  }
+  for (; i < nv; i += kThreads) {
+    const Pack<T, V> q = load_global<T, V>(p + i * V);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const double g = (double)to_float(q.v[e]);
+      a[0] += g * g;
+    }
+  }
+  const int rest = nv * V + threadIdx.x;
+  if (rest < n) {
+    const double g = (double)to_float<T>(p[rest]);
+    a[1] += g * g;
+  }
+  return (a[0] + a[1]) + (a[2] + a[3]);
+}
+
+__global__ __launch_bounds__(kThreads) void k_norm_part(TensorTable t, double* part) {
   __shared__ double s_red[kThreads];
   double a = 0.0;
-  for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    const int k = tensor_of(t, c);
-    const int64_t at = (int64_t)(c - t.first[k]) * kChunk, left = t.elems[k] - at;
-    const int n = (int)(left < kChunk ? left : kChunk);
-    const int d = t.dtype[k] & 15;
-    if (d == FNO_DTYPE_F32) a += sum_squares(static_cast<const float*>(t.ptr[0][k]) + at, n);
-    else if (d == FNO_DTYPE_BF16) a += sum_squares(static_cast<const __bf16*>(t.ptr[0][k]) + at, n);
-    else a += sum_squares(static_cast<const _Float16*>(t.ptr[0][k]) + at, n);
-  }
+  each_span(t, [&](uint32_t k, int64_t at, int n) {
+    const uint32_t d = uniform(t.entry[k].dtype);
+    if (d == FNO_DTYPE_F32) a += sum_squares<float>(data_of<const float>(t, k, at), n);
+    else if (d == FNO_DTYPE_BF16) a += sum_squares<__bf16>(data_of<const __bf16>(t, k, at), n);
+    else a += sum_squares<_Float16>(data_of<const _Float16>(t, k, at), n);
+  });
   a = group_sum(a, s_red);
   if (threadIdx.x == 0) part[blockIdx.x] = a;
 }
@@ -75,69 +118,126 @@ __global__ __launch_bounds__(kThreads) void k_norm_finish(const double* part, in
 }
 
 template <typename T, typename U>
-__device__ __forceinline__ void scale_chunk(const T* p, U* o, int n, float f) {
-  for (int i = threadIdx.x; i < n; i += kThreads) o[i] = from_float<U>(to_float(p[i]) * f);
+__device__ __forceinline__ void scale_chunk(Global<const T> p, Global<U> o, int n, float f) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const int nv = n / V;
+  int i = threadIdx.x;
+  const auto put = [&](const Pack<T, V>& q, int j) {
+    float g[V];
+    unpack<T, V>(q, g);
+#pragma unroll
+    for (int e = 0; e < V; ++e) g[e] *= f;
+    store_global<U, V>(o + j * V, g);
+  };
+  for (; i + (kAhead - 1) * kThreads < nv; i += kAhead * kThreads) {
+    Pack<T, V> q[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      q[u] = load_global<T, V>(p + (i + u * kThreads) * V);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) put(q[u], i + u * kThreads);
+  }
+  for (; i < nv; i += kThreads) put(load_global<T, V>(p + i * V), i);
+  const int rest = nv * V + threadIdx.x;
+  if (rest < n) o[rest] = from_float<U>(to_float<T>(p[rest]) * f);
 }
 
-__global__ __launch_bounds__(kThreads) void k_clip(NormTable t, const float* record) {
+__global__ __launch_bounds__(kThreads) void k_clip(TensorTable t, TensorTable out,
+                                                   const float* record) {
   const float f = record[1];
-  for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    const int k = tensor_of(t, c);
-    const int64_t at = (int64_t)(c - t.first[k]) * kChunk, left = t.elems[k] - at;
-    const int n = (int)(left < kChunk ? left : kChunk);
-    const int d = t.dtype[k] & 15, o = t.dtype[k] >> 4;
-    if (f == 1.0f && t.ptr[0][k] == t.ptr[1][k]) continue;
+  each_span(t, [&](uint32_t k, int64_t at, int n) {
+    if (f == 1.0f && data_of<char>(t, k, 0) == data_of<char>(out, k, 0)) return;
+    const uint32_t d = uniform(t.entry[k].dtype);
+    const bool wide = uniform(out.entry[k].dtype) == FNO_DTYPE_F32;
     if (d == FNO_DTYPE_F32) {
-      scale_chunk(static_cast<const float*>(t.ptr[0][k]) + at,
-                  static_cast<float*>(t.ptr[1][k]) + at, n, f);
+      scale_chunk<float, float>(data_of<const float>(t, k, at), data_of<float>(out, k, at), n, f);
     } else if (d == FNO_DTYPE_BF16) {
-      const __bf16* p = static_cast<const __bf16*>(t.ptr[0][k]) + at;
-      if (o == FNO_DTYPE_F32) scale_chunk(p, static_cast<float*>(t.ptr[1][k]) + at, n, f);
-      else scale_chunk(p, static_cast<__bf16*>(t.ptr[1][k]) + at, n, f);
+      const Global<const __bf16> p = data_of<const __bf16>(t, k, at);
+      if (wide) scale_chunk<__bf16, float>(p, data_of<float>(out, k, at), n, f);
+      else scale_chunk<__bf16, __bf16>(p, data_of<__bf16>(out, k, at), n, f);
     } else {
-      const _Float16* p = static_cast<const _Float16*>(t.ptr[0][k]) + at;
-      if (o == FNO_DTYPE_F32) scale_chunk(p, static_cast<float*>(t.ptr[1][k]) + at, n, f);
-      else scale_chunk(p, static_cast<_Float16*>(t.ptr[1][k]) + at, n, f);
+      const Global<const _Float16> p = data_of<const _Float16>(t, k, at);
+      if (wide) scale_chunk<_Float16, float>(p, data_of<float>(out, k, at), n, f);
+      else scale_chunk<_Float16, _Float16>(p, data_of<_Float16>(out, k, at), n, f);
     }
-  }
+  });
+}
+
+__device__ __forceinline__ void adamw_one(float& p, float g, float& m, float& v,
+                                          const AdamArgs& a, float f) {
+  g *= f;
+  m = a.beta1 * m + a.one_minus_beta1 * g;
+  v = a.beta2 * v + a.one_minus_beta2 * g * g;
+  p = a.decay * p - a.step_size * m / (sqrtf(v) * a.inv_bias2 + a.eps);
 }
 
 template <typename T>
-__device__ __forceinline__ void adamw_chunk(float* p, const T* g, float* m, float* v, int n,
-                                            const AdamArgs& a, float f) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const float gi = to_float(g[i]) * f;
-    const float mi = a.beta1 * m[i] + a.one_minus_beta1 * gi;
-    const float vi = a.beta2 * v[i] + a.one_minus_beta2 * gi * gi;
-    m[i] = mi;
-    v[i] = vi;
-    p[i] = a.decay * p[i] - a.step_size * mi / (sqrtf(vi) * a.inv_bias2 + a.eps);
+__device__ __forceinline__ void adamw_chunk(Global<float> p, Global<const T> g, Global<float> m,
+                                            Global<float> v, int n, const AdamArgs& a, float f) {
+  constexpr int V = 4, kTwo = 2;
+  typedef Pack<float, V> Q;
+  const int nv = n / V;
+  int i = threadIdx.x;
+  const auto put = [&](Q& qp, const Pack<T, V>& qg, Q& qm, Q& qv, int j) {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      adamw_one(qp.v[e], to_float(qg.v[e]), qm.v[e], qv.v[e], a, f);
+    store_global<float, V>(p + j, qp.v);
+    store_global<float, V>(m + j, qm.v);
+    store_global<float, V>(v + j, qv.v);
+  };
+  for (; i + (kTwo - 1) * kThreads < nv; i += kTwo * kThreads) {
+    Q qp[kTwo], qm[kTwo], qv[kTwo];
+    Pack<T, V> qg[kTwo];
+#pragma unroll
+    for (int u = 0; u < kTwo; ++u) {
+      const int j = (i + u * kThreads) * V;
+      qg[u] = load_global<T, V>(g + j);
+      qp[u] = load_global<float, V>(p + j);
+      qm[u] = load_global<float, V>(m + j);
+      qv[u] = load_global<float, V>(v + j);
+    }
+#pragma unroll
+    for (int u = 0; u < kTwo; ++u) put(qp[u], qg[u], qm[u], qv[u], (i + u * kThreads) * V);
+  }
+  for (; i < nv; i += kThreads) {
+    const int j = i * V;
+    Q qp = load_global<float, V>(p + j), qm = load_global<float, V>(m + j),
+      qv = load_global<float, V>(v + j);
+    put(qp, load_global<T, V>(g + j), qm, qv, j);
+  }
+  const int r = nv * V + threadIdx.x;
+  if (r < n) {
+    float qp = p[r], qm = m[r], qv = v[r];
+    adamw_one(qp, to_float<T>(g[r]), qm, qv, a, f);
+    p[r] = qp;
+    m[r] = qm;
+    v[r] = qv;
   }
 }
 
-__global__ __launch_bounds__(kThreads) void k_adamw(AdamTable t, AdamArgs a, const float* record) {
+__global__ __launch_bounds__(kThreads) void k_adamw(TensorTable params, TensorTable grads,
+                                                    TensorTable exp_avg, TensorTable exp_avg_sq,
+                                                    AdamArgs a, const float* record) {
   const float f = record ? record[1] : 1.0f;
   if (!(fabsf(f) < INFINITY)) return;  // the gradients were not finite: no update
-  for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    const int k = tensor_of(t, c);
-    const int64_t at = (int64_t)(c - t.first[k]) * kChunk, left = t.elems[k] - at;
-    const int n = (int)(left < kChunk ? left : kChunk);
-    const int d = t.dtype[k] >> 4;
-    float* p = static_cast<float*>(t.ptr[0][k]) + at;
-    float* m = static_cast<float*>(t.ptr[2][k]) + at;
-    float* v = static_cast<float*>(t.ptr[3][k]) + at;
-    if (d == FNO_DTYPE_F32)
-      adamw_chunk(p, static_cast<const float*>(t.ptr[1][k]) + at, m, v, n, a, f);
-    else if (d == FNO_DTYPE_BF16)
-      adamw_chunk(p, static_cast<const __bf16*>(t.ptr[1][k]) + at, m, v, n, a, f);
-    else
-      adamw_chunk(p, static_cast<const _Float16*>(t.ptr[1][k]) + at, m, v, n, a, f);
-  }
+  each_span(params, [&](uint32_t k, int64_t at, int n) {
+    const uint32_t d = uniform(grads.entry[k].dtype);
+    const Global<float> p = data_of<float>(params, k, at);
+    const Global<float> m = data_of<float>(exp_avg, k, at);
+    const Global<float> v = data_of<float>(exp_avg_sq, k, at);
+    if (d == FNO_DTYPE_F32) adamw_chunk<float>(p, data_of<const float>(grads, k, at), m, v, n, a, f);
+    else if (d == FNO_DTYPE_BF16) adamw_chunk<__bf16>(p, data_of<const __bf16>(grads, k, at), m, v, n, a, f);
+    else adamw_chunk<_Float16>(p, data_of<const _Float16>(grads, k, at), m, v, n, a, f);
+  });
 }
+
+// work-groups of the kernels that write: as many as the compute units hold at a time
+int write_groups(const TensorTable& t) { return (int)(t.chunks < 2048u ? t.chunks : 2048u); }
 
 }  // namespace
 
-hipError_t launch_norm_part(const NormTable& t, int groups, double* part, hipStream_t s) {
+hipError_t launch_norm_part(const TensorTable& t, int groups, double* part, hipStream_t s) {
   hipLaunchKernelGGL(k_norm_part, dim3(groups), dim3(kThreads), 0, s, t, part);
   return hipGetLastError();
 }
@@ -149,14 +249,17 @@ hipError_t launch_norm_finish(const double* part, int nparts, float max_norm, fl
   return hipGetLastError();
 }
 
-hipError_t launch_clip(const NormTable& t, int groups, const float* record, hipStream_t s) {
-  hipLaunchKernelGGL(k_clip, dim3(groups), dim3(kThreads), 0, s, t, record);
+hipError_t launch_clip(const TensorTable& t, const TensorTable& out, const float* record,
+                       hipStream_t s) {
+  hipLaunchKernelGGL(k_clip, dim3(write_groups(t)), dim3(kThreads), 0, s, t, out, record);
   return hipGetLastError();
 }
 
-hipError_t launch_adamw(const AdamTable& t, int groups, const AdamArgs& a, const float* record,
-                        hipStream_t s) {
-  hipLaunchKernelGGL(k_adamw, dim3(groups), dim3(kThreads), 0, s, t, a, record);
+hipError_t launch_adamw(const TensorTable& params, const TensorTable& grads,
+                        const TensorTable& exp_avg, const TensorTable& exp_avg_sq,
+                        const AdamArgs& a, const float* record, hipStream_t s) {
+  hipLaunchKernelGGL(k_adamw, dim3(write_groups(params)), dim3(kThreads), 0, s, params, grads,
+                     exp_avg, exp_avg_sq, a, record);
   return hipGetLastError();
 }
 

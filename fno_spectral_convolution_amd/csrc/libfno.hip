@@ -1816,80 +1816,90 @@ size_t norm_workspace(const fno::NormArgs& a, int32_t dtype) {
   return align_up(sizeof(float) * 2 * (size_t)a.channels * (size_t)fno::layer_norm_parts(a, dtype));
 }
 
-// elements of one tensor: a table's chunk numbers then stay below 2^31
 constexpr int64_t kMaxElems = (int64_t)1 << 36;
 
-fno_status check_list(int64_t count, const fno_tensor* t, const char* name) {
-  if (count < 0) return fail(FNO_ERR_INVALID_ARGUMENT, "count < 0");
-  if (count > 0 && !t) return fail(FNO_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+// A list's tensors checked; the chunks that they make.
+fno_status check_tensors(int64_t count, const fno_tensor* t, uint64_t* chunks) {
+  if (count < 0 || count > 0x7fffffff) return fail(FNO_ERR_INVALID_ARGUMENT, "bad tensor count");
+  if (count > 0 && !t) return fail(FNO_ERR_INVALID_ARGUMENT, "tensors is NULL");
+  uint64_t n = 0;
   for (int64_t i = 0; i < count; ++i) {
     const fno_tensor& e = t[i];
     if (!known_dtype(e.dtype) || e.reserved != 0 || e.elems < 0 || e.elems > kMaxElems)
-      return fail(FNO_ERR_INVALID_ARGUMENT, "%s[%lld]: bad dtype, reserved or elems", name,
+      return fail(FNO_ERR_INVALID_ARGUMENT, "tensor %lld: bad dtype, reserved or elems",
                   (long long)i);
     if (e.elems > 0 && (!e.data || !aligned_to(e.data, dtype_bytes(e.dtype))))
-      return fail(FNO_ERR_INVALID_ARGUMENT, "%s[%lld]: NULL or not aligned to its elements", name,
+      return fail(FNO_ERR_INVALID_ARGUMENT, "tensor %lld: NULL or not aligned to its elements",
                   (long long)i);
+    n += (uint64_t)((e.elems + fno::kChunk - 1) / fno::kChunk);
   }
+  if (n >= (uint64_t)1 << 31) return fail(FNO_ERR_UNSUPPORTED, "more than 2^42 elements in a list");
+  *chunks = n;
   return FNO_OK;
 }
 
-// Calls flush(table, groups) with tables of up to Cap of the lists' tensors that have elements,
-// each with at most `most` work-groups.
-template <typename Table, int Lists, int Cap, typename Flush>
-fno_status walk_lists(int64_t count, const fno_tensor* const (&lists)[Lists], int most,
-                             Flush&& flush) {
-  Table t;
-  t.count = 0;
-  t.first[0] = 0;
-  for (int64_t i = 0; i < count; ++i) {
-    const int64_t n = lists[0][i].elems;
-    if (n > 0) {
-      const int k = t.count++;
-      for (int l = 0; l < Lists; ++l) t.ptr[l][k] = lists[l][i].data;
-      t.elems[k] = n;
-      t.dtype[k] = (uint8_t)(lists[0][i].dtype | (lists[1][i].dtype << 4));
-      t.first[k + 1] = t.first[k] + (uint32_t)((n + fno::kChunk - 1) / fno::kChunk);
-    }
-    if (t.count > 0 && (t.count == Cap || i == count - 1)) {
-      const uint32_t chunks = t.first[t.count];
-      const fno_status st = flush(t, (int)(chunks < (uint32_t)most ? chunks : (uint32_t)most));
-      if (st != FNO_OK) return st;
-      t.count = 0;
-    }
-  }
+size_t table_bytes_of(int64_t count, uint64_t chunks) {
+  return align_up(sizeof(fno::TensorEntry) * (size_t)count + sizeof(uint32_t) * (size_t)chunks);
+}
+
+}  // namespace
+
+struct fno_tensor_list {
+  std::vector<fno_tensor> tensors;
+  std::vector<unsigned char> host;  // the table's bytes
+  fno::TensorTable table;
+  int device;
+};
+
+namespace {
+
+// A list given to a call: there, and made for the current device.
+fno_status check_list(const fno_tensor_list* l, const char* name) {
+  if (!l) return fail(FNO_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+  int dev = -1;
+  FNO_HIP(hipGetDevice(&dev), "hipGetDevice");
+  if (dev != l->device)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "%s: made for device %d, the current one is %d", name,
+                l->device, dev);
   return FNO_OK;
 }
 
-size_t norm_parts_bytes(int64_t count) {
-  const int64_t tables = count / fno::kNormTensors + 1;
-  return sizeof(double) * (size_t)tables * fno::kNormParts;
-}
-
-fno_status grad_norm_impl(int64_t count, const fno_tensor* grads, float max_norm,
-                                 float grad_scale, float* record, void* ws, size_t ws_bytes,
-                                 hipStream_t s) {
-  fno_status st = check_list(count, grads, "grads");
+// `l` has as many tensors as `like`, of the same elements.
+fno_status check_like(const fno_tensor_list* l, const fno_tensor_list* like, const char* name) {
+  fno_status st = check_list(l, name);
   if (st != FNO_OK) return st;
+  if (l->tensors.size() != like->tensors.size())
+    return fail(FNO_ERR_INVALID_ARGUMENT, "%s: another number of tensors", name);
+  for (size_t i = 0; i < l->tensors.size(); ++i)
+    if (l->tensors[i].elems != like->tensors[i].elems)
+      return fail(FNO_ERR_INVALID_ARGUMENT, "%s: tensor %lld has another number of elements", name,
+                  (long long)i);
+  return FNO_OK;
+}
+
+int norm_groups(const fno_tensor_list* l) {
+  return (int)std::min<uint32_t>(l->table.chunks, fno::kNormParts);
+}
+
+size_t norm_parts_bytes(const fno_tensor_list* l) {
+  return align_up(sizeof(double) * (size_t)std::max(norm_groups(l), 1));
+}
+
+fno_status grad_norm_impl(const fno_tensor_list* grads, float max_norm, float grad_scale,
+                          float* record, void* ws, size_t ws_bytes, hipStream_t s) {
   if (!(max_norm > 0.0f)) return fail(FNO_ERR_INVALID_ARGUMENT, "max_norm must be > 0");
   if (!(grad_scale > 0.0f) || !std::isfinite(grad_scale))
     return fail(FNO_ERR_INVALID_ARGUMENT, "grad_scale must be finite and > 0");
   REQ_AT(record, "record", sizeof(float));
   REQ(ws, "workspace");
-  if (ws_bytes < norm_parts_bytes(count))
+  if (ws_bytes < norm_parts_bytes(grads))
     return fail(FNO_ERR_INVALID_ARGUMENT, "workspace too small");
   double* part = static_cast<double*>(ws);
-  int nparts = 0;
-  const fno_tensor* const lists[2] = {grads, grads};
-  st = walk_lists<fno::NormTable, 2, fno::kNormTensors>(
-      count, lists, fno::kNormParts, [&](const fno::NormTable& t, int groups) -> fno_status {
-        LAUNCH("grad_norm", s, fno::launch_norm_part(t, groups, part + nparts, s));
-        nparts += groups;
-        return FNO_OK;
-      });
-  if (st != FNO_OK) return st;
+  const int groups = norm_groups(grads);
+  if (groups > 0)
+    LAUNCH("grad_norm", s, fno::launch_norm_part(grads->table, groups, part, s));
   LAUNCH("grad_norm_finish", s,
-         fno::launch_norm_finish(part, nparts, max_norm, grad_scale, record, s));
+         fno::launch_norm_finish(part, groups, max_norm, grad_scale, record, s));
   return FNO_OK;
 }
 
@@ -1968,48 +1978,106 @@ fno_status fno_layer_norm_bwd(const fno_layer_norm_desc* desc, const void* x, co
   return FNO_OK;
 }
 
-fno_status fno_grad_norm_workspace_bytes(int64_t count, size_t* bytes) {
-  if (count < 0 || count > (int64_t)1 << 40 || !bytes)
-    return fail(FNO_ERR_INVALID_ARGUMENT, "bad gradient norm workspace query");
-  *bytes = norm_parts_bytes(count);
+fno_status fno_tensor_list_bytes(int64_t count, const fno_tensor* tensors, size_t* bytes) {
+  if (!bytes) return fail(FNO_ERR_INVALID_ARGUMENT, "bytes is NULL");
+  uint64_t chunks;
+  const fno_status st = check_tensors(count, tensors, &chunks);
+  if (st == FNO_OK) *bytes = table_bytes_of(count, chunks);
+  return st;
+}
+
+fno_status fno_tensor_list_create(int64_t count, const fno_tensor* tensors, void* table,
+                                  size_t table_bytes, void* stream, fno_tensor_list** out) {
+  if (!out) return fail(FNO_ERR_INVALID_ARGUMENT, "out is NULL");
+  *out = nullptr;
+  uint64_t chunks;
+  fno_status st = check_tensors(count, tensors, &chunks);
+  if (st != FNO_OK) return st;
+  const size_t bytes = table_bytes_of(count, chunks);
+  if (bytes > 0) REQ(table, "table");
+  if (table_bytes < bytes) return fail(FNO_ERR_INVALID_ARGUMENT, "table too small");
+  fno_tensor_list* l = nullptr;
+  try {
+    l = new fno_tensor_list();
+    l->tensors.assign(tensors, tensors + count);
+    l->host.resize(bytes);
+  } catch (const std::bad_alloc&) {
+    delete l;
+    return fail(FNO_ERR_OUT_OF_MEMORY, "host memory for a tensor list");
+  }
+  auto* entry = reinterpret_cast<fno::TensorEntry*>(l->host.data());
+  auto* of_chunk = reinterpret_cast<uint32_t*>(entry + count);
+  uint32_t first = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const int64_t n = tensors[i].elems;
+    entry[i] = {tensors[i].data, n, first, tensors[i].dtype};
+    for (const uint32_t last = first + (uint32_t)((n + fno::kChunk - 1) / fno::kChunk);
+         first < last; ++first)
+      of_chunk[first] = (uint32_t)i;
+  }
+  l->table.entry = static_cast<const fno::TensorEntry*>(table);
+  l->table.of_chunk = reinterpret_cast<const uint32_t*>(l->table.entry + count);
+  l->table.chunks = (uint32_t)chunks;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+  hipError_t e = hipGetDevice(&l->device);
+  if (e == hipSuccess) e = hipStreamIsCapturing(s, &cap);
+  if (e == hipSuccess && cap != hipStreamCaptureStatusNone) {
+    delete l;
+    return fail(FNO_ERR_INVALID_ARGUMENT, "a tensor list cannot be made during stream capture");
+  }
+  // pageable memory: the copy has left it when the call returns
+  if (e == hipSuccess && bytes > 0)
+    e = hipMemcpyAsync(table, l->host.data(), bytes, hipMemcpyHostToDevice, s);
+  if (e != hipSuccess) {
+    delete l;
+    return hip_fail(e, "fno_tensor_list_create");
+  }
+  *out = l;
   return FNO_OK;
 }
 
-fno_status fno_grad_norm(int64_t count, const fno_tensor* grads, float max_norm,
-                         float grad_scale, float* record, void* ws, size_t ws_bytes,
-                         void* stream) {
-  return grad_norm_impl(count, grads, max_norm, grad_scale, record, ws, ws_bytes,
+fno_status fno_tensor_list_destroy(fno_tensor_list* list) {
+  delete list;
+  return FNO_OK;
+}
+
+fno_status fno_grad_norm_workspace_bytes(const fno_tensor_list* grads, size_t* bytes) {
+  if (!grads || !bytes) return fail(FNO_ERR_INVALID_ARGUMENT, "bad gradient norm workspace query");
+  *bytes = norm_parts_bytes(grads);
+  return FNO_OK;
+}
+
+fno_status fno_grad_norm(const fno_tensor_list* grads, float max_norm, float grad_scale,
+                         float* record, void* ws, size_t ws_bytes, void* stream) {
+  const fno_status st = check_list(grads, "grads");
+  if (st != FNO_OK) return st;
+  return grad_norm_impl(grads, max_norm, grad_scale, record, ws, ws_bytes,
                         static_cast<hipStream_t>(stream));
 }
 
-fno_status fno_clip_grad_norm(int64_t count, const fno_tensor* grads, const fno_tensor* out,
+fno_status fno_clip_grad_norm(const fno_tensor_list* grads, const fno_tensor_list* out,
                               float max_norm, float grad_scale, float* record, void* ws,
                               size_t ws_bytes, void* stream) {
-  fno_status st = check_list(count, grads, "grads");
-  if (st == FNO_OK) st = check_list(count, out, "out");
+  fno_status st = check_list(grads, "grads");
+  if (st == FNO_OK) st = check_like(out, grads, "out");
   if (st != FNO_OK) return st;
-  for (int64_t i = 0; i < count; ++i) {
-    if (out[i].elems != grads[i].elems)
-      return fail(FNO_ERR_INVALID_ARGUMENT, "out[%lld]: another number of elements",
-                  (long long)i);
-    if (out[i].dtype != grads[i].dtype &&
-        (out[i].dtype != FNO_DTYPE_F32 || (out[i].elems > 0 && out[i].data == grads[i].data)))
+  for (size_t i = 0; i < grads->tensors.size(); ++i) {
+    const fno_tensor &g = grads->tensors[i], &o = out->tensors[i];
+    if (o.dtype != g.dtype && (o.dtype != FNO_DTYPE_F32 || (o.elems > 0 && o.data == g.data)))
       return fail(FNO_ERR_INVALID_ARGUMENT,
-                  "out[%lld]: not its gradient's dtype, nor float32 apart from it", (long long)i);
+                  "out: tensor %lld is not of its gradient's dtype, nor float32 apart from it",
+                  (long long)i);
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
-  st = grad_norm_impl(count, grads, max_norm, grad_scale, record, ws, ws_bytes, s);
-  if (st != FNO_OK) return st;
-  const fno_tensor* const lists[2] = {grads, out};
-  return walk_lists<fno::NormTable, 2, fno::kNormTensors>(
-      count, lists, 2048, [&](const fno::NormTable& t, int groups) -> fno_status {
-        LAUNCH("grad_clip", s, fno::launch_clip(t, groups, record, s));
-        return FNO_OK;
-      });
+  st = grad_norm_impl(grads, max_norm, grad_scale, record, ws, ws_bytes, s);
+  if (st != FNO_OK || grads->table.chunks == 0) return st;
+  LAUNCH("grad_clip", s, fno::launch_clip(grads->table, out->table, record, s));
+  return FNO_OK;
 }
 
-fno_status fno_adamw(int64_t count, const fno_tensor* params, const fno_tensor* grads,
-                     const fno_tensor* exp_avg, const fno_tensor* exp_avg_sq,
+fno_status fno_adamw(const fno_tensor_list* params, const fno_tensor_list* grads,
+                     const fno_tensor_list* exp_avg, const fno_tensor_list* exp_avg_sq,
                      const fno_adamw_desc* d, const float* record, void* stream) {
   if (!d) return fail(FNO_ERR_INVALID_ARGUMENT, "AdamW descriptor is NULL");
   if (!std::isfinite(d->lr) || !std::isfinite(d->weight_decay) || !(d->eps >= 0.0) ||
@@ -2017,21 +2085,17 @@ fno_status fno_adamw(int64_t count, const fno_tensor* params, const fno_tensor* 
       !(d->beta2 >= 0.0 && d->beta2 < 1.0) || d->step < 1)
     return fail(FNO_ERR_INVALID_ARGUMENT,
                 "AdamW: lr, weight_decay finite, eps >= 0, betas in [0, 1), step >= 1");
-  fno_status st = check_list(count, params, "params");
-  if (st == FNO_OK) st = check_list(count, grads, "grads");
-  if (st == FNO_OK) st = check_list(count, exp_avg, "exp_avg");
-  if (st == FNO_OK) st = check_list(count, exp_avg_sq, "exp_avg_sq");
-  if (st != FNO_OK) return st;
-  for (int64_t i = 0; i < count; ++i) {
-    const int64_t n = params[i].elems;
-    if (grads[i].elems != n || exp_avg[i].elems != n || exp_avg_sq[i].elems != n)
-      return fail(FNO_ERR_INVALID_ARGUMENT, "AdamW: tensor %lld has different elems in its lists",
-                  (long long)i);
-    if (params[i].dtype != FNO_DTYPE_F32 || exp_avg[i].dtype != FNO_DTYPE_F32 ||
-        exp_avg_sq[i].dtype != FNO_DTYPE_F32)
-      return fail(FNO_ERR_UNSUPPORTED, "AdamW: parameters and moments are float32");
-  }
   OPT_AT(record, "record", sizeof(float));
+  fno_status st = check_list(params, "params");
+  if (st == FNO_OK) st = check_like(grads, params, "grads");
+  if (st == FNO_OK) st = check_like(exp_avg, params, "exp_avg");
+  if (st == FNO_OK) st = check_like(exp_avg_sq, params, "exp_avg_sq");
+  if (st != FNO_OK) return st;
+  for (const fno_tensor_list* l : {params, exp_avg, exp_avg_sq})
+    for (const fno_tensor& t : l->tensors)
+      if (t.dtype != FNO_DTYPE_F32)
+        return fail(FNO_ERR_UNSUPPORTED, "AdamW: parameters and moments are float32");
+  if (params->table.chunks == 0) return FNO_OK;
   fno::AdamArgs a;
   a.beta1 = (float)d->beta1;
   a.beta2 = (float)d->beta2;
@@ -2042,12 +2106,10 @@ fno_status fno_adamw(int64_t count, const fno_tensor* params, const fno_tensor* 
   a.inv_bias2 = (float)(1.0 / std::sqrt(1.0 - std::pow(d->beta2, (double)d->step)));
   a.eps = (float)d->eps;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const fno_tensor* const lists[4] = {params, grads, exp_avg, exp_avg_sq};
-  return walk_lists<fno::AdamTable, 4, fno::kAdamTensors>(
-      count, lists, 2048, [&](const fno::AdamTable& t, int groups) -> fno_status {
-        LAUNCH("adamw", s, fno::launch_adamw(t, groups, a, record, s));
-        return FNO_OK;
-      });
+  LAUNCH("adamw", s,
+         fno::launch_adamw(params->table, grads->table, exp_avg->table, exp_avg_sq->table, a,
+                           record, s));
+  return FNO_OK;
 }
 
 }  // extern "C"

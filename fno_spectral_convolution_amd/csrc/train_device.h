@@ -38,6 +38,37 @@ __device__ __forceinline__ void store_pack(T* p, const float (&f)[N]) {
   *reinterpret_cast<Pack<T, N>*>(p) = q;
 }
 
+// The same through pointers that the compiler cannot tell to be global (they come out of memory):
+// as such they would be read with flat instructions, which also occupy the LDS.
+template <typename T>
+using Global = T __attribute__((address_space(1)))*;
+template <typename T, int N>
+struct RawVector {
+  typedef T type __attribute__((ext_vector_type(N)));
+  typedef type unaligned __attribute__((aligned(sizeof(T))));
+};
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load_global(Global<const T> p) {
+  typedef typename RawVector<T, N>::unaligned V;
+  const V v = *(Global<const V>)p;
+  Pack<T, N> q;
+#pragma unroll
+  for (int i = 0; i < N; ++i) q.v[i] = v[i];
+  return q;
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_global(Global<T> p, const float (&f)[N]) {
+  constexpr int M = N * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : N;
+  typedef typename RawVector<T, M>::unaligned V;
+#pragma unroll
+  for (int k = 0; k < N; k += M) {
+    V v;
+#pragma unroll
+    for (int i = 0; i < M; ++i) v[i] = from_float<T>(f[k + i]);
+    *(Global<V>)(p + k) = v;
+  }
+}
+
 template <typename T, int N>
 __device__ __forceinline__ void unpack(const Pack<T, N>& q, float (&f)[N]) {
 #pragma unroll

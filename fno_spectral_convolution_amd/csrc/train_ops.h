@@ -28,30 +28,29 @@ hipError_t launch_layer_norm_finish(const NormArgs& a, int nparts, const float* 
                                     float* ggamma, float* gbeta, hipStream_t s);
 
 // ---- tensor lists (kernels_optim.hip) --------------------------------------------------------
-// A list travels in kernel arguments (at most 4 KB a launch), `Cap` tensors at a time: no device
-// table to upload or to go stale.  Work is cut into chunks of kChunk elements that do not cross a
-// tensor's end; first[k] is the first chunk of tensor k.
-constexpr int64_t kChunk = 8192;
-template <int Lists, int Cap>
-struct TensorTable {
-  void* ptr[Lists][Cap];
-  int64_t elems[Cap];
-  uint32_t first[Cap + 1];
-  uint8_t dtype[Cap];  // of list 0 in the low four bits, of list 1 in the high ones
-  int32_t count;
+// A list's device table: its entries, then the entry that holds each chunk.  Chunks are kChunk
+// elements of one tensor (its last one fewer); they are the grain at which work is shared out.
+constexpr int64_t kChunk = 2048;
+struct TensorEntry {
+  void* data;
+  int64_t elems;
+  uint32_t first;  // its first chunk
+  int32_t dtype;
 };
-constexpr int kNormTensors = 100;   // tensors a launch: gradients and outputs
-constexpr int kAdamTensors = 80;    // parameters, gradients, two moments
-typedef TensorTable<2, kNormTensors> NormTable;
-typedef TensorTable<4, kAdamTensors> AdamTable;
-static_assert(sizeof(NormTable) <= 3800 && sizeof(AdamTable) <= 3800, "kernel argument space");
-constexpr int kNormParts = 1024;    // partial sums a launch
+struct TensorTable {
+  const TensorEntry* entry;
+  const uint32_t* of_chunk;
+  uint32_t chunks;
+};
+// partial sums of the norm: a work-group's registers allow four to a compute unit
+constexpr int kNormParts = 1024;
 
 // one partial sum of squares per work-group into part[0 .. groups)
-hipError_t launch_norm_part(const NormTable& t, int groups, double* part, hipStream_t s);
+hipError_t launch_norm_part(const TensorTable& t, int groups, double* part, hipStream_t s);
 hipError_t launch_norm_finish(const double* part, int nparts, float max_norm, float grad_scale,
                               float* record, hipStream_t s);
-hipError_t launch_clip(const NormTable& t, int groups, const float* record, hipStream_t s);
+hipError_t launch_clip(const TensorTable& t, const TensorTable& out, const float* record,
+                       hipStream_t s);
 
 struct AdamArgs {
   float beta1, beta2, one_minus_beta1, one_minus_beta2;
@@ -60,7 +59,8 @@ struct AdamArgs {
   float inv_bias2;   // 1 / sqrt(1 - beta2^t)
   float eps;
 };
-hipError_t launch_adamw(const AdamTable& t, int groups, const AdamArgs& a, const float* record,
-                        hipStream_t s);
+hipError_t launch_adamw(const TensorTable& params, const TensorTable& grads,
+                        const TensorTable& exp_avg, const TensorTable& exp_avg_sq,
+                        const AdamArgs& a, const float* record, hipStream_t s);
 
 }  // namespace fno

@@ -389,13 +389,25 @@ fno_status fno_layer_norm_bwd(const fno_layer_norm_desc* desc, const void* x, co
  * twice its elements. */
 typedef struct fno_tensor {
   void* data;        /* NULL only with elems 0 */
-  int64_t elems;     /* >= 0                   */
+  int64_t elems;     /* 0 .. 2^36              */
   int32_t dtype;     /* fno_dtype              */
   int32_t reserved;  /* must be 0              */
 } fno_tensor;
 
-/* Bytes of workspace of fno_grad_norm and fno_clip_grad_norm on a list of `count` tensors. */
-fno_status fno_grad_norm_workspace_bytes(int64_t count, size_t* bytes);
+/* A list of tensors that one call goes over (gradients, parameters, moments), made once for
+ * buffers that stay: a host object, and a device table of their addresses and of the chunks that
+ * the work is cut into, in memory of the caller's (16-byte aligned, fno_tensor_list_bytes).  The
+ * table is uploaded on `stream`, which must not be capturing; calls on other streams are ordered
+ * after that by the caller, who keeps table and tensors until the calls have run.  Making a list
+ * launches nothing; any number of calls may use one list at a time. */
+typedef struct fno_tensor_list fno_tensor_list;
+fno_status fno_tensor_list_bytes(int64_t count, const fno_tensor* tensors, size_t* bytes);
+fno_status fno_tensor_list_create(int64_t count, const fno_tensor* tensors, void* table,
+                                  size_t table_bytes, void* stream, fno_tensor_list** out);
+fno_status fno_tensor_list_destroy(fno_tensor_list* list); /* host only; NULL accepted */
+
+/* Bytes of workspace of fno_grad_norm and fno_clip_grad_norm on a list. */
+fno_status fno_grad_norm_workspace_bytes(const fno_tensor_list* grads, size_t* bytes);
 
 /* The global norm of a list of gradients that carry the loss scale grad_scale (1 without one):
  *   norm = sqrt(sum over all elements of g^2) / grad_scale,
@@ -403,16 +415,15 @@ fno_status fno_grad_norm_workspace_bytes(int64_t count, size_t* bytes);
  * written to the device floats record[0] = norm, record[1] = factor.  The sum is taken in float64
  * (no float32 gradient over- or underflows it) in a fixed order.  max_norm > 0, INFINITY for no
  * clipping; grad_scale finite and > 0.  A tensor that is listed twice counts twice. */
-fno_status fno_grad_norm(int64_t count, const fno_tensor* grads, float max_norm,
-                         float grad_scale, float* record, void* workspace,
-                         size_t workspace_bytes, void* stream);
+fno_status fno_grad_norm(const fno_tensor_list* grads, float max_norm, float grad_scale,
+                         float* record, void* workspace, size_t workspace_bytes, void* stream);
 
 /* fno_grad_norm, then out = factor * g for every tensor.  out lists as many tensors of the same
  * elems, each of its gradient's dtype or float32 (where half gradients lose their loss scale
  * without underflow), each its gradient itself or apart from all gradients.  With a factor of
  * exactly 1 a tensor that is its own output is left as it is; a non-finite norm makes every
  * output NaN. */
-fno_status fno_clip_grad_norm(int64_t count, const fno_tensor* grads, const fno_tensor* out,
+fno_status fno_clip_grad_norm(const fno_tensor_list* grads, const fno_tensor_list* out,
                               float max_norm, float grad_scale, float* record, void* workspace,
                               size_t workspace_bytes, void* stream);
 
@@ -431,8 +442,8 @@ typedef struct fno_adamw_desc {
  * (m = exp_avg, v = exp_avg_sq, float32).  When record's factor is not finite the update is
  * skipped: nothing is written, so that a loss-scaled run needs no synchronisation to drop such a
  * step. */
-fno_status fno_adamw(int64_t count, const fno_tensor* params, const fno_tensor* grads,
-                     const fno_tensor* exp_avg, const fno_tensor* exp_avg_sq,
+fno_status fno_adamw(const fno_tensor_list* params, const fno_tensor_list* grads,
+                     const fno_tensor_list* exp_avg, const fno_tensor_list* exp_avg_sq,
                      const fno_adamw_desc* desc, const float* record, void* stream);
 
 /* Per-kernel timing with HIP events, for measurement (off by default).  While enabled, every

@@ -479,14 +479,79 @@ def test_adamw_complex_parameters():
     assert torch.equal(torch.view_as_real(w), p) and torch.equal(torch.view_as_real(mw), m)
 
 
+def test_refusals():
+    """What needs a GPU to be asked: wrong shapes, lists that do not match."""
+    L = _L()
+    announce("train ops refusals")
+    x = torch.zeros(4, 8, 6, device="cuda")
+    st = torch.zeros(2, 4, 6, device="cuda")
+    with pytest.raises(ValueError, match="gamma"):
+        L.layer_norm_fwd(x, torch.ones(7, device="cuda"))
+    with pytest.raises(ValueError, match="gamma"):
+        L.layer_norm_fwd(x, torch.ones(8))
+    with pytest.raises(ValueError, match="out"):
+        L.layer_norm_fwd(x, out=x[:2])
+    with pytest.raises(ValueError, match="stats"):
+        L.layer_norm_bwd(x, None, st[:1], x)
+    with pytest.raises(ValueError, match="grad_y"):
+        L.layer_norm_bwd(x, None, st, x.bfloat16())
+    with pytest.raises(ValueError, match="one GPU"):
+        L.TensorList([x, x.cpu()])
+    with pytest.raises(ValueError, match="float32"):
+        L.TensorList([x.double()])
+    a, b, h = L.TensorList([x]), L.TensorList([x, x]), L.TensorList([x.half()])
+    short, other = L.TensorList([x[:2]]), L.TensorList([x.bfloat16()])
+    rec = torch.zeros(2, device="cuda")
+    for grads, out in ((a, b), (a, short), (a, h), (h, other)):
+        with pytest.raises(L.FnoError):
+            L.clip_grad_norm(grads, 1.0, out=out)
+    same = L.fno_tensor(x.data_ptr(), 4, 1, 0), L.fno_tensor(x.data_ptr(), 4, 0, 0)
+    for bad in (0.0, -1.0, math.nan):
+        with pytest.raises(L.FnoError):
+            L.grad_norm(a, bad)
+        if bad != 1.0:
+            with pytest.raises(L.FnoError):
+                L.grad_norm(a, 1.0, bad)
+    with pytest.raises(L.FnoError):
+        L.grad_norm(a, 1.0, math.inf)
+    with pytest.raises(L.FnoError, match="workspace"):
+        L.grad_norm(a, 1.0, ws=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(L.FnoError, match="workspace"):
+        L.grad_norm(a, 1.0, ws=torch.empty(4, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="record"):
+        L.grad_norm(a, record=rec[:1])
+    with pytest.raises(ValueError, match="record"):
+        L.adamw(a, a, a, a, 1, 1e-3, record=rec.half())
+    for lists in ((a, b, a, a), (a, a, b, a), (a, a, a, b), (a, short, a, a), (a, a, short, a)):
+        with pytest.raises(L.FnoError, match="another number"):
+            L.adamw(*lists, 1, 1e-3)
+    for lists in ((h, h, a, a), (a, a, h, a), (a, a, a, h)):
+        with pytest.raises(L.FnoError, match="float32"):
+            L.adamw(*lists, 1, 1e-3)
+    # a half gradient cannot widen over itself
+    tables = [torch.empty(4096, dtype=torch.uint8, device="cuda") for _ in same]
+    import ctypes
+    handles = []
+    for t, e in zip(tables, same):
+        handles.append(L.fno_tensor_list_create(1, ctypes.addressof(e), t.data_ptr(), 4096,
+                                                torch.cuda.current_stream().cuda_stream))
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    assert L._lib.fno_clip_grad_norm(handles[0], handles[1], 1.0, 1.0, rec.data_ptr(),
+                                     ws.data_ptr(), ws.numel(), None) == L.FNO_ERR_INVALID_ARGUMENT
+    for hd in handles:
+        L.fno_tensor_list_destroy(hd)
+    torch.cuda.synchronize()
+    assert not x.any() and not rec.any()
+
+
 # ---- streams and graphs ------------------------------------------------------------------------
 def _everything(L, s):
     y, stats = L.layer_norm_fwd(s["x"], s["gamma"], s["beta"], EPS, out=s["y"], stats=s["stats"])
     gr = L.layer_norm_bwd(s["x"], s["gamma"], s["stats"], s["gy"], out=s["grads"], ws=s["ws"])
-    rec = L.clip_grad_norm([gr["gamma"], gr["beta"], s["half"]], 0.5, out=s["clipped"],
-                           record=s["record"], ws=s["ws2"])
-    L.adamw([s["gamma"], s["beta"]], s["clipped"][:2], s["m"], s["v"], 1, 1e-2, record=None)
-    return rec
+    assert gr["gamma"] is s["grads"]["gamma"]
+    rec = L.clip_grad_norm(s["lists"][0], 0.5, out=s["lists"][1], record=s["record"],
+                           ws=s["ws2"])
+    L.adamw(*s["lists"][2:], 1, 1e-2, record=rec)
 
 
 def _state(L, seed):
@@ -503,6 +568,9 @@ def _state(L, seed):
     s["clipped"] = [torch.empty(20, device="cuda"), torch.empty(20, device="cuda"),
                     torch.empty(30_001, device="cuda")]
     s["m"], s["v"] = ([torch.zeros(20, device="cuda") for _ in range(2)] for _ in range(2))
+    s["lists"] = [L.TensorList(t) for t in (
+        [s["grads"]["gamma"], s["grads"]["beta"], s["half"]], s["clipped"],
+        [s["gamma"], s["beta"]], s["clipped"][:2], s["m"], s["v"])]
     return s
 
 
@@ -538,6 +606,8 @@ def test_graph_replays_match_eager():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         _everything(L, cap)
+        with pytest.raises(L.FnoError, match="capture"):
+            L.TensorList([cap["x"]])
     for k in range(4):
         x = _randn(_gen(40 + k), 2, 20, 333)
         eager["x"].copy_(x)

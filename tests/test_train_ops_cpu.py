@@ -81,35 +81,48 @@ def _list(*entries):
     return a
 
 
-def _norm(n, g, max_norm=1.0, scale=1.0, record=P, ws=P, ws_bytes=1 << 30):
-    return L._lib.fno_grad_norm(n, g, max_norm, scale, record, ws, ws_bytes, None)
+def _create(n, tensors, table=P, table_bytes=1 << 30, out=True):
+    h = ctypes.c_void_p()
+    return L._lib.fno_tensor_list_create(n, tensors, table, table_bytes, None,
+                                         ctypes.byref(h) if out else None)
 
 
 def test_tensor_lists_refused():
-    ok = _list((P, 4, 0))
-    for n, g in ((-1, ok), (1, None), (1, _list((None, 4, 0))), (1, _list((P + 2, 4, 0))),
-                 (1, _list((P, -1, 0))), (1, _list((P, 4, 9))), (1, _list((P, 1 << 37, 0)))):
-        assert _norm(n, g) == BAD
-        assert L._lib.fno_clip_grad_norm(n, g, g, 1.0, 1.0, P, P, 1 << 30, None) == BAD
     odd = _list((P, 4, 0))
     odd[0].reserved = 1
-    assert _norm(1, odd) == BAD
-    for kw in (dict(max_norm=0.0), dict(max_norm=-1.0), dict(max_norm=math.nan), dict(scale=0.0),
-               dict(scale=math.inf), dict(scale=math.nan), dict(record=None), dict(record=P + 2),
-               dict(ws=None), dict(ws=P + 4), dict(ws_bytes=0)):
-        assert _norm(1, ok, **kw) == BAD, kw
     n = ctypes.c_size_t()
-    assert L._lib.fno_grad_norm_workspace_bytes(-1, ctypes.byref(n)) == BAD
-    assert L._lib.fno_grad_norm_workspace_bytes(1, None) == BAD
+    for count, ts in ((-1, _list((P, 4, 0))), (1 << 40, _list((P, 4, 0))), (1, None),
+                      (1, _list((None, 4, 0))), (1, _list((P + 2, 4, 0))),
+                      (1, _list((P + 1, 4, 1))), (1, _list((P, -1, 0))), (1, _list((P, 4, 9))),
+                      (1, _list((P, 1 << 37, 0))), (1, odd)):
+        assert _create(count, ts) == BAD
+        assert L._lib.fno_tensor_list_bytes(count, ts, ctypes.byref(n)) == BAD
+    huge = _list(*[(P, 1 << 36, 1)] * 64)
+    assert _create(64, huge) == L.FNO_ERR_UNSUPPORTED
+    ok = _list((P, 4, 0), (None, 0, 2), (P + 2, 5000, 1))
+    assert L._lib.fno_tensor_list_bytes(3, ok, None) == BAD
+    assert L._lib.fno_tensor_list_bytes(3, ok, ctypes.byref(n)) == L.FNO_OK and n.value >= 72 + 16
+    assert _create(3, ok, table=None) == BAD and _create(3, ok, table=P + 4) == BAD
+    assert _create(3, ok, table_bytes=n.value - 1) == BAD
+    assert _create(3, ok, out=False) == BAD
+    assert L._lib.fno_tensor_list_destroy(None) == L.FNO_OK
 
 
-def test_clip_outputs_refused():
-    half = _list((P, 4, 1))
-    for out in (_list((P, 5, 1)), _list((P, 4, 0)), _list((P, 4, 2)), _list((2 * P, 4, 2))):
-        assert L._lib.fno_clip_grad_norm(1, half, out, 1.0, 1.0, P, P, 1 << 30, None) == BAD
-    full = _list((P, 4, 0))
-    assert L._lib.fno_clip_grad_norm(1, full, _list((2 * P, 4, 1)), 1.0, 1.0, P, P, 1 << 30,
-                                     None) == BAD
+def test_tensor_list_host_logic():
+    """The whole host side of a list (checks, chunks, table) runs before its first HIP call."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: the made-up addresses must not reach it")
+    ok = _list((P, 4, 0), (None, 0, 2), (P + 2, 5000, 1), (P, 1 << 22, 0))
+    assert _create(4, ok) == L.FNO_ERR_HIP
+
+
+def test_calls_without_lists_refused():
+    d = L.fno_adamw_desc(1e-3, 0.9, 0.99, 1e-8, 0.0, 1)
+    assert L._lib.fno_grad_norm(None, 1.0, 1.0, P, P, 1 << 30, None) == BAD
+    assert L._lib.fno_clip_grad_norm(None, None, 1.0, 1.0, P, P, 1 << 30, None) == BAD
+    assert L._lib.fno_adamw(None, None, None, None, d, None, None) == BAD
+    assert L._lib.fno_adamw(None, None, None, None, None, None, None) == BAD
+    assert L._lib.fno_grad_norm_workspace_bytes(None, None) == BAD
 
 
 @pytest.mark.parametrize("kw", [
@@ -120,20 +133,8 @@ def test_clip_outputs_refused():
 def test_adamw_descriptor_refused(kw):
     base = dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, weight_decay=0.0, step=1)
     base.update(kw)
-    t = _list((P, 4, 0))
-    assert L._lib.fno_adamw(1, t, t, t, t, L.fno_adamw_desc(**base), None, None) == BAD
-
-
-def test_adamw_lists_refused():
-    d = L.fno_adamw_desc(1e-3, 0.9, 0.99, 1e-8, 0.0, 1)
-    t, more, half = _list((P, 4, 0)), _list((P, 5, 0)), _list((P, 4, 1))
-    assert L._lib.fno_adamw(1, t, t, t, t, None, None, None) == BAD
-    for lists in ((t, more, t, t), (t, t, more, t), (t, t, t, more), (None, t, t, t)):
-        assert L._lib.fno_adamw(1, *lists, d, None, None) == BAD
-    assert L._lib.fno_adamw(1, t, t, t, t, d, P + 2, None) == BAD
-    for lists in ((half, t, t, t), (t, t, half, t), (t, t, t, half)):
-        assert L._lib.fno_adamw(1, *lists, d, None, None) == L.FNO_ERR_UNSUPPORTED
-    assert L._lib.fno_adamw(0, None, None, None, None, d, None, None) == L.FNO_OK
+    assert L._lib.fno_adamw(None, None, None, None, L.fno_adamw_desc(**base), None, None) == BAD
+    assert "AdamW" in L.last_error_message()
 
 
 def test_binding_refuses():
@@ -146,23 +147,11 @@ def test_binding_refuses():
         L.layer_norm_fwd(x[0, 0])
     with pytest.raises(ValueError, match="packed"):
         L.layer_norm_fwd(x.transpose(1, 2))
-    with pytest.raises(ValueError, match="real"):
-        L.layer_norm_fwd(x.to(torch.complex64))
-    with pytest.raises(ValueError, match="gamma"):
-        L.layer_norm_fwd(x, torch.ones(7))
-    with pytest.raises(ValueError, match="out"):
-        L.layer_norm_fwd(x, out=x[:2])
-    with pytest.raises(ValueError, match="stats"):
-        L.layer_norm_bwd(x, None, torch.zeros(2, 4), x)
-    with pytest.raises(ValueError, match="grad_y"):
-        L.layer_norm_bwd(x, None, torch.zeros(2, 4, 6), x.bfloat16())
-    with pytest.raises(ValueError, match="packed"):
-        L.TensorList([x, x.transpose(0, 1)])
     with pytest.raises(ValueError, match="float32"):
-        L.TensorList([x.double()])
+        L.layer_norm_fwd(x.to(torch.complex64))
+    with pytest.raises(ValueError, match="packed"):
+        L.TensorList([x.transpose(0, 1)])
     with pytest.raises(ValueError, match="GPU"):
-        L.grad_norm([x], record=torch.zeros(2), ws=torch.zeros(64, dtype=torch.uint8))
-    with pytest.raises(ValueError, match="record"):
-        L.grad_norm([x], record=torch.zeros(3))
-    with pytest.raises(ValueError, match="same number"):
-        L.adamw([x], [x, x], [x], [x], 1, 1e-3)
+        L.TensorList([x])
+    with pytest.raises(ValueError, match="GPU"):
+        L.grad_norm([x])
