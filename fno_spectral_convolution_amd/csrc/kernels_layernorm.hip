@@ -1,4 +1,6 @@
 // Layer norm over the channels of a field [batch][channels][npts], forward and backward.
+#include <type_traits>
+
 #include "train_device.h"
 #include "train_ops.h"
 
@@ -19,7 +21,26 @@ __device__ __forceinline__ void place(int j, int d, int& start, int& lo) {
   lo = e < d ? e - start : VEC;
 }
 
-// elements of the row that wave `w` of the row's waves holds (TPR >= 64)
+// A row's slice of gamma or beta; `none` where there is none.
+template <int VEC>
+__device__ __forceinline__ void load_weight(const float* w, int start, float none,
+                                            float (&f)[VEC]) {
+  if (w) {
+    constexpr int M = VEC < 4 ? VEC : 4;
+#pragma unroll
+    for (int i = 0; i < VEC; i += M) {
+      float q[M];
+      load_pack<float, M>(w + start + i, q);
+#pragma unroll
+      for (int e = 0; e < M; ++e) f[i + e] = q[e];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = none;
+  }
+}
+
+// elements of the row that wave `w` of the row's waves holds (TPR > 64)
 template <int VEC, int TPR, int NV>
 __device__ __forceinline__ float wave_count(int w, int d) {
   int n = 0;
@@ -31,10 +52,26 @@ __device__ __forceinline__ float wave_count(int w, int d) {
   return (float)n;
 }
 
+// Sum over the row's WAVES waves of a value that lane l has for wave l % WAVES, in every lane.
+template <int WAVES>
+__device__ __forceinline__ float wave_sum(float v) {
+  constexpr int kLanes = WAVES < 8 ? 8 : WAVES;
+  return lane_sum<kLanes>(v) * ((float)WAVES / kLanes);
+}
+
+// Calls f(masked) with a constant: whether any lane of the wave has elements that are not its own
+// (asked once; most waves of most rows have none, and are spared a select per element and sum).
+template <typename F>
+__device__ __forceinline__ void by_mask(bool masked, F&& f) {
+  if (masked) f(std::true_type());
+  else f(std::false_type());
+}
+
 template <typename T, int VEC, int TPR, int NV, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void k_ln_fwd_rows(NormArgs a, const T* x, const float* gamma,
                                                        const float* beta, T* y, float* stats) {
   constexpr int kGroups = BLOCK / TPR, kWaves = TPR > 64 ? TPR / 64 : 1;
+  constexpr int kLanes = TPR < 64 ? TPR : 64;
   __shared__ float s_stat[2][kGroups][kWaves][2];
   const int tid = threadIdx.x, t = tid % TPR, group = tid / TPR, wave = t / 64;
   const int d = a.channels;
@@ -44,21 +81,24 @@ __global__ __launch_bounds__(BLOCK) void k_ln_fwd_rows(NormArgs a, const T* x, c
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     place<VEC>(k * TPR + t, d, start[k], lo[k]);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      ga[k][i] = gamma ? gamma[start[k] + i] : 1.f;
-      be[k][i] = beta ? beta[start[k] + i] : 0.f;
-    }
+    load_weight<VEC>(gamma, start[k], 1.f, ga[k]);
+    load_weight<VEC>(beta, start[k], 0.f, be[k]);
   }
+  bool partial = false;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) partial |= lo[k] != 0;
+  partial = __any(partial);
+  const int other = t % kWaves;  // the wave whose part of a joint sum this lane reads
+  const float n = wave_count<VEC, TPR, NV>(wave, d), n_other = wave_count<VEC, TPR, NV>(other, d);
+  const float inv_n = TPR > 64 ? 1.0f / fmaxf(n, 1.f) : inv_d;
   const int64_t rows = a.batch, step = (int64_t)gridDim.x * kGroups;
   int64_t base = (int64_t)blockIdx.x * kGroups;
-  Pack<T, VEC> next[NV];
+  Raw<T, VEC> next[NV];
   const auto fetch = [&](int64_t at) {
     const int64_t row = at + group < rows ? at + group : rows - 1;
     const T* p = x + row * a.x_stride;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      next[k] = *reinterpret_cast<const Pack<T, VEC>*>(p + start[k]);
+    for (int k = 0; k < NV; ++k) next[k] = load_raw<T, VEC, true>(p + start[k]);
   };
   if (base < rows) fetch(base);
   int flip = 0;
@@ -67,23 +107,23 @@ __global__ __launch_bounds__(BLOCK) void k_ln_fwd_rows(NormArgs a, const T* x, c
 #pragma unroll
     for (int k = 0; k < NV; ++k) unpack<T, VEC>(next[k], f[k]);
     if (base + step < rows) fetch(base + step);
-    float sum = 0.f;
+    float mean, sq;
+    by_mask(partial, [&](auto masked) {
+      float sum = 0.f, sum2 = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+      for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) sum += i >= lo[k] ? f[k][i] : 0.f;
-    sum = lane_sum<(TPR < 64 ? TPR : 64)>(sum);
-    const float n = TPR > 64 ? wave_count<VEC, TPR, NV>(wave, d) : (float)d;
-    float mean = TPR > 64 ? sum / fmaxf(n, 1.f) : sum * inv_d;
-    float sq = 0.f;
+        for (int i = 0; i < VEC; ++i) sum += !masked.value || i >= lo[k] ? f[k][i] : 0.f;
+      mean = lane_sum<kLanes>(sum) * inv_n;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+      for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float c = f[k][i] - mean;
-        sq += i >= lo[k] ? c * c : 0.f;
-      }
-    sq = lane_sum<(TPR < 64 ? TPR : 64)>(sq);
+        for (int i = 0; i < VEC; ++i) {
+          const float c = f[k][i] - mean;
+          sum2 += !masked.value || i >= lo[k] ? c * c : 0.f;
+        }
+      sq = lane_sum<kLanes>(sum2);
+    });
     if (TPR > 64) {
       // the waves' means and squared deviations join: M2 = sum M2_w + n_w (mean_w - mean)^2
       if (t % 64 == 0) {
@@ -91,29 +131,20 @@ __global__ __launch_bounds__(BLOCK) void k_ln_fwd_rows(NormArgs a, const T* x, c
         s_stat[flip][group][wave][1] = sq;
       }
       __syncthreads();
-      float mw[kWaves], nw[kWaves], all = 0.f;
-      sq = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        mw[w] = s_stat[flip][group][w][0];
-        sq += s_stat[flip][group][w][1];
-        nw[w] = wave_count<VEC, TPR, NV>(w, d);
-        all += nw[w] * mw[w];
-      }
-      mean = all * inv_d;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) sq += nw[w] * (mw[w] - mean) * (mw[w] - mean);
+      const float m = s_stat[flip][group][other][0], q2 = s_stat[flip][group][other][1];
+      mean = wave_sum<kWaves>(n_other * m) * inv_d;
+      sq = wave_sum<kWaves>(q2 + n_other * (m - mean) * (m - mean));
     }
-    const float rstd = 1.0f / sqrtf(sq * inv_d + a.eps);
+    const float rstd = rsqrtf(sq * inv_d + a.eps);
     const int64_t row = base + group;
     if (row < rows) {
-      T* q = y + row * a.y_stride;
+      T* o = y + row * a.y_stride;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        float o[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] = ga[k][i] * ((f[k][i] - mean) * rstd) + be[k][i];
-        if (lo[k] < VEC) store_pack<T, VEC>(q + start[k], o);
+        for (int i = 0; i < VEC; ++i)
+          f[k][i] = ga[k][i] * ((f[k][i] - mean) * rstd) + be[k][i];
+        if (lo[k] < VEC) store_pack<T, VEC>(o + start[k], f[k], a.stream);
       }
       if (stats && t == 0) {
         stats[row] = mean;
@@ -128,7 +159,9 @@ __global__ __launch_bounds__(BLOCK) void k_ln_bwd_rows(NormArgs a, const T* x, c
                                                        const float* stats, const T* gy, T* gx,
                                                        float* part) {
   constexpr int kGroups = BLOCK / TPR, kWaves = TPR > 64 ? TPR / 64 : 1;
-  constexpr bool kAhead = NV * VEC < 16;  // the next row's loads ahead, where registers allow
+  constexpr int kLanes = TPR < 64 ? TPR : 64;
+  // the next row's loads go ahead of this one's sums where the registers allow
+  constexpr bool kAhead = NV * VEC < 16;
   constexpr int kSets = BLOCK / (TPR < 64 ? 64 : TPR), kCols = TPR * VEC;
   __shared__ float s_sum[2][kGroups][kWaves][2];
   __shared__ float s_cols[kSets][kCols];
@@ -140,27 +173,28 @@ __global__ __launch_bounds__(BLOCK) void k_ln_bwd_rows(NormArgs a, const T* x, c
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     place<VEC>(k * TPR + t, d, start[k], lo[k]);
+    load_weight<VEC>(gamma, start[k], 1.f, ga[k]);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      ga[k][i] = gamma ? gamma[start[k] + i] : 1.f;
-      dg[k][i] = db[k][i] = 0.f;
-    }
+    for (int i = 0; i < VEC; ++i) dg[k][i] = db[k][i] = 0.f;
   }
+  bool partial = false;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) partial |= lo[k] != 0;
+  partial = __any(partial);
   const int64_t rows = a.batch, step = (int64_t)gridDim.x * kGroups;
   int64_t base = (int64_t)blockIdx.x * kGroups;
-  Pack<T, VEC> nx[NV], ng[NV];
-  float nmean = 0.f, nrstd = 0.f;
+  Raw<T, VEC> next_x[NV], next_g[NV];
+  float next_mean = 0.f, next_rstd = 0.f;
   const auto fetch = [&](int64_t at) {
     const int64_t row = at + group < rows ? at + group : rows - 1;
-    const T* p = x + row * a.x_stride;
-    const T* q = gy + row * a.y_stride;
+    const T *p = x + row * a.x_stride, *r = gy + row * a.y_stride;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      nx[k] = *reinterpret_cast<const Pack<T, VEC>*>(p + start[k]);
-      ng[k] = *reinterpret_cast<const Pack<T, VEC>*>(q + start[k]);
+      next_x[k] = load_raw<T, VEC, true>(p + start[k]);
+      next_g[k] = load_raw<T, VEC, true>(r + start[k]);
     }
-    nmean = stats[row];
-    nrstd = stats[rows + row];
+    next_mean = stats[row];
+    next_rstd = stats[rows + row];
   };
   if (kAhead && base < rows) fetch(base);
   int flip = 0;
@@ -168,53 +202,55 @@ __global__ __launch_bounds__(BLOCK) void k_ln_bwd_rows(NormArgs a, const T* x, c
     const int64_t row = base + group;
     const bool live = row < rows;
     if (!kAhead) fetch(base);
-    const float mean = nmean, rstd = nrstd;
+    const float mean = next_mean, rstd = next_rstd;
     float h[NV][VEC], g[NV][VEC], s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      unpack<T, VEC>(nx[k], h[k]);
-      unpack<T, VEC>(ng[k], g[k]);
+      unpack<T, VEC>(next_x[k], h[k]);
+      unpack<T, VEC>(next_g[k], g[k]);
     }
     if (kAhead && base + step < rows) fetch(base + step);
+    if (live) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+      for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const bool mine = i >= lo[k];
-        h[k][i] = (h[k][i] - mean) * rstd;
-        if (live) {
+        for (int i = 0; i < VEC; ++i) {
+          h[k][i] = (h[k][i] - mean) * rstd;
           dg[k][i] += g[k][i] * h[k][i];
           db[k][i] += g[k][i];
+          g[k][i] *= ga[k][i];
         }
-        g[k][i] *= ga[k][i];
-        s1 += mine ? g[k][i] : 0.f;
-        s2 += mine ? g[k][i] * h[k][i] : 0.f;
-      }
-    s1 = lane_sum<(TPR < 64 ? TPR : 64)>(s1);
-    s2 = lane_sum<(TPR < 64 ? TPR : 64)>(s2);
+    }
+    by_mask(partial, [&](auto masked) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float v = !masked.value || i >= lo[k] ? g[k][i] : 0.f;
+          s1 += v;
+          s2 += v * h[k][i];
+        }
+    });
+    s1 = lane_sum<kLanes>(s1);
+    s2 = lane_sum<kLanes>(s2);
     if (TPR > 64) {
       if (t % 64 == 0) {
         s_sum[flip][group][wave][0] = s1;
         s_sum[flip][group][wave][1] = s2;
       }
       __syncthreads();
-      s1 = s2 = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        s1 += s_sum[flip][group][w][0];
-        s2 += s_sum[flip][group][w][1];
-      }
+      s1 = wave_sum<kWaves>(s_sum[flip][group][t % kWaves][0]);
+      s2 = wave_sum<kWaves>(s_sum[flip][group][t % kWaves][1]);
     }
     s1 *= inv_d;
     s2 *= inv_d;
     if (gx && live) {
-      T* q = gx + row * a.gx_stride;
+      T* o = gx + row * a.gx_stride;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        float o[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] = rstd * (g[k][i] - s1 - h[k][i] * s2);
-        if (lo[k] < VEC) store_pack<T, VEC>(q + start[k], o);
+        for (int i = 0; i < VEC; ++i) g[k][i] = rstd * (g[k][i] - s1 - h[k][i] * s2);
+        if (lo[k] < VEC) store_pack<T, VEC>(o + start[k], g[k], a.stream);
       }
     }
   }
@@ -228,7 +264,7 @@ __global__ __launch_bounds__(BLOCK) void k_ln_bwd_rows(NormArgs a, const T* x, c
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float v = stride_sum<(TPR < 64 ? TPR : 64)>(m == 0 ? dg[k][i] : db[k][i]);
+        const float v = stride_sum<kLanes>(m == 0 ? dg[k][i] : db[k][i]);
         if (TPR >= 64 || tid % 64 < TPR)
           s_cols[tid / (TPR < 64 ? 64 : TPR)][t * VEC + i] = v;
       }
@@ -282,15 +318,17 @@ __global__ __launch_bounds__(kLong) void k_ln_fwd_long(NormArgs a, const T* x, c
 #pragma unroll
       for (int i = 0; i < VEC; ++i) sq += i >= lo ? (f[i] - mean) * (f[i] - mean) : 0.f;
     }
-    const float rstd = 1.0f / sqrtf(group_sum(sq, s_red) / (float)d + a.eps);
+    const float rstd = rsqrtf(group_sum(sq, s_red) / (float)d + a.eps);
     // in place the vector that overlaps its neighbour must not read what that one wrote: the last
     // vector stores only its own elements, one by one
     for (int j = tid; j < nvec; j += kLong) {
       place<VEC>(j, d, st, lo);
       load_pack<T, VEC>(p + st, f);
+      float ga[VEC], be[VEC];
+      load_weight<VEC>(gamma, st, 1.f, ga);
+      load_weight<VEC>(beta, st, 0.f, be);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        f[i] = (gamma ? gamma[st + i] : 1.f) * ((f[i] - mean) * rstd) + (beta ? beta[st + i] : 0.f);
+      for (int i = 0; i < VEC; ++i) f[i] = ga[i] * ((f[i] - mean) * rstd) + be[i];
       if (lo == 0) store_pack<T, VEC>(q + st, f);
       else
         for (int i = 0; i < VEC; ++i)
@@ -314,15 +352,16 @@ __global__ __launch_bounds__(kLong) void k_ln_bwd_long(NormArgs a, const T* x, c
     const T* r = gy + row * a.y_stride;
     T* q = gx + row * a.gx_stride;
     const float mean = stats[row], rstd = stats[a.batch + row];
-    float h[VEC], g[VEC], s1 = 0.f, s2 = 0.f;
+    float h[VEC], g[VEC], ga[VEC], s1 = 0.f, s2 = 0.f;
     int st, lo;
     for (int j = tid; j < nvec; j += kLong) {
       place<VEC>(j, d, st, lo);
       load_pack<T, VEC>(p + st, h);
       load_pack<T, VEC>(r + st, g);
+      load_weight<VEC>(gamma, st, 1.f, ga);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float v = g[i] * (gamma ? gamma[st + i] : 1.f);
+        const float v = g[i] * ga[i];
         s1 += i >= lo ? v : 0.f;
         s2 += i >= lo ? v * ((h[i] - mean) * rstd) : 0.f;
       }
@@ -333,9 +372,10 @@ __global__ __launch_bounds__(kLong) void k_ln_bwd_long(NormArgs a, const T* x, c
       place<VEC>(j, d, st, lo);
       load_pack<T, VEC>(p + st, h);
       load_pack<T, VEC>(r + st, g);
+      load_weight<VEC>(gamma, st, 1.f, ga);
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
-        g[i] = rstd * (g[i] * (gamma ? gamma[st + i] : 1.f) - s1 - (h[i] - mean) * rstd * s2);
+        g[i] = rstd * (g[i] * ga[i] - s1 - (h[i] - mean) * rstd * s2);
       if (lo == 0) store_pack<T, VEC>(q + st, g);
       else
         for (int i = 0; i < VEC; ++i)
@@ -378,41 +418,75 @@ __global__ __launch_bounds__(256) void k_ln_cols_long(NormArgs a, const T* x, co
 // registers; what a point's channels sum to joins through LDS.  FLAT: one point to a lane, counted
 // through all batch entries (short entries); else tiles of 64 VEC points of one entry.
 struct Tile {
-  int64_t at;    // (batch, point) of the lane's first element, in rows
-  int64_t b, p;
-  int lo;        // the lane's own points are i >= lo
+  int64_t b, p;   // batch entry and point where the tile starts (FLAT: of the lane's own point)
+  uint32_t off;   // the lane's first element from there (below 64 VEC)
+  int lo;         // the lane's own points are i >= lo
 };
 
+// The tiles of a work-group, a grid apart, without a division for each.
 template <int VEC, bool FLAT>
-__device__ __forceinline__ Tile tile_of(const NormArgs& a, int64_t tile, int64_t per_entry) {
-  Tile t;
-  const int lane = threadIdx.x & 63;
-  if (FLAT) {
-    const int64_t rows = a.batch * a.npts, r = tile * 64 + lane;
-    t.at = r < rows ? r : rows - 1;
-    t.lo = r < rows ? 0 : 1;
-    if (rows <= 0x7fffffff) {
-      const uint32_t b = (uint32_t)t.at / (uint32_t)a.npts;
-      t.b = b;
-      t.p = (uint32_t)t.at - b * (uint32_t)a.npts;
+struct Tiles {
+  int64_t left, entry, at, step_entries, step_at;
+  __device__ __forceinline__ Tiles(int64_t tiles, int64_t per_entry) {
+    left = tiles - blockIdx.x;
+    if (FLAT) {
+      entry = step_entries = step_at = 0;
+      at = blockIdx.x;
     } else {
-      t.b = t.at / a.npts;
-      t.p = t.at - t.b * a.npts;
+      entry = uniform((int64_t)blockIdx.x / per_entry);
+      at = (int64_t)blockIdx.x - entry * per_entry;
+      step_entries = uniform((int64_t)gridDim.x / per_entry);
+      step_at = (int64_t)gridDim.x - step_entries * per_entry;
     }
-  } else {
-    t.b = tile / per_entry;
-    const int64_t e = (tile - t.b * per_entry) * (64 * VEC) + lane * VEC;
-    t.p = e < a.npts - VEC ? e : a.npts - VEC;
-    t.lo = e < a.npts ? (int)(e - t.p) : VEC;
-    t.at = t.b * a.npts + t.p;
   }
-  return t;
-}
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ void next(int64_t per_entry) {
+    left -= gridDim.x;
+    if (FLAT) {
+      at += gridDim.x;
+      return;
+    }
+    entry += step_entries;
+    at += step_at;
+    if (at >= per_entry) {
+      at -= per_entry;
+      ++entry;
+    }
+  }
+  __device__ __forceinline__ Tile tile(const NormArgs& a) const {
+    Tile t;
+    const int lane = threadIdx.x & 63;
+    if (FLAT) {
+      const int64_t rows = a.batch * a.npts;
+      int64_t r = at * 64 + lane;
+      t.lo = r < rows ? 0 : 1;
+      r = r < rows ? r : rows - 1;
+      t.off = 0;
+      if (rows <= 0x7fffffff) {
+        const uint32_t b = (uint32_t)r / (uint32_t)a.npts;
+        t.b = b;
+        t.p = (uint32_t)r - b * (uint32_t)a.npts;
+      } else {
+        t.b = r / a.npts;
+        t.p = r - t.b * a.npts;
+      }
+    } else {
+      t.b = entry;
+      const int64_t first = at * (64 * VEC), last = a.npts - VEC;
+      t.p = first < last ? first : last;
+      const int most = last - t.p < 64 * VEC ? (int)(last - t.p) : 64 * VEC;
+      const int e = (int)(first - t.p) + lane * VEC, own = e < most ? e : most;
+      t.off = (uint32_t)own;
+      t.lo = e - own < VEC ? e - own : VEC;
+    }
+    return t;
+  }
+};
 
 template <typename T, int VEC>
-__device__ __forceinline__ void store_own(T* p, const float (&f)[VEC], int lo) {
+__device__ __forceinline__ void store_own(T* p, const float (&f)[VEC], int lo, bool stream) {
   if (lo == 0) {
-    store_pack<T, VEC>(p, f);
+    store_pack<T, VEC>(p, f, stream);
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
@@ -421,39 +495,39 @@ __device__ __forceinline__ void store_own(T* p, const float (&f)[VEC], int lo) {
 }
 
 template <typename T, int N, int VEC, bool FLAT>
-__global__ __launch_bounds__(1024) void k_ln_fwd_field(NormArgs a, int64_t tiles,
-                                                       int64_t per_entry, const T* x,
-                                                       const float* gamma, const float* beta,
-                                                       T* y, float* stats) {
+__global__ __launch_bounds__(N <= 8 ? 512 : 1024) void k_ln_fwd_field(
+    NormArgs a, int64_t tiles, int64_t per_entry, const T* x, const float* gamma,
+    const float* beta, T* y, float* stats) {
   extern __shared__ float s_mem[];  // [2][waves][2][64 VEC]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
   const int c0 = wave * N, nc = a.channels - c0 < N ? a.channels - c0 : N;
   const float inv_c = 1.0f / (float)a.channels, inv_n = 1.0f / (float)nc;
   int flip = 0;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, flip ^= 1) {
-    const Tile t = tile_of<VEC, FLAT>(a, tile, per_entry);
+  for (Tiles<VEC, FLAT> at(tiles, per_entry); at.more(); at.next(per_entry), flip ^= 1) {
+    const Tile t = at.tile(a);
     const T* p = x + t.b * a.x_stride + t.p;
-    float f[N][VEC], mean[VEC], sq[VEC];
+    float f[N][VEC], mean[VEC] = {}, sq[VEC] = {};
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      unpack<T, VEC>(
+          load_raw<T, VEC, true>(p + (c < nc ? c0 + c : a.channels - 1) * a.npts + t.off), f[c]);
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) mean[i] += c < nc ? f[c][i] : 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) mean[i] *= inv_n;
 #pragma unroll
     for (int c = 0; c < N; ++c) {
-      const int ch = c < nc ? c0 + c : a.channels - 1;
-      load_pack<T, VEC>(p + ch * a.npts, f[c]);
-    }
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      float s = 0.f, q = 0.f;
-#pragma unroll
-      for (int c = 0; c < N; ++c) s += c < nc ? f[c][i] : 0.f;
-      mean[i] = s * inv_n;
-#pragma unroll
-      for (int c = 0; c < N; ++c) {
+      for (int i = 0; i < VEC; ++i) {
         const float e = f[c][i] - mean[i];
-        q += c < nc ? e * e : 0.f;
+        sq[i] += c < nc ? e * e : 0.f;
       }
-      sq[i] = q;
     }
     if (waves > 1) {
+      // the waves' means and squared deviations join: M2 = sum M2_w + n_w (mean_w - mean)^2
       float* s_t = s_mem + flip * waves * 2 * 64 * VEC;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
@@ -483,21 +557,21 @@ __global__ __launch_bounds__(1024) void k_ln_fwd_field(NormArgs a, int64_t tiles
     }
     float rstd[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) rstd[i] = 1.0f / sqrtf(sq[i] * inv_c + a.eps);
+    for (int i = 0; i < VEC; ++i) rstd[i] = rsqrtf(sq[i] * inv_c + a.eps);
     if (t.lo < VEC) {
-      T* q = y + t.b * a.y_stride + t.p;
+      T* o = y + t.b * a.y_stride + t.p;
 #pragma unroll
       for (int c = 0; c < N; ++c)
         if (c < nc) {
           const float ga = gamma ? gamma[c0 + c] : 1.f, be = beta ? beta[c0 + c] : 0.f;
-          float o[VEC];
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) o[i] = ga * ((f[c][i] - mean[i]) * rstd[i]) + be;
-          store_own<T, VEC>(q + (c0 + c) * a.npts, o, t.lo);
+          for (int i = 0; i < VEC; ++i) f[c][i] = ga * ((f[c][i] - mean[i]) * rstd[i]) + be;
+          store_own<T, VEC>(o + (c0 + c) * a.npts + t.off, f[c], t.lo, a.stream);
         }
       if (stats && wave == 0) {
-        store_own<float, VEC>(stats + t.at, mean, t.lo);
-        store_own<float, VEC>(stats + a.batch * a.npts + t.at, rstd, t.lo);
+        float* st = stats + t.b * a.npts + t.p;
+        store_own<float, VEC>(st + t.off, mean, t.lo, false);
+        store_own<float, VEC>(st + a.batch * a.npts + t.off, rstd, t.lo, false);
       }
     }
   }
@@ -515,19 +589,20 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_field(NormArgs a, int64_t tiles
   const float inv_c = 1.0f / (float)a.channels;
   float dg[N] = {}, db[N] = {};
   int flip = 0;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, flip ^= 1) {
-    const Tile t = tile_of<VEC, FLAT>(a, tile, per_entry);
+  for (Tiles<VEC, FLAT> at(tiles, per_entry); at.more(); at.next(per_entry), flip ^= 1) {
+    const Tile t = at.tile(a);
     const T* p = x + t.b * a.x_stride + t.p;
     const T* r = gy + t.b * a.y_stride + t.p;
     float h[N][VEC], g[N][VEC], mean[VEC], rstd[VEC], s1[VEC] = {}, s2[VEC] = {};
 #pragma unroll
     for (int c = 0; c < N; ++c) {
-      const int ch = c < nc ? c0 + c : a.channels - 1;
-      load_pack<T, VEC>(p + ch * a.npts, h[c]);
-      load_pack<T, VEC>(r + ch * a.npts, g[c]);
+      const int64_t ch = (c < nc ? c0 + c : a.channels - 1) * a.npts;
+      unpack<T, VEC>(load_raw<T, VEC, true>(p + ch + t.off), h[c]);
+      unpack<T, VEC>(load_raw<T, VEC, true>(r + ch + t.off), g[c]);
     }
-    load_pack<float, VEC>(stats + t.at, mean);
-    load_pack<float, VEC>(stats + a.batch * a.npts + t.at, rstd);
+    const float* st = stats + t.b * a.npts + t.p;
+    load_pack<float, VEC>(st + t.off, mean);
+    load_pack<float, VEC>(st + a.batch * a.npts + t.off, rstd);
 #pragma unroll
     for (int c = 0; c < N; ++c) {
       const float ga = c < nc ? (gamma ? gamma[c0 + c] : 1.f) : 0.f;
@@ -562,15 +637,15 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_field(NormArgs a, int64_t tiles
         }
     }
     if (gx && t.lo < VEC) {
-      T* q = gx + t.b * a.gx_stride + t.p;
+      T* o = gx + t.b * a.gx_stride + t.p;
 #pragma unroll
       for (int c = 0; c < N; ++c)
         if (c < nc) {
-          float o[VEC];
+          float f[VEC];
 #pragma unroll
           for (int i = 0; i < VEC; ++i)
-            o[i] = rstd[i] * (g[c][i] - s1[i] * inv_c - h[c][i] * (s2[i] * inv_c));
-          store_own<T, VEC>(q + (c0 + c) * a.npts, o, t.lo);
+            f[i] = rstd[i] * (g[c][i] - s1[i] * inv_c - h[c][i] * (s2[i] * inv_c));
+          store_own<T, VEC>(o + (c0 + c) * a.npts + t.off, f, t.lo, a.stream);
         }
     }
   }
@@ -603,7 +678,7 @@ __global__ __launch_bounds__(256) void k_ln_fwd_points(NormArgs a, const T* x, c
       const float d = to_float(xr[c * a.npts]) - mean;
       sq += d * d;
     }
-    const float rstd = 1.0f / sqrtf(sq / (float)a.channels + a.eps);
+    const float rstd = rsqrtf(sq / (float)a.channels + a.eps);
     for (int c = 0; c < a.channels; ++c) {
       const float h = (to_float(xr[c * a.npts]) - mean) * rstd;
       yr[c * a.npts] = from_float<T>((gamma ? gamma[c] : 1.f) * h + (beta ? beta[c] : 0.f));
@@ -708,6 +783,18 @@ Form form_of(const NormArgs& a) {
 int64_t cut(int64_t v, int64_t most) { return v < most ? v : most; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Work-groups of a kernel that the 256 compute units hold at a time (asked for once).
+template <auto Kernel>
+int64_t resident(int block) {
+  static const int64_t n = [block]() {
+    int per_cu = 0;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, Kernel, block, 0) != hipSuccess)
+      per_cu = 1;
+    return (int64_t)256 * (per_cu > 0 ? per_cu : 1);
+  }();
+  return n;
+}
+
 // Calls f(threads to a row, vectors to a thread) as constants, for rows of `nvec` vectors.
 template <int N>
 struct Int {
@@ -715,7 +802,7 @@ struct Int {
 };
 template <typename T, typename F>
 void pick_rows(int channels, F&& f) {
-  constexpr int VEC = kVec<T>;
+  constexpr int VEC = kVec<T>, NV = 8 / VEC;  // 8 elements to a thread, 16 in the longest rows
   if (channels < VEC) return f(Int<1>(), Int<8>(), Int<1>());
   const int nvec = (channels + VEC - 1) / VEC;
   const Int<VEC> v;
@@ -723,12 +810,13 @@ void pick_rows(int channels, F&& f) {
   if (nvec <= 16) return f(v, Int<16>(), Int<1>());
   if (nvec <= 32) return f(v, Int<32>(), Int<1>());
   if (nvec <= 64) return f(v, Int<64>(), Int<1>());
-  if (nvec <= 128) return f(v, Int<128>(), Int<1>());
-  if (nvec <= 256) return f(v, Int<256>(), Int<1>());
-  if (nvec <= 512) return f(v, Int<512>(), Int<1>());
-  if (nvec <= 1024) return f(v, Int<1024>(), Int<1>());
-  if (nvec <= 2048) return f(v, Int<1024>(), Int<2>());
-  if constexpr (VEC == 4) return f(v, Int<1024>(), Int<4>());
+  if constexpr (NV > 1)
+    if (nvec <= 64 * NV) return f(v, Int<64>(), Int<NV>());
+  if (nvec <= 128 * NV) return f(v, Int<128>(), Int<NV>());
+  if (nvec <= 256 * NV) return f(v, Int<256>(), Int<NV>());
+  if (nvec <= 512 * NV) return f(v, Int<512>(), Int<NV>());
+  if (nvec <= 1024 * NV) return f(v, Int<1024>(), Int<NV>());
+  return f(v, Int<1024>(), Int<2 * NV>());
 }
 
 constexpr int kBwdBlock = 1024;
@@ -737,32 +825,14 @@ int bwd_rows_groups(int64_t rows) {
   return (int)cut(ceil_div(rows, kBwdBlock / TPR), 256);
 }
 
-// fields: channels to a wave, and waves
-#ifndef FN
-#define FN 8
-#endif
-#ifndef BN
-#define BN 8
-#endif
-#ifndef FV
-#define FV 4
-#endif
-#ifndef BV
-#define BV 2
-#endif
-#ifndef FG
-#define FG (1<<20)
-#endif
-#ifndef BG
-#define BG 4096
-#endif
-int field_n(int c, int most) {
-  const int waves = (int)cut(ceil_div(c, most), 16), n = (int)ceil_div(c, waves);
-  return n <= 8 ? n : n <= 12 ? 12 : 16;
+// fields: channels to a wave, at most 8 for up to 64 channels (and so at most 8 waves)
+int field_n(int c) {
+  if (c <= 64) return (int)ceil_div(c, ceil_div(c, 8));
+  return c <= 100 ? 10 : c <= 120 ? 12 : 16;
 }
 template <typename F>
-void pick_field(int n, F&& f) {
-  switch (n) {
+void pick_field(int c, F&& f) {
+  switch (field_n(c)) {
     case 1: return f(Int<1>());
     case 2: return f(Int<2>());
     case 3: return f(Int<3>());
@@ -771,58 +841,75 @@ void pick_field(int n, F&& f) {
     case 6: return f(Int<6>());
     case 7: return f(Int<7>());
     case 8: return f(Int<8>());
+    case 10: return f(Int<10>());
     case 12: return f(Int<12>());
     default: return f(Int<16>());
   }
 }
+// points to a lane
+template <typename T>
+constexpr int kFwdVec = 4;
+template <typename T, int N>
+constexpr int kBwdVec = N <= 10 ? 2 : 1;
 struct FieldShape {
   bool flat;
-  int n, waves;
+  int waves;
   int64_t per_entry, tiles;
   size_t lds;
 };
-FieldShape field_shape(const NormArgs& a, int most, int wide) {
+FieldShape field_shape(const NormArgs& a, int n, int wide) {
   FieldShape s;
-  s.flat = a.npts < 512;
+  s.flat = a.npts < 256;
   const int vec = s.flat ? 1 : wide;
-  s.n = field_n(a.channels, most);
-  s.waves = (int)ceil_div(a.channels, s.n);
+  s.waves = (int)ceil_div(a.channels, n);
   s.per_entry = ceil_div(a.npts, 64 * vec);
   s.tiles = s.flat ? ceil_div(a.batch * a.npts, 64) : a.batch * s.per_entry;
   s.lds = s.waves > 1 ? sizeof(float) * 2 * s.waves * 2 * 64 * vec : 0;
   return s;
 }
-int field_bwd_groups(const FieldShape& s) { return (int)cut(s.tiles, ceil_div(BG, s.waves)); }
+int field_bwd_groups(const FieldShape& s) { return (int)cut(s.tiles, ceil_div(8192, s.waves)); }
+
+// Whether an output goes past the caches: where it is larger than the L2s together (32 MB) and
+// its rows or planes are whole 128-byte lines.
+template <typename T>
+bool stream_out(const NormArgs& a, const T* out, int64_t stride) {
+  const int64_t pitch = (a.npts == 1 ? stride : a.npts) * (int64_t)sizeof(T);
+  return a.batch * a.npts * a.channels * (int64_t)sizeof(T) > ((int64_t)256 << 20) && pitch % 128 == 0 &&
+         (a.batch <= 1 || stride * (int64_t)sizeof(T) % 128 == 0) &&
+         reinterpret_cast<uintptr_t>(out) % 128 == 0;
+}
 
 template <typename T>
-hipError_t fwd_t(const NormArgs& a, const T* x, const float* gamma, const float* beta, T* y,
+hipError_t fwd_t(NormArgs a, const T* x, const float* gamma, const float* beta, T* y,
                  float* stats, hipStream_t s) {
+  a.stream = stream_out(a, y, a.y_stride);
   switch (form_of<T>(a)) {
     case kRows:
       pick_rows<T>(a.channels, [&](auto vec, auto tpr, auto nv) {
         constexpr int kBlock = tpr.value < 256 ? 256 : tpr.value;
-        const int64_t groups = cut(ceil_div(a.batch, kBlock / tpr.value), 256 * 2048 / kBlock);
-        hipLaunchKernelGGL((k_ln_fwd_rows<T, vec.value, tpr.value, nv.value, kBlock>),
-                           dim3(groups), dim3(kBlock), 0, s, a, x, gamma, beta, y, stats);
+        constexpr auto kernel = k_ln_fwd_rows<T, vec.value, tpr.value, nv.value, kBlock>;
+        const int64_t need = ceil_div(a.batch, kBlock / tpr.value), most = resident<kernel>(kBlock);
+        // as many rounds as that takes, shared out evenly
+        const int64_t groups = ceil_div(need, ceil_div(need, most));
+        hipLaunchKernelGGL(kernel, dim3(groups), dim3(kBlock), 0, s, a, x, gamma, beta, y, stats);
       });
       break;
     case kLongRows:
       hipLaunchKernelGGL(k_ln_fwd_long<T>, dim3(cut(a.batch, 1024)), dim3(kLong), 0, s, a, x, gamma,
                          beta, y, stats);
       break;
-    case kField: {
-      const FieldShape f = field_shape(a, FN, FV);
-      const dim3 grid(cut(f.tiles, FG)), block(64 * f.waves);
-      pick_field(f.n, [&](auto n) {
+    case kField:
+      pick_field(a.channels, [&](auto n) {
+        const FieldShape f = field_shape(a, n.value, kFwdVec<T>);
+        const dim3 grid(cut(f.tiles, 1 << 20)), block(64 * f.waves);
         if (f.flat)
           hipLaunchKernelGGL((k_ln_fwd_field<T, n.value, 1, true>), grid, block, f.lds, s, a,
                              f.tiles, f.per_entry, x, gamma, beta, y, stats);
         else
-          hipLaunchKernelGGL((k_ln_fwd_field<T, n.value, FV, false>), grid, block, f.lds, s,
-                             a, f.tiles, f.per_entry, x, gamma, beta, y, stats);
+          hipLaunchKernelGGL((k_ln_fwd_field<T, n.value, kFwdVec<T>, false>), grid, block, f.lds,
+                             s, a, f.tiles, f.per_entry, x, gamma, beta, y, stats);
       });
       break;
-    }
     case kPoints:
       hipLaunchKernelGGL(k_ln_fwd_points<T>, dim3(cut(ceil_div(a.batch * a.npts, 256), 4096)),
                          dim3(256), 0, s, a, x, gamma, beta, y, stats);
@@ -840,15 +927,22 @@ int parts_t(const NormArgs& a) {
                    [&](auto, auto tpr, auto) { n = bwd_rows_groups<tpr.value>(a.batch); });
       return n;
     }
-    case kField: return field_bwd_groups(field_shape(a, BN, BV));
+    case kField: {
+      int n = 0;
+      pick_field(a.channels, [&](auto c) {
+        n = field_bwd_groups(field_shape(a, c.value, kBwdVec<T, c.value>));
+      });
+      return n;
+    }
     default: return (int)cut(a.npts == 1 ? a.batch : kPointParts, kPointParts);
   }
 }
 
 template <typename T>
-hipError_t bwd_t(const NormArgs& a, const T* x, const float* gamma, const float* stats,
+hipError_t bwd_t(NormArgs a, const T* x, const float* gamma, const float* stats,
                  const T* gy, T* gx, float* part, hipStream_t s) {
   const int parts = parts_t<T>(a);
+  a.stream = stream_out(a, gx, a.gx_stride);
   switch (form_of<T>(a)) {
     case kRows:
       pick_rows<T>(a.channels, [&](auto vec, auto tpr, auto nv) {
@@ -856,19 +950,19 @@ hipError_t bwd_t(const NormArgs& a, const T* x, const float* gamma, const float*
                            dim3(parts), dim3(kBwdBlock), 0, s, a, x, gamma, stats, gy, gx, part);
       });
       break;
-    case kField: {
-      const FieldShape f = field_shape(a, BN, BV);
-      const dim3 grid(parts), block(64 * f.waves);
-      pick_field(f.n, [&](auto n) {
+    case kField:
+      pick_field(a.channels, [&](auto n) {
+        constexpr int kWide = kBwdVec<T, n.value>;
+        const FieldShape f = field_shape(a, n.value, kWide);
+        const dim3 grid(parts), block(64 * f.waves);
         if (f.flat)
           hipLaunchKernelGGL((k_ln_bwd_field<T, n.value, 1, true>), grid, block, f.lds, s, a,
                              f.tiles, f.per_entry, x, gamma, stats, gy, gx, part);
         else
-          hipLaunchKernelGGL((k_ln_bwd_field<T, n.value, BV, false>), grid, block, f.lds, s,
-                             a, f.tiles, f.per_entry, x, gamma, stats, gy, gx, part);
+          hipLaunchKernelGGL((k_ln_bwd_field<T, n.value, kWide, false>), grid, block, f.lds, s, a,
+                             f.tiles, f.per_entry, x, gamma, stats, gy, gx, part);
       });
       break;
-    }
     // the column sums first: grad_x may overwrite x or grad_y
     case kLongRows:
       if (part)

@@ -20,15 +20,9 @@ __device__ __forceinline__ double group_sum(double v, double* s_red) {
   return s_red[0];
 }
 
-// A value that is the same in all lanes, in scalar registers.
-__device__ __forceinline__ uint32_t uniform(uint32_t v) {
-  return __builtin_amdgcn_readfirstlane(v);
-}
 template <typename T>
 __device__ __forceinline__ Global<T> data_of(const TensorTable& t, uint32_t k, int64_t at) {
-  const uint64_t v = reinterpret_cast<uint64_t>(t.entry[k].data);
-  const uint64_t u = (uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v);
-  return (Global<T>)u + at;
+  return (Global<T>)uniform(reinterpret_cast<int64_t>(t.entry[k].data)) + at;
 }
 
 // Calls f(entry number, first element, elements) for the spans of this work-group's share of the
@@ -41,8 +35,7 @@ __device__ __forceinline__ void each_span(const TensorTable& t, F&& f) {
   const uint32_t end = (uint32_t)(total * (blockIdx.x + 1) / gridDim.x);
   while (c < end) {
     const uint32_t k = uniform(t.of_chunk[c]), first = uniform(t.entry[k].first);
-    const int64_t elems = (int64_t)((uint64_t)uniform((uint32_t)(t.entry[k].elems >> 32)) << 32 |
-                                    uniform((uint32_t)t.entry[k].elems));
+    const int64_t elems = uniform(t.entry[k].elems);
     const int64_t at = (int64_t)(c - first) * kChunk;
     const uint32_t most = end - c < (1u << 28) / kChunk ? end - c : (1u << 28) / kChunk;
     const int64_t n = elems - at < most * kChunk ? elems - at : most * kChunk;
@@ -60,7 +53,7 @@ __device__ __forceinline__ double sum_squares(Global<const T> p, int n) {
   const int nv = n / V;
   int i = threadIdx.x;
   for (; i + (kAhead - 1) * kThreads < nv; i += kAhead * kThreads) {
-    Pack<T, V> q[kAhead];
+    Raw<T, V> q[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
       q[u] = load_global<T, V>(p + (i + u * kThreads) * V);
@@ -68,15 +61,15 @@ __device__ __forceinline__ double sum_squares(Global<const T> p, int n) {
     for (int u = 0; u < kAhead; ++u)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const double g = (double)to_float(q[u].v[e]);
+        const double g = (double)element<T, V>(q[u], e);
         a[u] += g * g;
       }
   }
   for (; i < nv; i += kThreads) {
-    const Pack<T, V> q = load_global<T, V>(p + i * V);
+    const Raw<T, V> q = load_global<T, V>(p + i * V);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const double g = (double)to_float(q.v[e]);
+      const double g = (double)element<T, V>(q, e);
       a[0] += g * g;
     }
   }
@@ -92,7 +85,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_part(TensorTable t, double* p
   __shared__ double s_red[kThreads];
   double a = 0.0;
   each_span(t, [&](uint32_t k, int64_t at, int n) {
-    const uint32_t d = uniform(t.entry[k].dtype);
+    const uint32_t d = uniform((uint32_t)t.entry[k].dtype);
     if (d == FNO_DTYPE_F32) a += sum_squares<float>(data_of<const float>(t, k, at), n);
     else if (d == FNO_DTYPE_BF16) a += sum_squares<__bf16>(data_of<const __bf16>(t, k, at), n);
     else a += sum_squares<_Float16>(data_of<const _Float16>(t, k, at), n);
@@ -122,7 +115,7 @@ __device__ __forceinline__ void scale_chunk(Global<const T> p, Global<U> o, int 
   constexpr int V = 16 / (int)sizeof(T);
   const int nv = n / V;
   int i = threadIdx.x;
-  const auto put = [&](const Pack<T, V>& q, int j) {
+  const auto put = [&](const Raw<T, V>& q, int j) {
     float g[V];
     unpack<T, V>(q, g);
 #pragma unroll
@@ -130,7 +123,7 @@ __device__ __forceinline__ void scale_chunk(Global<const T> p, Global<U> o, int 
     store_global<U, V>(o + j * V, g);
   };
   for (; i + (kAhead - 1) * kThreads < nv; i += kAhead * kThreads) {
-    Pack<T, V> q[kAhead];
+    Raw<T, V> q[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
       q[u] = load_global<T, V>(p + (i + u * kThreads) * V);
@@ -147,8 +140,8 @@ __global__ __launch_bounds__(kThreads) void k_clip(TensorTable t, TensorTable ou
   const float f = record[1];
   each_span(t, [&](uint32_t k, int64_t at, int n) {
     if (f == 1.0f && data_of<char>(t, k, 0) == data_of<char>(out, k, 0)) return;
-    const uint32_t d = uniform(t.entry[k].dtype);
-    const bool wide = uniform(out.entry[k].dtype) == FNO_DTYPE_F32;
+    const uint32_t d = uniform((uint32_t)t.entry[k].dtype);
+    const bool wide = uniform((uint32_t)out.entry[k].dtype) == FNO_DTYPE_F32;
     if (d == FNO_DTYPE_F32) {
       scale_chunk<float, float>(data_of<const float>(t, k, at), data_of<float>(out, k, at), n, f);
     } else if (d == FNO_DTYPE_BF16) {
@@ -175,20 +168,25 @@ template <typename T>
 __device__ __forceinline__ void adamw_chunk(Global<float> p, Global<const T> g, Global<float> m,
                                             Global<float> v, int n, const AdamArgs& a, float f) {
   constexpr int V = 4, kTwo = 2;
-  typedef Pack<float, V> Q;
+  typedef Raw<float, V> Q;
   const int nv = n / V;
   int i = threadIdx.x;
-  const auto put = [&](Q& qp, const Pack<T, V>& qg, Q& qm, Q& qv, int j) {
+  const auto put = [&](const Q& qp, const Raw<T, V>& qg, const Q& qm, const Q& qv, int j) {
+    float fp[V], fm[V], fv[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      adamw_one(qp.v[e], to_float(qg.v[e]), qm.v[e], qv.v[e], a, f);
-    store_global<float, V>(p + j, qp.v);
-    store_global<float, V>(m + j, qm.v);
-    store_global<float, V>(v + j, qv.v);
+    for (int e = 0; e < V; ++e) {
+      fp[e] = qp[e];
+      fm[e] = qm[e];
+      fv[e] = qv[e];
+      adamw_one(fp[e], to_float<T>(qg[e]), fm[e], fv[e], a, f);
+    }
+    store_global<float, V>(p + j, fp);
+    store_global<float, V>(m + j, fm);
+    store_global<float, V>(v + j, fv);
   };
   for (; i + (kTwo - 1) * kThreads < nv; i += kTwo * kThreads) {
     Q qp[kTwo], qm[kTwo], qv[kTwo];
-    Pack<T, V> qg[kTwo];
+    Raw<T, V> qg[kTwo];
 #pragma unroll
     for (int u = 0; u < kTwo; ++u) {
       const int j = (i + u * kThreads) * V;
@@ -202,9 +200,8 @@ __device__ __forceinline__ void adamw_chunk(Global<float> p, Global<const T> g, 
   }
   for (; i < nv; i += kThreads) {
     const int j = i * V;
-    Q qp = load_global<float, V>(p + j), qm = load_global<float, V>(m + j),
-      qv = load_global<float, V>(v + j);
-    put(qp, load_global<T, V>(g + j), qm, qv, j);
+    put(load_global<float, V>(p + j), load_global<T, V>(g + j), load_global<float, V>(m + j),
+        load_global<float, V>(v + j), j);
   }
   const int r = nv * V + threadIdx.x;
   if (r < n) {
@@ -222,7 +219,7 @@ __global__ __launch_bounds__(kThreads) void k_adamw(TensorTable params, TensorTa
   const float f = record ? record[1] : 1.0f;
   if (!(fabsf(f) < INFINITY)) return;  // the gradients were not finite: no update
   each_span(params, [&](uint32_t k, int64_t at, int n) {
-    const uint32_t d = uniform(grads.entry[k].dtype);
+    const uint32_t d = uniform((uint32_t)grads.entry[k].dtype);
     const Global<float> p = data_of<float>(params, k, at);
     const Global<float> m = data_of<float>(exp_avg, k, at);
     const Global<float> v = data_of<float>(exp_avg_sq, k, at);

@@ -21,21 +21,63 @@ __device__ __forceinline__ T from_float(float v) {
 // bytes: the global memory instructions take 16 bytes at any address (gfx950 runs in unaligned
 // access mode), so odd row lengths and views need no code of their own.
 template <typename T, int N>
-struct __attribute__((packed, aligned(sizeof(T)))) Pack {
-  T v[N];
+struct RawVector {
+  typedef T type __attribute__((ext_vector_type(N)));
+  typedef type unaligned __attribute__((aligned(sizeof(T))));
+};
+template <typename T>
+struct RawVector<T, 1> {
+  typedef T type;
+  typedef T unaligned;
 };
 template <typename T, int N>
-__device__ __forceinline__ void load_pack(const T* p, float (&f)[N]) {
-  const Pack<T, N> q = *reinterpret_cast<const Pack<T, N>*>(p);
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = to_float(q.v[i]);
+using Raw = typename RawVector<T, N>::type;
+
+template <typename T, int N>
+__device__ __forceinline__ float element(const Raw<T, N>& q, int i) {
+  if constexpr (N == 1) return to_float(q);
+  else return to_float<T>(q[i]);
 }
 template <typename T, int N>
-__device__ __forceinline__ void store_pack(T* p, const float (&f)[N]) {
-  Pack<T, N> q;
+__device__ __forceinline__ void unpack(const Raw<T, N>& q, float (&f)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) q.v[i] = from_float<T>(f[i]);
-  *reinterpret_cast<Pack<T, N>*>(p) = q;
+  for (int i = 0; i < N; ++i) f[i] = element<T, N>(q, i);
+}
+template <typename T, int N>
+__device__ __forceinline__ Raw<T, N> pack(const float* f) {
+  Raw<T, N> q;
+  if constexpr (N == 1) {
+    q = from_float<T>(f[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = from_float<T>(f[i]);
+  }
+  return q;
+}
+
+// Fields that are read or written once go past the caches (nontemporal) where `Stream`.
+template <typename T, int N, bool Stream = false>
+__device__ __forceinline__ Raw<T, N> load_raw(const T* p) {
+  typedef typename RawVector<T, N>::unaligned V;
+  if constexpr (Stream) return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+  else return *reinterpret_cast<const V*>(p);
+}
+template <typename T, int N>
+__device__ __forceinline__ void load_pack(const T* p, float (&f)[N]) {
+  unpack<T, N>(load_raw<T, N>(p), f);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_pack(T* p, const float (&f)[N], bool stream = false) {
+  typedef typename RawVector<T, N>::unaligned V;
+  const V q = pack<T, N>(f);
+  if (stream) {
+    // the empty statements keep the compiler from folding the two stores into a plain one
+    asm volatile("");
+    __builtin_nontemporal_store(q, reinterpret_cast<V*>(p));
+    asm volatile("");
+  } else {
+    *reinterpret_cast<V*>(p) = q;
+  }
 }
 
 // The same through pointers that the compiler cannot tell to be global (they come out of memory):
@@ -43,36 +85,24 @@ __device__ __forceinline__ void store_pack(T* p, const float (&f)[N]) {
 template <typename T>
 using Global = T __attribute__((address_space(1)))*;
 template <typename T, int N>
-struct RawVector {
-  typedef T type __attribute__((ext_vector_type(N)));
-  typedef type unaligned __attribute__((aligned(sizeof(T))));
-};
-template <typename T, int N>
-__device__ __forceinline__ Pack<T, N> load_global(Global<const T> p) {
+__device__ __forceinline__ Raw<T, N> load_global(Global<const T> p) {
   typedef typename RawVector<T, N>::unaligned V;
-  const V v = *(Global<const V>)p;
-  Pack<T, N> q;
-#pragma unroll
-  for (int i = 0; i < N; ++i) q.v[i] = v[i];
-  return q;
+  return *(Global<const V>)p;
 }
 template <typename T, int N>
 __device__ __forceinline__ void store_global(Global<T> p, const float (&f)[N]) {
   constexpr int M = N * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : N;
   typedef typename RawVector<T, M>::unaligned V;
 #pragma unroll
-  for (int k = 0; k < N; k += M) {
-    V v;
-#pragma unroll
-    for (int i = 0; i < M; ++i) v[i] = from_float<T>(f[k + i]);
-    *(Global<V>)(p + k) = v;
-  }
+  for (int k = 0; k < N; k += M) *(Global<V>)(p + k) = pack<T, M>(f + k);
 }
 
-template <typename T, int N>
-__device__ __forceinline__ void unpack(const Pack<T, N>& q, float (&f)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = to_float(q.v[i]);
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return __builtin_amdgcn_readfirstlane(v);
+}
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)uniform((uint32_t)((uint64_t)v >> 32)) << 32 | uniform((uint32_t)v));
 }
 
 // ---- sums over lanes ---------------------------------------------------------------------------

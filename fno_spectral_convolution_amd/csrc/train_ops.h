@@ -15,6 +15,7 @@ struct NormArgs {
   int channels;
   int64_t x_stride, y_stride, gx_stride;  // elements between batch entries
   float eps;
+  bool stream;  // the output goes past the caches (set by the launches)
 };
 hipError_t launch_layer_norm_fwd(const NormArgs& a, int dtype, const void* x, const float* gamma,
                                  const float* beta, void* y, float* stats, hipStream_t s);
