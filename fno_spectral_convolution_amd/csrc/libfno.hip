@@ -1885,8 +1885,10 @@ size_t norm_parts_bytes(const fno_tensor_list* l) {
   return align_up(sizeof(double) * (size_t)std::max(norm_groups(l), 1));
 }
 
-fno_status grad_norm_impl(const fno_tensor_list* grads, float max_norm, float grad_scale,
-                          float* record, void* ws, size_t ws_bytes, hipStream_t s) {
+// Checks of the norm's arguments, and the partial sums into the workspace.
+fno_status norm_parts(const fno_tensor_list* grads, float max_norm, float grad_scale,
+                      const float* record, void* ws, size_t ws_bytes, hipStream_t s,
+                      fno::NormRecord* r) {
   if (!(max_norm > 0.0f)) return fail(FNO_ERR_INVALID_ARGUMENT, "max_norm must be > 0");
   if (!(grad_scale > 0.0f) || !std::isfinite(grad_scale))
     return fail(FNO_ERR_INVALID_ARGUMENT, "grad_scale must be finite and > 0");
@@ -1894,12 +1896,20 @@ fno_status grad_norm_impl(const fno_tensor_list* grads, float max_norm, float gr
   REQ(ws, "workspace");
   if (ws_bytes < norm_parts_bytes(grads))
     return fail(FNO_ERR_INVALID_ARGUMENT, "workspace too small");
-  double* part = static_cast<double*>(ws);
-  const int groups = norm_groups(grads);
-  if (groups > 0)
-    LAUNCH("grad_norm", s, fno::launch_norm_part(grads->table, groups, part, s));
+  *r = {norm_groups(grads), max_norm, grad_scale};
+  if (r->nparts > 0)
+    LAUNCH("grad_norm", s,
+           fno::launch_norm_part(grads->table, r->nparts, static_cast<double*>(ws), s));
+  return FNO_OK;
+}
+
+fno_status finish_norm(const fno_tensor_list* grads, float max_norm, float grad_scale,
+                       float* record, void* ws, size_t ws_bytes, hipStream_t s) {
+  fno::NormRecord r;
+  const fno_status st = norm_parts(grads, max_norm, grad_scale, record, ws, ws_bytes, s, &r);
+  if (st != FNO_OK) return st;
   LAUNCH("grad_norm_finish", s,
-         fno::launch_norm_finish(part, groups, max_norm, grad_scale, record, s));
+         fno::launch_norm_finish(static_cast<const double*>(ws), r, record, s));
   return FNO_OK;
 }
 
@@ -2018,6 +2028,9 @@ fno_status fno_tensor_list_create(int64_t count, const fno_tensor* tensors, void
   l->table.entry = static_cast<const fno::TensorEntry*>(table);
   l->table.of_chunk = reinterpret_cast<const uint32_t*>(l->table.entry + count);
   l->table.chunks = (uint32_t)chunks;
+  l->table.bytes = 0;
+  for (int64_t i = 0; i < count; ++i)
+    l->table.bytes += tensors[i].elems * (int64_t)dtype_bytes(tensors[i].dtype);
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
   hipError_t e = hipGetDevice(&l->device);
@@ -2052,8 +2065,8 @@ fno_status fno_grad_norm(const fno_tensor_list* grads, float max_norm, float gra
                          float* record, void* ws, size_t ws_bytes, void* stream) {
   const fno_status st = check_list(grads, "grads");
   if (st != FNO_OK) return st;
-  return grad_norm_impl(grads, max_norm, grad_scale, record, ws, ws_bytes,
-                        static_cast<hipStream_t>(stream));
+  return finish_norm(grads, max_norm, grad_scale, record, ws, ws_bytes,
+                     static_cast<hipStream_t>(stream));
 }
 
 fno_status fno_clip_grad_norm(const fno_tensor_list* grads, const fno_tensor_list* out,
@@ -2070,9 +2083,13 @@ fno_status fno_clip_grad_norm(const fno_tensor_list* grads, const fno_tensor_lis
                   (long long)i);
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
-  st = grad_norm_impl(grads, max_norm, grad_scale, record, ws, ws_bytes, s);
-  if (st != FNO_OK || grads->table.chunks == 0) return st;
-  LAUNCH("grad_clip", s, fno::launch_clip(grads->table, out->table, record, s));
+  if (grads->table.chunks == 0)
+    return finish_norm(grads, max_norm, grad_scale, record, ws, ws_bytes, s);
+  fno::NormRecord r;
+  st = norm_parts(grads, max_norm, grad_scale, record, ws, ws_bytes, s, &r);
+  if (st != FNO_OK) return st;
+  LAUNCH("grad_clip", s,
+         fno::launch_clip(grads->table, out->table, static_cast<const double*>(ws), r, record, s));
   return FNO_OK;
 }
 

@@ -90,11 +90,20 @@ __device__ __forceinline__ Raw<T, N> load_global(Global<const T> p) {
   return *(Global<const V>)p;
 }
 template <typename T, int N>
-__device__ __forceinline__ void store_global(Global<T> p, const float (&f)[N]) {
+__device__ __forceinline__ void store_global(Global<T> p, const float (&f)[N], bool stream) {
   constexpr int M = N * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : N;
   typedef typename RawVector<T, M>::unaligned V;
 #pragma unroll
-  for (int k = 0; k < N; k += M) *(Global<V>)(p + k) = pack<T, M>(f + k);
+  for (int k = 0; k < N; k += M) {
+    const V q = pack<T, M>(f + k);
+    if (stream) {
+      asm volatile("");  // as in store_pack
+      __builtin_nontemporal_store(q, (Global<V>)(p + k));
+      asm volatile("");
+    } else {
+      *(Global<V>)(p + k) = q;
+    }
+  }
 }
 
 // A value that is the same in all lanes, in scalar registers.
@@ -130,6 +139,11 @@ __device__ __forceinline__ float lane_sum(float v) {
   if (N >= 16) v += dpp<0x140>(v);
   if (N >= 32) v = add_across<16>(v);
   if (N >= 64) v = add_across<32>(v);
+  return v;
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
   return v;
 }
 // Sum over the lanes of a wave that share lane % N (N = 8, 16, 32; 64: v itself).

@@ -42,16 +42,23 @@ struct TensorTable {
   const TensorEntry* entry;
   const uint32_t* of_chunk;
   uint32_t chunks;
+  int64_t bytes;  // of all its tensors
 };
-// partial sums of the norm: a work-group's registers allow four to a compute unit
-constexpr int kNormParts = 1024;
+// how the partial sums of squares become a record
+struct NormRecord {
+  int nparts;
+  float max_norm, grad_scale;
+};
+// most partial sums of the norm: eight work-groups of four waves fill a compute unit
+constexpr int kNormParts = 2048;
 
 // one partial sum of squares per work-group into part[0 .. groups)
 hipError_t launch_norm_part(const TensorTable& t, int groups, double* part, hipStream_t s);
-hipError_t launch_norm_finish(const double* part, int nparts, float max_norm, float grad_scale,
-                              float* record, hipStream_t s);
-hipError_t launch_clip(const TensorTable& t, const TensorTable& out, const float* record,
-                       hipStream_t s);
+hipError_t launch_norm_finish(const double* part, const NormRecord& r, float* record,
+                              hipStream_t s);
+// writes the record too
+hipError_t launch_clip(const TensorTable& t, const TensorTable& out, const double* part,
+                       const NormRecord& r, float* record, hipStream_t s);
 
 struct AdamArgs {
   float beta1, beta2, one_minus_beta1, one_minus_beta2;
