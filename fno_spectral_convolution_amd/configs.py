@@ -30,6 +30,8 @@ class Workload:
     input_kind: str = "grf"       # grf | normal | grf_coords | grf_layered
     tucker_ranks: Optional[Tuple[int, ...]] = None  # Tucker-factorised spectral weights
                                   # (TFNO): ranks R_in, R_out, R_0..R_{d-1}
+    norm: bool = False            # layer norm over the channels between blocks, each point's own:
+                                  # block i > 0 reads GELU(norm(z_{i-1}))
     notes: str = ""
 
     @property

@@ -7,7 +7,7 @@ the other through it.  Every array is generated on the host in float64 from
 so the GPU and the oracle receive byte-identical values.
 
 Streams: 0 input field, 1 spectral weights, 2 bypass weights, 3 bias, 4 target field,
-5 lift/projection weights, 6 permeability layers, 7 Tucker core and factors.
+5 lift/projection weights, 6 permeability layers, 7 Tucker core and factors, 8 norm weights.
 
 The pages' datasets (CO2 plume simulations, the mixed-precision study's PDE datasets) are
 not available; these fields stand in for them with the same shapes:
@@ -23,7 +23,7 @@ import numpy as np
 import scipy.fft as _sfft
 
 (STREAM_INPUT, STREAM_W, STREAM_WB, STREAM_BIAS, STREAM_TARGET, STREAM_PROJ, STREAM_LAYERS,
- STREAM_TUCKER) = range(8)
+ STREAM_TUCKER, STREAM_NORM) = range(9)
 
 
 def rng(cfg_id: int, stream: int, index: int = 0) -> np.random.Generator:
@@ -152,9 +152,16 @@ def tucker_params(w, block: int = 0, cin=None, cout=None, modes=None, ranks=None
     return core.astype(np.complex64), factors
 
 
+def norm_params(w, block: int = 0):
+    """Weight [C] ~ N(1, 0.1^2) and bias [C] ~ N(0, 0.1^2) of the layer norm before a block."""
+    g = rng(w.cfg_id, STREAM_NORM, block)
+    return 1.0 + normal(g, w.width, 0.1), normal(g, w.width, 0.1)
+
+
 def block_params(w, n_blocks=None):
     """Per-block parameter dicts for ``n_blocks`` blocks: (w, wb, bias), or (core, factors,
-    wb, bias) for workloads with Tucker-factorised spectral weights."""
+    wb, bias) for workloads with Tucker-factorised spectral weights; with a layer norm between
+    blocks also (gamma, beta) for every block but the first."""
     n = w.blocks if n_blocks is None else n_blocks
     out = []
     for i in range(n):
@@ -163,6 +170,8 @@ def block_params(w, n_blocks=None):
             blk["core"], blk["factors"] = tucker_params(w, i)
         else:
             blk["w"] = spectral_weights(w, i)
+        if getattr(w, "norm", False) and i > 0:
+            blk["gamma"], blk["beta"] = norm_params(w, i)
         out.append(blk)
     return out
 

@@ -4,8 +4,12 @@
 the spectral blocks (GELU after each), an optional projection head, and for training
 workloads the MSE loss against a target and the backward through every block (input,
 spectral-weight, bypass-weight and bias gradients).  Workloads with Tucker ranks hold each
-block's spectral weight as a Tucker core and factors (TFNO) and run the Tucker entry points.  Torch provides device memory and the
-stream; all arithmetic runs in libfno's kernels.
+block's spectral weight as a Tucker core and factors (TFNO) and run the Tucker entry points.
+Workloads with ``norm`` take a layer norm over the channels between blocks, with its gradients.
+Torch provides device memory and the stream; all arithmetic runs in libfno's kernels.
+
+``StackRunner.parameters()`` and ``gradients()`` list what a step trains and what it returns, in
+one order: ``optim.AdamW`` clips and updates by them.
 
 ``PrecisionSchedule`` with ``StackRunner.run`` moves a training run from a half-precision
 spectral path to fp32 at a chosen step (precision scheduling, mixed-precision neural-operator
@@ -110,8 +114,18 @@ class StackRunner:
                     gr["factors"] = [torch.empty_like(u) for u in p["factors"]]
                 else:
                     gr["w"] = torch.empty_like(p["w"])
+                for k in ("gamma", "beta"):
+                    if k in p:
+                        gr[k] = torch.empty_like(p[k])
                 self.grads.append(gr)
             self.loss = torch.empty(1, dtype=torch.float32, device=dev)
+            if wl.norm:
+                # block i > 0 reads normed[i]; its norm's backward reads acts[i] and norm_stats[i]
+                self.normed = [None] + [torch.empty(shape, dtype=torch.float32, device=dev)
+                                        for _ in range(1, nb)]
+                self.norm_stats = [None] + [
+                    torch.empty((2, wl.batch) + tuple(wl.grid), dtype=torch.float32, device=dev)
+                    for _ in range(1, nb)]
             self.mse_ws = torch.empty(max(L.fno_mse_workspace_bytes(self.acts[-1].numel()), 16),
                                       dtype=torch.uint8, device=dev)
         else:
@@ -125,9 +139,10 @@ class StackRunner:
         """(input GELU, output GELU) of block i.  A training stack moves the GELU between two
         blocks to the start of the later one: each inner block then keeps only its
         pre-activation z, and its backward reads z and the incoming gradient once instead of
-        twice.  The network, its outputs and its gradients are those of the plain stack."""
+        twice.  The network, its outputs and its gradients are those of the plain stack.  A
+        stack with norms does so always: they go between a block's z and the next one's GELU."""
         nb = self.wl.blocks
-        if not self.wl.train or nb == 1:
+        if nb == 1 or not (self.wl.train or self.wl.norm):
             return (False, True)
         return (i > 0, i == nb - 1)
 
@@ -191,6 +206,34 @@ class StackRunner:
         or its plan."""
         return self.block_tuckers[i] if self.tucker else self.block_plans[i]
 
+    def parameters(self):
+        """What a training step trains: per block the spectral weight (or core and factors), the
+        bypass, the bias and the norm's weight and bias, as they are updated in place."""
+        return self._listed(self.params)
+
+    def gradients(self):
+        """The gradients that step() fills (times grad_scale), as parameters() lists them."""
+        return self._listed(self.grads)
+
+    @staticmethod
+    def _listed(blocks):
+        out = []
+        for b in blocks:
+            for k in ("w", "core", "factors", "wb", "bias", "gamma", "beta"):
+                if k in b:
+                    out += b[k] if k == "factors" else [b[k]]
+        return out
+
+    def _norm(self, i, h):
+        """The layer norm in front of block i > 0."""
+        p = self.params[i]
+        if self.wl.train:
+            L.layer_norm_fwd(h, p["gamma"], p["beta"], out=self.normed[i],
+                             stats=self.norm_stats[i])
+            return self.normed[i]
+        L.layer_norm_fwd(h, p["gamma"], p["beta"], out=h, want_stats=False)
+        return h
+
     def _act(self, i):
         return self.acts[i] if self.wl.train else self.acts[i % 2]
 
@@ -208,6 +251,8 @@ class StackRunner:
         nb = len(self.params)
         for i, p in enumerate(self.params):
             dst = self._act(i + 1)
+            if wl.norm and i > 0:
+                h = self._norm(i, h)
             if self.fuse_loss and i == nb - 1:
                 # loss and the gradient at the last pre-activation, into g[0]; y is not stored
                 if self.tucker:
@@ -238,7 +283,7 @@ class StackRunner:
             gin = 0
             for i in reversed(range(len(self.params))):
                 p = self.params[i]
-                x_i = src0 if i == 0 else self.acts[i]
+                x_i = src0 if i == 0 else self.normed[i] if wl.norm else self.acts[i]
                 gout = 1 - gin
                 if self.fuse_loss and i == nb - 1:
                     if self.tucker:
@@ -257,6 +302,10 @@ class StackRunner:
                     self.block_plans[i].block_bwd(x_i, p["w"], p["wb"], p["bias"], self.saves[i],
                                                   self.g[gin],
                                                   out={"x": self.g[gout], **self.grads[i]})
+                if wl.norm and i > 0:  # from the gradient at its output to that at its input
+                    L.layer_norm_bwd(self.acts[i], p["gamma"], self.norm_stats[i], self.g[gout],
+                                     out={"x": self.g[gout], "gamma": self.grads[i]["gamma"],
+                                          "beta": self.grads[i]["beta"]})
                 gin = gout
             self.grad_x = self.g[gin]
         return h
