@@ -10,6 +10,7 @@ importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from ctypes import (POINTER, byref, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t,
                     c_uint32, c_void_p)
@@ -803,68 +804,80 @@ _KINDS = {_torch.float32: FNO_DTYPE_F32, _torch.bfloat16: FNO_DTYPE_BF16,
 _LIST_KINDS = {**_KINDS, _torch.complex64: FNO_DTYPE_F32}  # as pairs of float32
 
 
-def _kind(t, kinds):
-    k = kinds.get(t.dtype)
-    if k is None:
-        raise ValueError(f"float32, bfloat16 or float16 data expected, not {t.dtype}")
-    return k
-
-
-# The handle of a device's current stream, without the Stream object that the public call makes
-# (0.1 us against 1.9, next to 3.3 for a launch); the public call where torch has no such function.
+# The handle of a device's current stream and the current device, without the Stream object and the
+# set-up check of the public calls (0.1 us each against 1.9 and 0.3, next to 3.3 for a launch); the
+# public calls where torch has no such functions.
 _stream_handle = getattr(_torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: _torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(_torch._C, "_cuda_getDevice", None) or _torch.cuda.current_device
 
 
-def _on_stream(device, fn, *args):
-    """fn(*args, current stream of `device`), with the device current."""
-    current = _torch.cuda.current_device()
-    index = current if device.index is None else device.index
-    if index == current:
+def _on_stream(index, fn, *args):
+    """fn(*args, current stream of device `index`), with that device current."""
+    if index == _current_device():
         return fn(*args, _stream_handle(index))
     with _torch.cuda.device(index):
         return fn(*args, _stream_handle(index))
 
 
-def _batch_stride(t, packed, name):
-    """Elements between the batch entries of a field whose entries, `packed` elements, are packed."""
-    if t.is_contiguous():
-        return packed
-    if t.shape[0] and not t[0].is_contiguous():
-        raise ValueError(f"{name}: its batch entries must be packed (call .contiguous())")
-    return t.stride(0)
-
-
-def _like_x(t, x, name):
-    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
-        raise ValueError(f"{name}: needs x's shape, dtype and device, {tuple(x.shape)} "
-                         f"{x.dtype} on {x.device}")
-    return t
-
-
-def _vector(t, shape, device, name):
-    """The address of packed float32 values of a shape (None: none given)."""
+def _vector(t, shape, index, name):
+    """The address of packed float32 values of a shape on device `index` (None: none given)."""
     if t is None:
         return None
-    if t.dtype != _torch.float32 or t.shape != shape or t.device != device \
+    if t.dtype != _torch.float32 or t.shape != shape or t.get_device() != index \
             or not t.is_contiguous():
-        raise ValueError(f"{name}: needs packed float32 {tuple(shape)} on {device}")
+        raise ValueError(f"{name}: needs packed float32 {tuple(shape)} on cuda:{index}")
     return t.data_ptr()
 
 
-def _norm_desc(x, eps):
-    shape = x.shape
-    if len(shape) < 2:
-        raise ValueError("layer norm: x is [batch, channels, *grid]")
-    npts = 1
-    for n in shape[2:]:
-        npts *= n
-    packed = shape[1] * npts
-    d = fno_layer_norm_desc(_kind(x, _KINDS), 0, shape[0], shape[1], npts,
-                            _batch_stride(x, packed, "x"), packed, packed, eps)
-    if not x.is_cuda:
+class _NormShape:
+    """What a layer norm call needs to know of the shapes and strides of its fields: worked out
+    once for each combination, as a plan's is."""
+
+    def __init__(self, dtype, shape, x_stride, y_stride, gx_stride, eps):
+        if len(shape) < 2:
+            raise ValueError("layer norm: x is [batch, channels, *grid]")
+        if dtype not in _KINDS:
+            raise ValueError(f"float32, bfloat16 or float16 data expected, not {dtype}")
+        npts = 1
+        for n in shape[2:]:
+            npts *= n
+        batch = [self._batch_stride(shape, st, name) for st, name in
+                 ((x_stride, "x"), (y_stride, "y or grad_y"), (gx_stride, "grad_x"))]
+        self.desc = fno_layer_norm_desc(_KINDS[dtype], 0, shape[0], shape[1], npts, *batch, eps)
+        self.ptr = byref(self.desc)
+        self.channels = shape[1:2]
+        self.stats = (2, shape[0]) + shape[2:]
+        self.ws_bytes = max(fno_layer_norm_workspace_bytes(self.desc), 16)
+
+    @staticmethod
+    def _batch_stride(shape, stride, name):
+        """Elements between the batch entries of a field whose entries have to be packed."""
+        packed = 1
+        if 0 not in shape:
+            for n, st in zip(shape[:0:-1], stride[:0:-1]):
+                if n != 1 and st != packed:
+                    raise ValueError(f"{name}: its batch entries must be packed "
+                                     "(call .contiguous())")
+                packed *= n
+        return stride[0] if shape[0] > 1 else packed
+
+
+_norm_shape = functools.lru_cache(maxsize=256)(_NormShape)
+
+
+def _on_gpu(x):
+    index = x.get_device()
+    if index < 0:
         raise ValueError(f"tensors on the GPU expected, not on {x.device}")
-    return d, packed
+    return index
+
+
+def _like_x(t, x, name):
+    if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != x.get_device():
+        raise ValueError(f"{name}: needs x's shape, dtype and device, {tuple(x.shape)} "
+                         f"{x.dtype} on {x.device}")
+    return t.stride()
 
 
 def layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, out=None, stats=None, want_stats=True):
@@ -872,19 +885,20 @@ def layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, out=None, stats=None, wan
     row), times gamma plus beta (float32 [C]; None: 1 and 0).  Returns (y, stats); stats, float32
     [2, B, *grid], holds the means and the reciprocal deviations for layer_norm_bwd (None without
     want_stats)."""
-    d, packed = _norm_desc(x, eps)
-    device, shape = x.device, x.shape
+    strides = x.stride()
     if out is None:
-        out = x.new_empty(shape)
+        out = x.new_empty(x.shape)
+        y_strides = out.stride()
     else:
-        d.y_stride = _batch_stride(_like_x(out, x, "out"), packed, "out")
-    of_stats = (2, shape[0]) + shape[2:]
+        y_strides = _like_x(out, x, "out")
+    n = _norm_shape(x.dtype, x.shape, strides, y_strides, y_strides, eps)
+    index = _on_gpu(x)
     if stats is None and want_stats:
-        stats = x.new_empty(of_stats, dtype=_torch.float32)
-    _on_stream(device, fno_layer_norm_fwd, d, x.data_ptr(),
-               _vector(gamma, shape[1:2], device, "gamma"),
-               _vector(beta, shape[1:2], device, "beta"), out.data_ptr(),
-               _vector(stats, of_stats, device, "stats"))
+        stats = x.new_empty(n.stats, dtype=_torch.float32)
+    _check(_on_stream(index, _lib.fno_layer_norm_fwd, n.ptr, x.data_ptr(),
+                      _vector(gamma, n.channels, index, "gamma"),
+                      _vector(beta, n.channels, index, "beta"), out.data_ptr(),
+                      _vector(stats, n.stats, index, "stats")), "fno_layer_norm_fwd")
     return out, stats
 
 
@@ -892,30 +906,23 @@ def layer_norm_bwd(x, gamma, stats, grad_y, want=("x", "gamma", "beta"), out=Non
     """Gradients of layer_norm_fwd from its x and stats: dict(x, gamma, beta), None where not
     asked.  out: tensors to write instead of new ones (out["x"] may be grad_y itself).  ws: uint8
     workspace of fno_layer_norm_workspace_bytes (allocated when None)."""
-    d, packed = _norm_desc(x, 0.0)
-    device, shape = x.device, x.shape
-    d.y_stride = _batch_stride(_like_x(grad_y, x, "grad_y"), packed, "grad_y")
-    channels = shape[1:2]
-    got = {}
-    for k in ("x", "gamma", "beta"):
-        if out is not None and k in out:
-            got[k] = out[k]
-        elif k not in want:
-            got[k] = None
-        else:
-            got[k] = x.new_empty(shape) if k == "x" else x.new_empty(channels,
-                                                                    dtype=_torch.float32)
-    gx = got["x"]
-    if gx is not None:
-        d.grad_x_stride = _batch_stride(_like_x(gx, x, "grad_x"), packed, "grad_x")
-    gamma, gg, gb = (_vector(t, channels, device, name) for t, name in
-                     ((gamma, "gamma"), (got["gamma"], "grad_gamma"), (got["beta"], "grad_beta")))
-    stats = _vector(stats, (2, shape[0]) + shape[2:], device, "stats")
-    if ws is None and not (gg is None and gb is None):
-        ws = x.new_empty(max(fno_layer_norm_workspace_bytes(d), 16), dtype=_torch.uint8)
-    _on_stream(device, fno_layer_norm_bwd, d, x.data_ptr(), gamma, stats, grad_y.data_ptr(),
-               _ptr(gx), gg, gb, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
-    return got
+    gy_strides = _like_x(grad_y, x, "grad_y")
+    o = out or {}
+    gx = o["x"] if "x" in o else x.new_empty(x.shape) if "x" in want else None
+    n = _norm_shape(x.dtype, x.shape, x.stride(), gy_strides,
+                    gy_strides if gx is None else _like_x(gx, x, "grad_x"), 0.0)
+    index = _on_gpu(x)
+    gg, gb = (o[k] if k in o else x.new_empty(n.channels, dtype=_torch.float32) if k in want
+              else None for k in ("gamma", "beta"))
+    if ws is None:
+        ws = x.new_empty(n.ws_bytes, dtype=_torch.uint8)
+    _check(_on_stream(index, _lib.fno_layer_norm_bwd, n.ptr, x.data_ptr(),
+                      _vector(gamma, n.channels, index, "gamma"),
+                      _vector(stats, n.stats, index, "stats"), grad_y.data_ptr(), _ptr(gx),
+                      _vector(gg, n.channels, index, "grad_gamma"),
+                      _vector(gb, n.channels, index, "grad_beta"), ws.data_ptr(),
+                      ws.numel() * ws.element_size()), "fno_layer_norm_bwd")
+    return {"x": gx, "gamma": gg, "beta": gb}
 
 
 class TensorList:
@@ -929,14 +936,18 @@ class TensorList:
         self.tensors = list(tensors)
         self.device = self.tensors[0].device if self.tensors else \
             _torch.device("cuda", _torch.cuda.current_device())
+        self.index = _torch.cuda.current_device() if self.device.index is None and \
+            self.device.type == "cuda" else self.device.index
         entries = (fno_tensor * max(len(self.tensors), 1))()
         for i, t in enumerate(self.tensors):
             if not t.is_contiguous() or t.is_conj() or t.is_neg():
                 raise ValueError(f"tensor {i} of the list is not packed (call .contiguous())")
             if t.device != self.device or not t.is_cuda:
                 raise ValueError("the tensors of a list are on one GPU")
+            if t.dtype not in _LIST_KINDS:
+                raise ValueError(f"float32, bfloat16 or float16 data expected, not {t.dtype}")
             e = entries[i]
-            e.data, e.dtype = t.data_ptr(), _kind(t, _LIST_KINDS)
+            e.data, e.dtype = t.data_ptr(), _LIST_KINDS[t.dtype]
             e.elems = 2 * t.numel() if t.is_complex() else t.numel()
         count = len(self.tensors)
         ptr = ctypes.addressof(entries)
@@ -947,7 +958,7 @@ class TensorList:
             return fno_tensor_list_create(count, ptr, self.table.data_ptr(), self.table.numel(),
                                           stream)
 
-        self.handle = _on_stream(self.device, create)
+        self.handle = _on_stream(self.index, create)
         self.norm_ws_bytes = fno_grad_norm_workspace_bytes(self.handle)
 
     def __len__(self):
@@ -972,14 +983,16 @@ def _tensor_list(ts):
 def _norm_buffers(gl, record, ws):
     if record is None:
         record = gl.table.new_empty(2, dtype=_torch.float32)
-    elif record.device != gl.device or record.numel() != 2 or record.dtype != _torch.float32 \
-            or not record.is_contiguous():
-        raise ValueError(f"record: needs two packed float32 on {gl.device}")
+    else:
+        _vector(record, _RECORD, gl.index, "record")
     if ws is None:
         ws = gl.table.new_empty(gl.norm_ws_bytes)
-    elif ws.device != gl.device or not ws.is_contiguous():
+    elif ws.get_device() != gl.index or not ws.is_contiguous():
         raise ValueError(f"ws: needs packed memory on {gl.device}")
     return record, ws
+
+
+_RECORD = _torch.Size([2])
 
 
 def grad_norm(grads, max_norm=float("inf"), grad_scale=1.0, record=None, ws=None):
@@ -988,8 +1001,9 @@ def grad_norm(grads, max_norm=float("inf"), grad_scale=1.0, record=None, ws=None
     fno_grad_norm)."""
     gl = _tensor_list(grads)
     record, ws = _norm_buffers(gl, record, ws)
-    _on_stream(gl.device, fno_grad_norm, gl.handle, max_norm, grad_scale, record.data_ptr(),
-               ws.data_ptr(), ws.numel() * ws.element_size())
+    _check(_on_stream(gl.index, _lib.fno_grad_norm, gl.handle, max_norm, grad_scale,
+                      record.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size()),
+           "fno_grad_norm")
     return record
 
 
@@ -999,8 +1013,9 @@ def clip_grad_norm(grads, max_norm, grad_scale=1.0, out=None, record=None, ws=No
     gl = _tensor_list(grads)
     ol = gl if out is None else _tensor_list(out)
     record, ws = _norm_buffers(gl, record, ws)
-    _on_stream(gl.device, fno_clip_grad_norm, gl.handle, ol.handle, max_norm, grad_scale,
-               record.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    _check(_on_stream(gl.index, _lib.fno_clip_grad_norm, gl.handle, ol.handle, max_norm,
+                      grad_scale, record.data_ptr(), ws.data_ptr(),
+                      ws.numel() * ws.element_size()), "fno_clip_grad_norm")
     return record
 
 
@@ -1009,9 +1024,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps=
     """One AdamW update, number `step` (from 1), of float32 (or complex64, as pairs) parameters in
     place, from gradients times the factor of `record` (grad_norm's; None: as they are).  A factor
     that is not finite leaves parameters and moments as they are."""
-    pl, gl, ml, vl = (_tensor_list(t) for t in (params, grads, exp_avg, exp_avg_sq))
+    pl, gl, ml, vl = (_tensor_list(params), _tensor_list(grads), _tensor_list(exp_avg),
+                      _tensor_list(exp_avg_sq))
     d = fno_adamw_desc(lr, betas[0], betas[1], eps, weight_decay, step)
-    if record is not None and (record.device != pl.device or record.numel() != 2
-                               or record.dtype != _torch.float32 or not record.is_contiguous()):
-        raise ValueError(f"record: needs two packed float32 on {pl.device}")
-    _on_stream(pl.device, fno_adamw, pl.handle, gl.handle, ml.handle, vl.handle, d, _ptr(record))
+    _check(_on_stream(pl.index, _lib.fno_adamw, pl.handle, gl.handle, ml.handle, vl.handle,
+                      byref(d), _vector(record, _RECORD, pl.index, "record")), "fno_adamw")
