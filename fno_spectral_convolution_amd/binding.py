@@ -848,7 +848,7 @@ class _NormShape:
         self.ptr = byref(self.desc)
         self.channels = shape[1:2]
         self.stats = (2, shape[0]) + shape[2:]
-        self.ws_bytes = max(fno_layer_norm_workspace_bytes(self.desc), 16)
+        self.ws_bytes = fno_layer_norm_workspace_bytes(self.desc)
 
     @staticmethod
     def _batch_stride(shape, stride, name):
@@ -914,14 +914,14 @@ def layer_norm_bwd(x, gamma, stats, grad_y, want=("x", "gamma", "beta"), out=Non
     index = _on_gpu(x)
     gg, gb = (o[k] if k in o else x.new_empty(n.channels, dtype=_torch.float32) if k in want
               else None for k in ("gamma", "beta"))
-    if ws is None:
+    if ws is None and n.ws_bytes:
         ws = x.new_empty(n.ws_bytes, dtype=_torch.uint8)
     _check(_on_stream(index, _lib.fno_layer_norm_bwd, n.ptr, x.data_ptr(),
                       _vector(gamma, n.channels, index, "gamma"),
                       _vector(stats, n.stats, index, "stats"), grad_y.data_ptr(), _ptr(gx),
                       _vector(gg, n.channels, index, "grad_gamma"),
-                      _vector(gb, n.channels, index, "grad_beta"), ws.data_ptr(),
-                      ws.numel() * ws.element_size()), "fno_layer_norm_bwd")
+                      _vector(gb, n.channels, index, "grad_beta"), _ptr(ws),
+                      0 if ws is None else ws.numel() * ws.element_size()), "fno_layer_norm_bwd")
     return {"x": gx, "gamma": gg, "beta": gb}
 
 

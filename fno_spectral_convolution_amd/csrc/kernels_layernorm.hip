@@ -154,17 +154,19 @@ __global__ __launch_bounds__(BLOCK) void k_ln_fwd_rows(NormArgs a, const T* x, c
   }
 }
 
-template <typename T, int VEC, int TPR, int NV, int BLOCK>
-__global__ __launch_bounds__(BLOCK) void k_ln_bwd_rows(NormArgs a, const T* x, const float* gamma,
-                                                       const float* stats, const T* gy, T* gx,
-                                                       float* part) {
+// Work-group `block` of `blocks` of the backward.  WEIGHTS: also the sums of its rows for the weight
+// gradients, into row `block` of part.
+template <typename T, int VEC, int TPR, int NV, int BLOCK, bool WEIGHTS>
+__device__ __forceinline__ void bwd_rows(const NormArgs& a, const T* x, const float* gamma,
+                                         const float* stats, const T* gy, T* gx, float* part,
+                                         int block, int blocks) {
   constexpr int kGroups = BLOCK / TPR, kWaves = TPR > 64 ? TPR / 64 : 1;
   constexpr int kLanes = TPR < 64 ? TPR : 64;
   // the next row's loads go ahead of this one's sums where the registers allow
   constexpr bool kAhead = NV * VEC < 16;
   constexpr int kSets = BLOCK / (TPR < 64 ? 64 : TPR), kCols = TPR * VEC;
   __shared__ float s_sum[2][kGroups][kWaves][2];
-  __shared__ float s_cols[kSets][kCols];
+  __shared__ float s_cols[WEIGHTS ? kSets : 1][WEIGHTS ? kCols : 1];
   const int tid = threadIdx.x, t = tid % TPR, group = tid / TPR, wave = t / 64;
   const int d = a.channels;
   const float inv_d = 1.0f / (float)d;
@@ -181,8 +183,8 @@ __global__ __launch_bounds__(BLOCK) void k_ln_bwd_rows(NormArgs a, const T* x, c
 #pragma unroll
   for (int k = 0; k < NV; ++k) partial |= lo[k] != 0;
   partial = __any(partial);
-  const int64_t rows = a.batch, step = (int64_t)gridDim.x * kGroups;
-  int64_t base = (int64_t)blockIdx.x * kGroups;
+  const int64_t rows = a.batch, step = (int64_t)blocks * kGroups;
+  int64_t base = (int64_t)block * kGroups;
   Raw<T, VEC> next_x[NV], next_g[NV];
   float next_mean = 0.f, next_rstd = 0.f;
   const auto fetch = [&](int64_t at) {
@@ -216,8 +218,10 @@ __global__ __launch_bounds__(BLOCK) void k_ln_bwd_rows(NormArgs a, const T* x, c
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           h[k][i] = (h[k][i] - mean) * rstd;
-          dg[k][i] += g[k][i] * h[k][i];
-          db[k][i] += g[k][i];
+          if (WEIGHTS) {
+            dg[k][i] += g[k][i] * h[k][i];
+            db[k][i] += g[k][i];
+          }
           g[k][i] *= ga[k][i];
         }
     }
@@ -254,9 +258,9 @@ __global__ __launch_bounds__(BLOCK) void k_ln_bwd_rows(NormArgs a, const T* x, c
       }
     }
   }
-  if (!part) return;
+  if (!WEIGHTS) return;
   // the work-group's rows' sums of each column: lanes of a wave first, then its waves through LDS
-  part += (int64_t)blockIdx.x * 2 * d;
+  part += (int64_t)block * 2 * d;
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -279,6 +283,51 @@ __global__ __launch_bounds__(BLOCK) void k_ln_bwd_rows(NormArgs a, const T* x, c
         part[(int64_t)m * d + st + c % VEC] = v;
       }
     }
+}
+
+template <typename T, int VEC, int TPR, int NV, int BLOCK, bool WEIGHTS>
+__global__ __launch_bounds__(BLOCK) void k_ln_bwd_rows(NormArgs a, const T* x, const float* gamma,
+                                                       const float* stats, const T* gy, T* gx,
+                                                       float* part) {
+  bwd_rows<T, VEC, TPR, NV, BLOCK, WEIGHTS>(a, x, gamma, stats, gy, gx, part, blockIdx.x,
+                                            gridDim.x);
+}
+
+// Few rows: work-groups [0, row_blocks) take the rows, and the others 64 columns each, down all
+// rows, whose weight gradients they finish: x and grad_y are read twice (out of a cache), which
+// costs less than a second launch.
+template <typename T, int VEC, int TPR, int NV, int BLOCK>
+__global__ __launch_bounds__(BLOCK) void k_ln_bwd_few(NormArgs a, const T* x, const float* gamma,
+                                                      const float* stats, const T* gy, T* gx,
+                                                      float* ggamma, float* gbeta,
+                                                      int row_blocks) {
+  if ((int)blockIdx.x < row_blocks) {
+    bwd_rows<T, VEC, TPR, NV, BLOCK, false>(a, x, gamma, stats, gy, gx, nullptr, blockIdx.x,
+                                            row_blocks);
+    return;
+  }
+  constexpr int kWaves = BLOCK / 64;
+  __shared__ float s_sum[2][kWaves][64];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int c = (blockIdx.x - row_blocks) * 64 + lane, col = c < a.channels ? c : a.channels - 1;
+  float sg = 0.f, sb = 0.f;
+#pragma unroll 4
+  for (int r = wave; r < (int)a.batch; r += kWaves) {
+    const float g = to_float(gy[r * a.y_stride + col]);
+    const float h = (to_float(x[r * a.x_stride + col]) - stats[r]) * stats[a.batch + r];
+    sg += g * h;
+    sb += g;
+  }
+  s_sum[0][wave][lane] = sg;
+  s_sum[1][wave][lane] = sb;
+  __syncthreads();
+  if (threadIdx.x < 128 && c < a.channels) {
+    float* out = wave == 0 ? ggamma : gbeta;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v += s_sum[wave][w][lane];
+    if (out) out[c] = v;
+  }
 }
 
 // Rows longer than a work-group's registers hold: sweeps over the row, which stays in the L2.
@@ -427,23 +476,25 @@ struct Tile {
 template <int VEC, bool FLAT>
 struct Tiles {
   int64_t left, entry, at, step_entries, step_at;
-  __device__ __forceinline__ Tiles(int64_t tiles, int64_t per_entry) {
-    left = tiles - blockIdx.x;
+  int blocks;
+  __device__ __forceinline__ Tiles(int64_t tiles, int64_t per_entry, int block, int blocks_)
+      : blocks(blocks_) {
+    left = tiles - block;
     if (FLAT) {
       entry = step_entries = step_at = 0;
-      at = blockIdx.x;
+      at = block;
     } else {
-      entry = uniform((int64_t)blockIdx.x / per_entry);
-      at = (int64_t)blockIdx.x - entry * per_entry;
-      step_entries = uniform((int64_t)gridDim.x / per_entry);
-      step_at = (int64_t)gridDim.x - step_entries * per_entry;
+      entry = uniform((int64_t)block / per_entry);
+      at = (int64_t)block - entry * per_entry;
+      step_entries = uniform((int64_t)blocks / per_entry);
+      step_at = (int64_t)blocks - step_entries * per_entry;
     }
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ void next(int64_t per_entry) {
-    left -= gridDim.x;
+    left -= blocks;
     if (FLAT) {
-      at += gridDim.x;
+      at += blocks;
       return;
     }
     entry += step_entries;
@@ -504,7 +555,8 @@ __global__ __launch_bounds__(N <= 8 ? 512 : 1024) void k_ln_fwd_field(
   const int c0 = wave * N, nc = a.channels - c0 < N ? a.channels - c0 : N;
   const float inv_c = 1.0f / (float)a.channels, inv_n = 1.0f / (float)nc;
   int flip = 0;
-  for (Tiles<VEC, FLAT> at(tiles, per_entry); at.more(); at.next(per_entry), flip ^= 1) {
+  for (Tiles<VEC, FLAT> at(tiles, per_entry, blockIdx.x, gridDim.x); at.more();
+       at.next(per_entry), flip ^= 1) {
     const Tile t = at.tile(a);
     const T* p = x + t.b * a.x_stride + t.p;
     float f[N][VEC], mean[VEC] = {}, sq[VEC] = {};
@@ -577,11 +629,13 @@ __global__ __launch_bounds__(N <= 8 ? 512 : 1024) void k_ln_fwd_field(
   }
 }
 
-template <typename T, int N, int VEC, bool FLAT>
-__global__ __launch_bounds__(1024) void k_ln_bwd_field(NormArgs a, int64_t tiles,
-                                                       int64_t per_entry, const T* x,
-                                                       const float* gamma, const float* stats,
-                                                       const T* gy, T* gx, float* part) {
+// Work-group `block` of `blocks` of the backward.  WEIGHTS: also the sums of its points for the
+// weight gradients, into row `block` of part.
+template <typename T, int N, int VEC, bool FLAT, bool WEIGHTS>
+__device__ __forceinline__ void bwd_field(const NormArgs& a, int64_t tiles, int64_t per_entry,
+                                          const T* x, const float* gamma, const float* stats,
+                                          const T* gy, T* gx, float* part, int block,
+                                          int blocks) {
   extern __shared__ float s_mem[];  // [2][waves][2][64 VEC]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
@@ -589,7 +643,7 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_field(NormArgs a, int64_t tiles
   const float inv_c = 1.0f / (float)a.channels;
   float dg[N] = {}, db[N] = {};
   int flip = 0;
-  for (Tiles<VEC, FLAT> at(tiles, per_entry); at.more(); at.next(per_entry), flip ^= 1) {
+  for (Tiles<VEC, FLAT> at(tiles, per_entry, block, blocks); at.more(); at.next(per_entry), flip ^= 1) {
     const Tile t = at.tile(a);
     const T* p = x + t.b * a.x_stride + t.p;
     const T* r = gy + t.b * a.y_stride + t.p;
@@ -609,7 +663,7 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_field(NormArgs a, int64_t tiles
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         h[c][i] = (h[c][i] - mean[i]) * rstd[i];
-        if (i >= t.lo) {
+        if (WEIGHTS && i >= t.lo) {
           dg[c] += g[c][i] * h[c][i];
           db[c] += g[c][i];
         }
@@ -649,8 +703,8 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_field(NormArgs a, int64_t tiles
         }
     }
   }
-  if (!part) return;
-  part += (int64_t)blockIdx.x * 2 * a.channels + c0;
+  if (!WEIGHTS) return;
+  part += (int64_t)block * 2 * a.channels + c0;
 #pragma unroll
   for (int c = 0; c < N; ++c) {
     const float sg = lane_sum<64>(dg[c]), sb = lane_sum<64>(db[c]);
@@ -658,6 +712,65 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_field(NormArgs a, int64_t tiles
       part[c] = sg;
       part[a.channels + c] = sb;
     }
+  }
+}
+
+template <typename T, int N, int VEC, bool FLAT, bool WEIGHTS>
+__global__ __launch_bounds__(1024) void k_ln_bwd_field(NormArgs a, int64_t tiles,
+                                                       int64_t per_entry, const T* x,
+                                                       const float* gamma, const float* stats,
+                                                       const T* gy, T* gx, float* part) {
+  bwd_field<T, N, VEC, FLAT, WEIGHTS>(a, tiles, per_entry, x, gamma, stats, gy, gx, part,
+                                      blockIdx.x, gridDim.x);
+}
+
+// Few points: as k_ln_bwd_few, with a channel to each of the work-groups from tile_blocks on.
+template <typename T, int N, int VEC, bool FLAT>
+__global__ __launch_bounds__(1024) void k_ln_bwd_field_few(NormArgs a, int64_t tiles,
+                                                           int64_t per_entry, const T* x,
+                                                           const float* gamma, const float* stats,
+                                                           const T* gy, T* gx, float* ggamma,
+                                                           float* gbeta, int tile_blocks) {
+  if ((int)blockIdx.x < tile_blocks) {
+    bwd_field<T, N, VEC, FLAT, false>(a, tiles, per_entry, x, gamma, stats, gy, gx, nullptr,
+                                      blockIdx.x, tile_blocks);
+    return;
+  }
+  __shared__ float s_sum[2][16];
+  constexpr int V = FLAT ? 1 : 4;
+  const int c = blockIdx.x - tile_blocks, npts = (int)a.npts, rows = (int)a.batch * npts;
+  const int per = (npts + V - 1) / V, vectors = (int)a.batch * per;
+  const T *p = x + c * a.npts, *r = gy + c * a.npts;
+  float sg = 0.f, sb = 0.f;
+#pragma unroll 4
+  for (int q = threadIdx.x; q < vectors; q += blockDim.x) {
+    const int b = (uint32_t)q / (uint32_t)per;
+    int at, lo;
+    place<V>(q - b * per, npts, at, lo);
+    float g[V], h[V], mean[V], rstd[V];
+    load_pack<T, V>(r + b * a.y_stride + at, g);
+    load_pack<T, V>(p + b * a.x_stride + at, h);
+    load_pack<float, V>(stats + b * npts + at, mean);
+    load_pack<float, V>(stats + rows + b * npts + at, rstd);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i >= lo) {
+        sg += g[i] * ((h[i] - mean[i]) * rstd[i]);
+        sb += g[i];
+      }
+  }
+  sg = lane_sum<64>(sg);
+  sb = lane_sum<64>(sb);
+  if (threadIdx.x % 64 == 0) {
+    s_sum[0][threadIdx.x / 64] = sg;
+    s_sum[1][threadIdx.x / 64] = sb;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    float v = 0.f;
+    for (int w = 0; w < (int)blockDim.x / 64; ++w) v += s_sum[threadIdx.x][w];
+    float* out = threadIdx.x == 0 ? ggamma : gbeta;
+    if (out) out[c] = v;
   }
 }
 
@@ -917,8 +1030,9 @@ hipError_t fwd_t(NormArgs a, const T* x, const float* gamma, const float* beta, 
   return hipGetLastError();
 }
 
+// work-groups of the backward's pass over rows, and rows of its partial sums
 template <typename T>
-int parts_t(const NormArgs& a) {
+int groups_t(const NormArgs& a) {
   if (a.batch == 0 || a.npts == 0) return 0;
   switch (form_of<T>(a)) {
     case kRows: {
@@ -938,49 +1052,106 @@ int parts_t(const NormArgs& a) {
   }
 }
 
+hipError_t finish(const NormArgs& a, int parts, const float* part, float* ggamma, float* gbeta,
+                  hipStream_t s) {
+  const int64_t width = 2 * (int64_t)a.channels;
+  const auto go = [&](auto cols) {
+    hipLaunchKernelGGL(k_ln_finish<cols.value>, dim3(ceil_div(width, cols.value)), dim3(256), 0, s,
+                       a.channels, parts, part, ggamma, gbeta);
+    return hipGetLastError();
+  };
+  return width >= 8192 ? go(Int<64>()) : width >= 1024 ? go(Int<16>()) : go(Int<4>());
+}
+
+// Whether the weight gradients come from the columns' own reading of x and grad_y and not from
+// partial sums of the rows' pass: few enough rows that this is short, which saves a launch (4 us for
+// the host) and the workspace.  On the GPU, one launch against two and their gap: 48 x 640 float32
+// 3.7 us against 8; 512 x 1024 6.7 against 10; 5 x 20 x 4095 (27 vectors to a thread) 10 against 10,
+// 20 x 26000 (34) 12 against 10; 16 x 32 x 250 (16 points to a thread) 6.4 against 9, 32 x 16 x 250
+// (62) 16 against 9.  By the shape alone, so that what else is asked for does not change their bits.
 template <typename T>
-hipError_t bwd_t(NormArgs a, const T* x, const float* gamma, const float* stats,
-                 const T* gy, T* gx, float* part, hipStream_t s) {
-  const int parts = parts_t<T>(a);
+bool few(const NormArgs& a) {
+  const int64_t rows = a.batch * a.npts;
+  if (rows * a.channels > 1 << 19) return false;
+  if (form_of<T>(a) == kRows) return rows <= 512;
+  if (form_of<T>(a) != kField) return false;
+  // a channel's work-group has 64 threads for each wave of the tiles'
+  const int threads = 64 * (int)ceil_div(a.channels, field_n(a.channels));
+  return rows <= threads * (a.npts < 256 ? 16 : 4 * 28);
+}
+
+template <typename T>
+hipError_t bwd_t(NormArgs a, const T* x, const float* gamma, const float* stats, const T* gy,
+                 T* gx, float* ggamma, float* gbeta, float* part, hipStream_t s) {
+  const bool weights = ggamma || gbeta, by_columns = few<T>(a);
+  const int groups = groups_t<T>(a);
+  // one launch takes the rows and the columns, except in place, where the columns go first
+  if (by_columns && weights && gx && (gx == x || gx == gy)) {
+    const hipError_t e = bwd_t<T>(a, x, gamma, stats, gy, nullptr, ggamma, gbeta, part, s);
+    return e != hipSuccess ? e : bwd_t<T>(a, x, gamma, stats, gy, gx, nullptr, nullptr, part, s);
+  }
+  const bool columns = by_columns && weights, sums = weights && !by_columns;
+  const int with_rows = gx ? groups : 0;  // work-groups before the columns'
   a.stream = stream_out(a, gx, a.gx_stride);
   switch (form_of<T>(a)) {
     case kRows:
       pick_rows<T>(a.channels, [&](auto vec, auto tpr, auto nv) {
-        hipLaunchKernelGGL((k_ln_bwd_rows<T, vec.value, tpr.value, nv.value, kBwdBlock>),
-                           dim3(parts), dim3(kBwdBlock), 0, s, a, x, gamma, stats, gy, gx, part);
+        constexpr int V = vec.value, TPR = tpr.value, NV = nv.value;
+        if (columns)
+          hipLaunchKernelGGL((k_ln_bwd_few<T, V, TPR, NV, kBwdBlock>),
+                             dim3(with_rows + ceil_div(a.channels, 64)), dim3(kBwdBlock), 0, s, a, x,
+                             gamma, stats, gy, gx, ggamma, gbeta, with_rows);
+        else if (sums)
+          hipLaunchKernelGGL((k_ln_bwd_rows<T, V, TPR, NV, kBwdBlock, true>), dim3(groups),
+                             dim3(kBwdBlock), 0, s, a, x, gamma, stats, gy, gx, part);
+        else
+          hipLaunchKernelGGL((k_ln_bwd_rows<T, V, TPR, NV, kBwdBlock, false>), dim3(groups),
+                             dim3(kBwdBlock), 0, s, a, x, gamma, stats, gy, gx, part);
       });
       break;
     case kField:
       pick_field(a.channels, [&](auto n) {
-        constexpr int kWide = kBwdVec<T, n.value>;
-        const FieldShape f = field_shape(a, n.value, kWide);
-        const dim3 grid(parts), block(64 * f.waves);
-        if (f.flat)
-          hipLaunchKernelGGL((k_ln_bwd_field<T, n.value, 1, true>), grid, block, f.lds, s, a,
-                             f.tiles, f.per_entry, x, gamma, stats, gy, gx, part);
-        else
-          hipLaunchKernelGGL((k_ln_bwd_field<T, n.value, kWide, false>), grid, block, f.lds, s, a,
-                             f.tiles, f.per_entry, x, gamma, stats, gy, gx, part);
+        constexpr int N = n.value, kWide = kBwdVec<T, N>;
+        const FieldShape f = field_shape(a, N, kWide);
+        const auto go = [&](auto vec, auto flat) {
+          constexpr int V = vec.value;
+          constexpr bool F = flat.value;
+          const dim3 grid(groups), block(64 * f.waves);
+          if (columns)
+            hipLaunchKernelGGL((k_ln_bwd_field_few<T, N, V, F>), dim3(with_rows + a.channels), block,
+                               f.lds, s, a, f.tiles, f.per_entry, x, gamma, stats, gy, gx, ggamma,
+                               gbeta, with_rows);
+          else if (sums)
+            hipLaunchKernelGGL((k_ln_bwd_field<T, N, V, F, true>), grid, block, f.lds, s, a,
+                               f.tiles, f.per_entry, x, gamma, stats, gy, gx, part);
+          else
+            hipLaunchKernelGGL((k_ln_bwd_field<T, N, V, F, false>), grid, block, f.lds, s, a,
+                               f.tiles, f.per_entry, x, gamma, stats, gy, gx, part);
+        };
+        if (f.flat) go(Int<1>(), std::true_type());
+        else go(Int<kWide>(), std::false_type());
       });
       break;
     // the column sums first: grad_x may overwrite x or grad_y
     case kLongRows:
-      if (part)
-        hipLaunchKernelGGL(k_ln_cols_long<T>, dim3(ceil_div(a.channels, 256 * kVec<T>), parts),
+      if (weights)
+        hipLaunchKernelGGL(k_ln_cols_long<T>, dim3(ceil_div(a.channels, 256 * kVec<T>), groups),
                            dim3(256), 0, s, a, x, stats, gy, part);
       if (gx)
         hipLaunchKernelGGL(k_ln_bwd_long<T>, dim3(cut(a.batch, 1024)), dim3(kLong), 0, s, a, x,
                            gamma, stats, gy, gx);
       break;
     case kPoints:
-      if (part)
-        hipLaunchKernelGGL(k_ln_cols_points<T>, dim3(parts, cut(a.channels, 32768)), dim3(256), 0,
+      if (weights)
+        hipLaunchKernelGGL(k_ln_cols_points<T>, dim3(groups, cut(a.channels, 32768)), dim3(256), 0,
                            s, a, x, stats, gy, part);
       if (gx)
         hipLaunchKernelGGL(k_ln_bwd_points<T>, dim3(cut(ceil_div(a.batch * a.npts, 256), 4096)),
                            dim3(256), 0, s, a, x, gamma, stats, gy, gx);
   }
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !sums) return e;
+  return finish(a, groups, part, ggamma, gbeta, s);
 }
 
 }  // namespace
@@ -996,30 +1167,24 @@ hipError_t launch_layer_norm_fwd(const NormArgs& a, int dtype, const void* x, co
 }
 
 int layer_norm_parts(const NormArgs& a, int dtype) {
-  return dtype == FNO_DTYPE_F32 ? parts_t<float>(a) : parts_t<__bf16>(a);
+  const auto parts = [&](auto t) {
+    typedef decltype(t) T;
+    return few<T>(a) ? 0 : groups_t<T>(a);
+  };
+  return dtype == FNO_DTYPE_F32 ? parts(0.f) : parts((__bf16)0.f);
 }
 
 hipError_t launch_layer_norm_bwd(const NormArgs& a, int dtype, const void* x, const float* gamma,
-                                 const float* stats, const void* gy, void* gx, float* part,
-                                 hipStream_t s) {
+                                 const float* stats, const void* gy, void* gx, float* ggamma,
+                                 float* gbeta, float* part, hipStream_t s) {
+  if (a.batch == 0 || a.npts == 0) return finish(a, 0, part, ggamma, gbeta, s);
   const auto go = [&](auto t) {
     typedef decltype(t) T;
     return bwd_t<T>(a, static_cast<const T*>(x), gamma, stats, static_cast<const T*>(gy),
-                    static_cast<T*>(gx), part, s);
+                    static_cast<T*>(gx), ggamma, gbeta, part, s);
   };
   if (dtype == FNO_DTYPE_F32) return go(0.f);
   return dtype == FNO_DTYPE_BF16 ? go((__bf16)0.f) : go((_Float16)0.f);
-}
-
-hipError_t launch_layer_norm_finish(const NormArgs& a, int nparts, const float* part,
-                                    float* ggamma, float* gbeta, hipStream_t s) {
-  const int64_t width = 2 * (int64_t)a.channels;
-  const auto go = [&](auto cols) {
-    hipLaunchKernelGGL(k_ln_finish<cols.value>, dim3(ceil_div(width, cols.value)), dim3(256), 0, s,
-                       a.channels, nparts, part, ggamma, gbeta);
-    return hipGetLastError();
-  };
-  return width >= 8192 ? go(Int<64>()) : width >= 1024 ? go(Int<16>()) : go(Int<4>());
 }
 
 }  // namespace fno

@@ -1970,21 +1970,17 @@ fno_status fno_layer_norm_bwd(const fno_layer_norm_desc* desc, const void* x, co
     if (a.batch > 1 && ((grad_x == x && a.gx_stride != a.x_stride) ||
                         (grad_x == grad_y && a.gx_stride != a.y_stride)))
       return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm in place needs equal strides");
-    if (weights) {
+    const size_t need = weights ? norm_workspace(a, desc->dtype) : 0;
+    if (need > 0) {
       REQ(ws, "workspace");
-      if (ws_bytes < norm_workspace(a, desc->dtype))
-        return fail(FNO_ERR_INVALID_ARGUMENT, "workspace too small");
+      if (ws_bytes < need) return fail(FNO_ERR_INVALID_ARGUMENT, "workspace too small");
     }
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
-  float* part = weights ? static_cast<float*>(ws) : nullptr;
-  if (!none && (weights || grad_x))
-    LAUNCH("layer_norm_bwd", s,
-           fno::launch_layer_norm_bwd(a, desc->dtype, x, gamma, stats, grad_y, grad_x, part, s));
-  if (weights)
-    LAUNCH("layer_norm_finish", s,
-           fno::launch_layer_norm_finish(a, none ? 0 : fno::layer_norm_parts(a, desc->dtype),
-                                         part, grad_gamma, grad_beta, s));
+  if ((none && !weights) || (!weights && !grad_x)) return FNO_OK;
+  LAUNCH("layer_norm_bwd", s,
+         fno::launch_layer_norm_bwd(a, desc->dtype, x, gamma, stats, grad_y, grad_x, grad_gamma,
+                                    grad_beta, static_cast<float*>(ws), s));
   return FNO_OK;
 }
 

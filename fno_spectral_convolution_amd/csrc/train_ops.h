@@ -21,12 +21,11 @@ hipError_t launch_layer_norm_fwd(const NormArgs& a, int dtype, const void* x, co
                                  const float* beta, void* y, float* stats, hipStream_t s);
 // rows of partial sums that the backward writes for the weight gradients, each [2][channels] floats
 int layer_norm_parts(const NormArgs& a, int dtype);
-// part: layer_norm_parts rows (unused when both weight gradients are NULL)
+// the whole backward; part: layer_norm_parts rows (unused when both weight gradients are NULL);
+// without rows only the weight gradients' zeros
 hipError_t launch_layer_norm_bwd(const NormArgs& a, int dtype, const void* x, const float* gamma,
-                                 const float* stats, const void* gy, void* gx, float* part,
-                                 hipStream_t s);
-hipError_t launch_layer_norm_finish(const NormArgs& a, int nparts, const float* part,
-                                    float* ggamma, float* gbeta, hipStream_t s);
+                                 const float* stats, const void* gy, void* gx, float* ggamma,
+                                 float* gbeta, float* part, hipStream_t s);
 
 // ---- tensor lists (kernels_optim.hip) --------------------------------------------------------
 // A list's device table: its entries, then the entry that holds each chunk.  Chunks are kChunk

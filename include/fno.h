@@ -371,7 +371,8 @@ typedef struct fno_layer_norm_desc {
 fno_status fno_layer_norm_fwd(const fno_layer_norm_desc* desc, const void* x, const float* gamma,
                               const float* beta, void* y, float* stats, void* stream);
 
-/* Bytes of workspace of fno_layer_norm_bwd on this descriptor. */
+/* Bytes of workspace of fno_layer_norm_bwd on this descriptor (0 for small fields, which need
+ * none: workspace may then be NULL). */
 fno_status fno_layer_norm_workspace_bytes(const fno_layer_norm_desc* desc, size_t* bytes);
 
 /* Backward from the forward's x and stats.  With h = (x - mu) r and g = gamma grad_y:

@@ -61,8 +61,14 @@ def test_layer_norm_pointers_refused():
     assert _fwd(_desc(y_stride=23)) == BAD            # outputs would overlap
     assert _fwd(_desc(x_stride=30)) == BAD            # in place with another stride
     for kw in (dict(x=None), dict(gy=None), dict(stats=None), dict(gx=P + 2), dict(gg=P + 2),
-               dict(gb=P + 1), dict(ws=None), dict(ws=P + 8), dict(ws_bytes=0)):
+               dict(gb=P + 1)):
         assert _bwd(d, **kw) == BAD, kw
+    big = _desc(npts=1 << 20, x_stride=8 << 20, y_stride=8 << 20, grad_x_stride=8 << 20)
+    for kw in (dict(ws=None), dict(ws=P + 8), dict(ws_bytes=0)):
+        assert _bwd(big, **kw) == BAD, kw
+    n = ctypes.c_size_t()
+    assert L._lib.fno_layer_norm_workspace_bytes(d, ctypes.byref(n)) == L.FNO_OK and n.value == 0
+    assert L._lib.fno_layer_norm_workspace_bytes(big, ctypes.byref(n)) == L.FNO_OK and n.value > 0
     assert _bwd(_desc(grad_x_stride=23)) == BAD
     assert _bwd(_desc(y_stride=30)) == BAD            # grad_x is grad_y with another stride
     assert L._lib.fno_layer_norm_workspace_bytes(d, None) == BAD
