@@ -1,7 +1,8 @@
 """ctypes binding of libfno (argument marshalling only).
 
-Every function of ``include/fno.h`` is exposed under its C name and takes plain integers
-for pointers (``tensor.data_ptr()``) and streams (``torch.cuda.current_stream().cuda_stream``).
+Every function of ``include/fno.h`` and ``include/fno_train.h`` is exposed under its C name and
+takes plain integers for pointers (``tensor.data_ptr()``) and streams
+(``torch.cuda.current_stream().cuda_stream``).
 ``Plan`` wraps a plan for torch tensors: it allocates outputs, workspace and save buffers
 with torch on the plan's device and forwards pointers; every step of the computation runs
 in libfno's HIP kernels.  There is no fallback: if libfno.so is missing or fails to load,
@@ -47,12 +48,16 @@ EXPORTS = [
     "fno_tucker_keep_intermediates", "fno_tucker_save_bytes",
     "fno_tucker_block_fwd", "fno_tucker_block_bwd", "fno_tucker_spectral_conv_fwd",
     "fno_tucker_spectral_conv_bwd", "fno_tucker_block_fwd_mse", "fno_tucker_block_bwd_preact",
-    "fno_layer_norm_fwd", "fno_layer_norm_workspace_bytes", "fno_layer_norm_bwd",
-    "fno_tensor_list_bytes", "fno_tensor_list_create", "fno_tensor_list_destroy",
-    "fno_grad_norm_workspace_bytes", "fno_grad_norm", "fno_clip_grad_norm", "fno_adamw",
     "fno_timing_enable", "fno_timing_select",
     "fno_timing_reset", "fno_timing_count", "fno_timing_get", "fno_status_string",
     "fno_last_error_message",
+]
+
+# the training operators of fno_train.h
+TRAIN_EXPORTS = [
+    "fno_layer_norm_fwd", "fno_layer_norm_workspace_bytes", "fno_layer_norm_bwd",
+    "fno_tensor_list_bytes", "fno_tensor_list_create", "fno_tensor_list_destroy",
+    "fno_grad_norm_workspace_bytes", "fno_grad_norm", "fno_clip_grad_norm", "fno_adamw",
 ]
 
 

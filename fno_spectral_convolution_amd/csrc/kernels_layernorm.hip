@@ -1,4 +1,26 @@
 // Layer norm over the channels of a field [batch][channels][npts], forward and backward.
+//
+//   forward   mu = sum_c x / C,  r = 1 / sqrt(sum_c (x - mu)^2 / C + eps),  h = (x - mu) r,
+//             y = gamma h + beta
+//   backward  g = gamma grad_y,  grad_x = r (g - sum_c g / C - h sum_c(g h) / C),
+//             grad_gamma = sum grad_y h,  grad_beta = sum grad_y  (over batch and points)
+//
+// Each pass reads its fields once and writes once; memory bounds it (8 and 14 operations an element
+// against 8 and 12 bytes in float32).  A row or point is therefore held in registers from its load
+// to its store, and only the sums over channels leave a lane.  All sums and statistics are float32.
+// The variance comes from deviations about a mean, never from E[x^2] - E[x]^2; where several waves
+// share a row or point, each takes its own mean and the squared deviations about it, and they join
+// as M2 = sum_w (M2_w + n_w (mean_w - mean)^2), which needs one exchange where two sweeps need two.
+// The reciprocal square root is the hardware's (1 ulp).  The weight gradients are sums in a fixed
+// order: per work-group over its rows or points, then over the work-groups' partial rows.
+//
+// Measured on an MI355X whose large copies run at 4.9 TB/s (out of HBM, several buffers in turn):
+//   rows    8192 x 4096 bf16       forward  24 us (5.6 TB/s)   backward  40 us (5.1)
+//           8192 x 4096 float32    forward  42 us (6.4)        backward  69 us (5.8)
+//           16384 x 1024 bf16      forward  14 us (4.8)        backward  23 us (4.4)
+//   fields  8 x 64 x 512^2 float32 forward 195 us (5.6)        backward 291 us (5.6)
+//           2 x 20 x 128^3 float32 forward 140 us (5.0)        backward 200 us (5.2)
+//           8 x 64 x 512^2 bf16    forward 140 us (4.0)        backward 168 us (4.9)
 #include <type_traits>
 
 #include "train_device.h"
@@ -11,9 +33,10 @@ template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);  // elements of a 16-byte load
 
 // ---- rows (npts = 1) ---------------------------------------------------------------------------
-// Threads(TPR) hold a row, NV vectors of VEC elements each.  Vector j of the row starts at element
-// j VEC; the last one is moved back to end with the row, and the elements that it then shares with
-// its neighbour (i < lo) count once in sums and are stored twice with the same value.
+// TPR threads hold a row, NV vectors of VEC elements each: eight lanes for the shortest rows, the
+// work-group for the longest.  Vector j of the row starts at element j VEC; the last one is moved
+// back to end with the row, and the elements that it then shares with its neighbour (i < lo) count
+// once in sums and are stored twice with the same value.  So any length takes whole 16-byte loads.
 template <int VEC>
 __device__ __forceinline__ void place(int j, int d, int& start, int& lo) {
   const int e = j * VEC;
@@ -21,7 +44,9 @@ __device__ __forceinline__ void place(int j, int d, int& start, int& lo) {
   lo = e < d ? e - start : VEC;
 }
 
-// A row's slice of gamma or beta; `none` where there is none.
+// A row's slice of gamma or beta; `none` where there is none.  In 16-byte loads: loaded element by
+// element, 32 bytes apart from lane to lane, the weights cost more than the row itself (8192 x 4096
+// bf16 forward 39 us instead of 24).
 template <int VEC>
 __device__ __forceinline__ void load_weight(const float* w, int start, float none,
                                             float (&f)[VEC]) {
@@ -67,6 +92,10 @@ __device__ __forceinline__ void by_mask(bool masked, F&& f) {
   else f(std::false_type());
 }
 
+// A work-group goes over many rows: the weights stay in its registers, and the next row's loads go
+// ahead of this row's sums (two rows ahead measured the same).  Sums go over a wave's lanes without
+// LDS; a row of several waves takes one barrier, after which every lane reads one wave's part.
+// Eight elements to a thread keep eight waves on a SIMD; sixteen measured 0 to 4% slower.
 template <typename T, int VEC, int TPR, int NV, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void k_ln_fwd_rows(NormArgs a, const T* x, const float* gamma,
                                                        const float* beta, T* y, float* stats) {
@@ -155,7 +184,10 @@ __global__ __launch_bounds__(BLOCK) void k_ln_fwd_rows(NormArgs a, const T* x, c
 }
 
 // Work-group `block` of `blocks` of the backward.  WEIGHTS: also the sums of its rows for the weight
-// gradients, into row `block` of part.
+// gradients, into row `block` of part; they stay in registers until its last row is done.  One
+// work-group of 16 waves to a compute unit: 256 partial rows, the fewest that fill the card, since
+// each is 8 bytes a channel to write and read again (512 of them, half as long, cost 8192 x 4096
+// bf16 52 us instead of 43).
 template <typename T, int VEC, int TPR, int NV, int BLOCK, bool WEIGHTS>
 __device__ __forceinline__ void bwd_rows(const NormArgs& a, const T* x, const float* gamma,
                                          const float* stats, const T* gy, T* gx, float* part,
@@ -330,7 +362,8 @@ __global__ __launch_bounds__(BLOCK) void k_ln_bwd_few(NormArgs a, const T* x, co
   }
 }
 
-// Rows longer than a work-group's registers hold: sweeps over the row, which stays in the L2.
+// Rows longer than a work-group's registers hold (over 16384): sweeps over the row, which stays in
+// the L2.
 constexpr int kLong = 1024;
 
 __device__ __forceinline__ float group_sum(float v, float* s_red) {
@@ -463,9 +496,12 @@ __global__ __launch_bounds__(256) void k_ln_cols_long(NormArgs a, const T* x, co
 }
 
 // ---- fields (npts > 1) -------------------------------------------------------------------------
-// A work-group takes a tile of points, VEC to a lane, and its waves share the channels, N each, in
-// registers; what a point's channels sum to joins through LDS.  FLAT: one point to a lane, counted
-// through all batch entries (short entries); else tiles of 64 VEC points of one entry.
+// A channel's points are next to one another, so lanes go along the points, VEC to a lane, and the
+// sums over channels stay inside a lane.  A work-group takes a tile of points, and its waves share
+// the channels, N each, in registers; what a point's channels sum to joins through LDS, one barrier
+// a tile.  Few waves with many channels beat many with few (64 channels as 16 waves of 4: forward
+// 539 us, as 8 waves of 8: 217, both before streaming stores).  FLAT: one point to a lane, counted
+// through all batch entries; else tiles of 64 VEC points of one entry.
 struct Tile {
   int64_t b, p;   // batch entry and point where the tile starts (FLAT: of the lane's own point)
   uint32_t off;   // the lane's first element from there (below 64 VEC)
@@ -908,7 +944,7 @@ int64_t resident(int block) {
   return n;
 }
 
-// Calls f(threads to a row, vectors to a thread) as constants, for rows of `nvec` vectors.
+// Calls f(elements of a vector, threads to a row, vectors to a thread) as constants.
 template <int N>
 struct Int {
   static constexpr int value = N;
@@ -959,7 +995,9 @@ void pick_field(int c, F&& f) {
     default: return f(Int<16>());
   }
 }
-// points to a lane
+// Points to a lane.  Forward: 4 (8 of a half type, whole 16-byte loads, spill: 8 x 64 x 512^2 bf16
+// 202 us against 140).  Backward, with twice the registers: 2 (4: 496 us against 322 on
+// 8 x 64 x 512^2 float32, before streaming stores), 1 beyond 10 channels a wave.
 template <typename T>
 constexpr int kFwdVec = 4;
 template <typename T, int N>
@@ -970,6 +1008,8 @@ struct FieldShape {
   int64_t per_entry, tiles;
   size_t lds;
 };
+// Entries below 256 points go FLAT.  Forward, flat and not: 400 x 32 x 200 9.0 and 9.4 us,
+// 400 x 32 x 300 12.6 and 12.1, 400 x 32 x 600 18.9 and 14.4.
 FieldShape field_shape(const NormArgs& a, int n, int wide) {
   FieldShape s;
   s.flat = a.npts < 256;
@@ -982,8 +1022,12 @@ FieldShape field_shape(const NormArgs& a, int n, int wide) {
 }
 int field_bwd_groups(const FieldShape& s) { return (int)cut(s.tiles, ceil_div(8192, s.waves)); }
 
-// Whether an output goes past the caches: where it is larger than the L2s together (32 MB) and
-// its rows or planes are whole 128-byte lines.
+// Whether an output goes past the caches (nontemporal stores): where it is larger than the 256 MB
+// cache behind the L2s, and its rows or planes are whole 128-byte lines.  Forward, with and without:
+// 8 x 64 x 512^2 (537 MB) 196 against 208 us, 2 x 20 x 128^3 (336 MB) 140 against 149; backward 291
+// against 319 and 201 against 217.  Below it the cache takes the writes: 8 x 20 x 512^2 (168 MB) 65
+// against 60, backward 111 against 102.  Lines that two work-groups share suffer: 8 x 20 x 300001
+// 92 against 72, backward 171 against 130.
 template <typename T>
 bool stream_out(const NormArgs& a, const T* out, int64_t stride) {
   const int64_t pitch = (a.npts == 1 ? stride : a.npts) * (int64_t)sizeof(T);

@@ -1,4 +1,22 @@
 // The global gradient norm over a list of tensors, clipping, and the AdamW update.
+//
+//   norm = sqrt(sum g^2) / scale,  factor = min(1, max / norm) / scale,  out = factor g
+//   m = b1 m + (1 - b1) factor g,  v = b2 v + (1 - b2) (factor g)^2,
+//   p = (1 - lr decay) p - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// Memory bounds all three: 4 bytes an element read, 8 read and written, 28.  A list is one launch
+// whatever its number of tensors: the work-groups share its chunks out evenly, each a run of
+// neighbours, so that a work-group meets few tensors and goes through each in 16-byte vectors, four
+// (AdamW: two of each of its four operands) under way.  Offsets inside a run are 32 bits, where it
+// lies is 64.  The sum of squares is float64: no gradient over- or underflows it, and it costs
+// nothing (float32 sums measured the same).  Its order is fixed by the list and the work-groups.
+//
+// Measured on an MI355X whose large copies run at 4.9 TB/s:
+//   norm   300 MB of half gradients 57 us (5.2 TB/s), 400 MB of float32 73 us (5.5)
+//   clip   301 half tensors, 150 million entries, into float32, with its norm 230 us (the 900 MB that
+//          it reads and writes at 3.9 TB/s, the norm's 300 MB besides)
+//   AdamW  52 million float32 entries 276 us (5.3 TB/s), with the norm before it 351 us: what the
+//          update wrote last is still on its way out of the 256 MB cache while the next norm reads
 #include "train_device.h"
 #include "train_ops.h"
 
@@ -269,7 +287,9 @@ __global__ __launch_bounds__(kThreads) void k_adamw(TensorTable params, TensorTa
   });
 }
 
-// Whether what a list's call writes outgrows the 256 MB cache behind the L2s: it goes past them.
+// Whether what a clip writes outgrows the 256 MB cache behind the L2s: it goes past them (150
+// million half entries into float32 226 us against 255, 100 million float32 229 against 246).  AdamW's
+// writes measured the same either way.
 bool large(const TensorTable& t) { return t.bytes > ((int64_t)256 << 20); }
 
 // work-groups of the kernels that write: as many as the compute units hold at a time

@@ -5,7 +5,7 @@
 #include <stdint.h>
 #include <string.h>
 
-#include "fno.h"
+#include "fno_train.h"
 
 namespace fno {
 

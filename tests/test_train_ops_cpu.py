@@ -2,11 +2,15 @@
 the library makes on the host before any HIP call, and the binding's own."""
 import ctypes
 import math
+import os
+import re
 
 import pytest
 import torch
 
 from fno_spectral_convolution_amd import binding as L
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 BAD = L.FNO_ERR_INVALID_ARGUMENT
 P = 1 << 20  # an aligned address that no call gets as far as reading
@@ -28,6 +32,16 @@ def _fwd(d, x=P, gamma=P, beta=P, y=P, stats=P):
 
 def _bwd(d, x=P, gamma=P, stats=P, gy=P, gx=P, gg=P, gb=P, ws=P, ws_bytes=1 << 30):
     return L._lib.fno_layer_norm_bwd(d, x, gamma, stats, gy, gx, gg, gb, ws, ws_bytes, None)
+
+
+def test_header_binding_and_library_agree():
+    src = open(os.path.join(ROOT, "include", "fno_train.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    names = sorted(set(re.findall(r"\b(fno_[a-z0-9_]+)\s*\(", src)))
+    assert names == sorted(L.TRAIN_EXPORTS)
+    lib = ctypes.CDLL(L.LIB_PATH)
+    for name in names:
+        assert hasattr(lib, name) and hasattr(L, name), name
 
 
 def test_struct_layouts():
