@@ -18,9 +18,9 @@
 //   rows    8192 x 4096 bf16       forward  24 us (5.6 TB/s)   backward  40 us (5.1)
 //           8192 x 4096 float32    forward  42 us (6.4)        backward  69 us (5.8)
 //           16384 x 1024 bf16      forward  14 us (4.8)        backward  23 us (4.4)
-//   fields  8 x 64 x 512^2 float32 forward 195 us (5.6)        backward 291 us (5.6)
+//   fields  8 x 64 x 512^2 float32 forward 193 us (5.7)        backward 288 us (5.7)
 //           2 x 20 x 128^3 float32 forward 140 us (5.0)        backward 200 us (5.2)
-//           8 x 64 x 512^2 bf16    forward 140 us (4.0)        backward 168 us (4.9)
+//           8 x 64 x 512^2 bf16    forward 123 us (4.5)        backward 166 us (5.0)
 #include <type_traits>
 
 #include "train_device.h"
@@ -498,10 +498,11 @@ __global__ __launch_bounds__(256) void k_ln_cols_long(NormArgs a, const T* x, co
 // ---- fields (npts > 1) -------------------------------------------------------------------------
 // A channel's points are next to one another, so lanes go along the points, VEC to a lane, and the
 // sums over channels stay inside a lane.  A work-group takes a tile of points, and its waves share
-// the channels, N each, in registers; what a point's channels sum to joins through LDS, one barrier
-// a tile.  Few waves with many channels beat many with few (64 channels as 16 waves of 4: forward
-// 539 us, as 8 waves of 8: 217, both before streaming stores).  FLAT: one point to a lane, counted
-// through all batch entries; else tiles of 64 VEC points of one entry.
+// the channels, N each, in registers; what a point's channels sum to joins through LDS, one thread
+// to a point, between two barriers (every wave adding up for itself needs only one, but reads LDS
+// for as many values as the fields have: 4 x 100 x 100003 forward 79 us instead of 66, 8 x 64 x
+// 512^2 bf16 141 instead of 124).  FLAT: one point to a lane, counted through all batch entries;
+// else tiles of 64 VEC points of one entry.
 struct Tile {
   int64_t b, p;   // batch entry and point where the tile starts (FLAT: of the lane's own point)
   uint32_t off;   // the lane's first element from there (below 64 VEC)
@@ -585,14 +586,15 @@ template <typename T, int N, int VEC, bool FLAT>
 __global__ __launch_bounds__(N <= 8 ? 512 : 1024) void k_ln_fwd_field(
     NormArgs a, int64_t tiles, int64_t per_entry, const T* x, const float* gamma,
     const float* beta, T* y, float* stats) {
-  extern __shared__ float s_mem[];  // [2][waves][2][64 VEC]
+  extern __shared__ float s_mem[];  // a tile's means and deviations, then each wave's
+  constexpr int kTile = 64 * VEC;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
   const int c0 = wave * N, nc = a.channels - c0 < N ? a.channels - c0 : N;
   const float inv_c = 1.0f / (float)a.channels, inv_n = 1.0f / (float)nc;
-  int flip = 0;
+  const auto count = [&](int w) { return (float)(a.channels - w * N < N ? a.channels - w * N : N); };
   for (Tiles<VEC, FLAT> at(tiles, per_entry, blockIdx.x, gridDim.x); at.more();
-       at.next(per_entry), flip ^= 1) {
+       at.next(per_entry)) {
     const Tile t = at.tile(a);
     const T* p = x + t.b * a.x_stride + t.p;
     float f[N][VEC], mean[VEC] = {}, sq[VEC] = {};
@@ -600,52 +602,52 @@ __global__ __launch_bounds__(N <= 8 ? 512 : 1024) void k_ln_fwd_field(
     for (int c = 0; c < N; ++c)
       unpack<T, VEC>(
           load_raw<T, VEC, true>(p + (c < nc ? c0 + c : a.channels - 1) * a.npts + t.off), f[c]);
+    by_mask(nc < N, [&](auto masked) {
 #pragma unroll
-    for (int c = 0; c < N; ++c)
+      for (int c = 0; c < N; ++c)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) mean[i] += c < nc ? f[c][i] : 0.f;
+        for (int i = 0; i < VEC; ++i) mean[i] += !masked.value || c < nc ? f[c][i] : 0.f;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) mean[i] *= inv_n;
+      for (int i = 0; i < VEC; ++i) mean[i] *= inv_n;
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float e = f[c][i] - mean[i];
-        sq[i] += c < nc ? e * e : 0.f;
-      }
-    }
-    if (waves > 1) {
-      // the waves' means and squared deviations join: M2 = sum M2_w + n_w (mean_w - mean)^2
-      float* s_t = s_mem + flip * waves * 2 * 64 * VEC;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        s_t[(wave * 2) * 64 * VEC + lane * VEC + i] = mean[i];
-        s_t[(wave * 2 + 1) * 64 * VEC + lane * VEC + i] = sq[i];
-      }
-      __syncthreads();
-      float all[VEC] = {};
-      for (int w = 0; w < waves; ++w) {
-        const float n = (float)(a.channels - w * N < N ? a.channels - w * N : N);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) all[i] += n * s_t[(w * 2) * 64 * VEC + lane * VEC + i];
-      }
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        mean[i] = all[i] * inv_c;
-        sq[i] = 0.f;
-      }
-      for (int w = 0; w < waves; ++w) {
-        const float n = (float)(a.channels - w * N < N ? a.channels - w * N : N);
+      for (int c = 0; c < N; ++c)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          const float e = s_t[(w * 2) * 64 * VEC + lane * VEC + i] - mean[i];
-          sq[i] += s_t[(w * 2 + 1) * 64 * VEC + lane * VEC + i] + n * e * e;
+          const float e = f[c][i] - mean[i];
+          sq[i] += !masked.value || c < nc ? e * e : 0.f;
         }
-      }
-    }
+    });
     float rstd[VEC];
+    if (waves > 1) {
+      // the waves' means and squared deviations join, one point to a thread
+      float *s_part = s_mem + 2 * kTile, *mine = s_part + wave * 2 * kTile + lane * VEC;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) rstd[i] = rsqrtf(sq[i] * inv_c + a.eps);
+      for (int i = 0; i < VEC; ++i) {
+        mine[i] = mean[i];
+        mine[kTile + i] = sq[i];
+      }
+      __syncthreads();
+      for (int q = threadIdx.x; q < kTile; q += blockDim.x) {
+        float all = 0.f, m2 = 0.f;
+        for (int w = 0; w < waves; ++w) all += count(w) * s_part[w * 2 * kTile + q];
+        all *= inv_c;
+        for (int w = 0; w < waves; ++w) {
+          const float e = s_part[w * 2 * kTile + q] - all;
+          m2 += s_part[(w * 2 + 1) * kTile + q] + count(w) * e * e;
+        }
+        s_mem[q] = all;
+        s_mem[kTile + q] = rsqrtf(m2 * inv_c + a.eps);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        mean[i] = s_mem[lane * VEC + i];
+        rstd[i] = s_mem[kTile + lane * VEC + i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) rstd[i] = rsqrtf(sq[i] * inv_c + a.eps);
+    }
     if (t.lo < VEC) {
       T* o = y + t.b * a.y_stride + t.p;
 #pragma unroll
@@ -672,14 +674,14 @@ __device__ __forceinline__ void bwd_field(const NormArgs& a, int64_t tiles, int6
                                           const T* x, const float* gamma, const float* stats,
                                           const T* gy, T* gx, float* part, int block,
                                           int blocks) {
-  extern __shared__ float s_mem[];  // [2][waves][2][64 VEC]
+  extern __shared__ float s_mem[];  // a tile's two sums, then each wave's
+  constexpr int kTile = 64 * VEC;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
   const int c0 = wave * N, nc = a.channels - c0 < N ? a.channels - c0 : N;
   const float inv_c = 1.0f / (float)a.channels;
   float dg[N] = {}, db[N] = {};
-  int flip = 0;
-  for (Tiles<VEC, FLAT> at(tiles, per_entry, block, blocks); at.more(); at.next(per_entry), flip ^= 1) {
+  for (Tiles<VEC, FLAT> at(tiles, per_entry, block, blocks); at.more(); at.next(per_entry)) {
     const Tile t = at.tile(a);
     const T* p = x + t.b * a.x_stride + t.p;
     const T* r = gy + t.b * a.y_stride + t.p;
@@ -711,20 +713,24 @@ __device__ __forceinline__ void bwd_field(const NormArgs& a, int64_t tiles, int6
       }
     }
     if (waves > 1) {
-      float* s_t = s_mem + flip * waves * 2 * 64 * VEC;
+      float *s_part = s_mem + 2 * kTile, *mine = s_part + wave * 2 * kTile + lane * VEC;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        s_t[(wave * 2) * 64 * VEC + lane * VEC + i] = s1[i];
-        s_t[(wave * 2 + 1) * 64 * VEC + lane * VEC + i] = s2[i];
-        s1[i] = s2[i] = 0.f;
+        mine[i] = s1[i];
+        mine[kTile + i] = s2[i];
       }
       __syncthreads();
-      for (int w = 0; w < waves; ++w)
+      for (int q = threadIdx.x; q < 2 * kTile; q += blockDim.x) {
+        float v = 0.f;
+        for (int w = 0; w < waves; ++w) v += s_part[w * 2 * kTile + q];
+        s_mem[q] = v;
+      }
+      __syncthreads();
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          s1[i] += s_t[(w * 2) * 64 * VEC + lane * VEC + i];
-          s2[i] += s_t[(w * 2 + 1) * 64 * VEC + lane * VEC + i];
-        }
+      for (int i = 0; i < VEC; ++i) {
+        s1[i] = s_mem[lane * VEC + i];
+        s2[i] = s_mem[kTile + lane * VEC + i];
+      }
     }
     if (gx && t.lo < VEC) {
       T* o = gx + t.b * a.gx_stride + t.p;
@@ -974,14 +980,20 @@ int bwd_rows_groups(int64_t rows) {
   return (int)cut(ceil_div(rows, kBwdBlock / TPR), 256);
 }
 
-// fields: channels to a wave, at most 8 for up to 64 channels (and so at most 8 waves)
+// Fields: channels to a wave, at most 8 for up to 64 channels (and so at most 8 waves).
 int field_n(int c) {
   if (c <= 64) return (int)ceil_div(c, ceil_div(c, 8));
   return c <= 100 ? 10 : c <= 120 ? 12 : 16;
 }
+// The float32 forward goes on with six waves of up to 12 from 49 channels on (8 x 64 x 512^2: 193 us
+// against 206 as eight waves of 8; bf16 130 against 123).
+template <typename T>
+int field_fwd_n(int c) {
+  return sizeof(T) == 4 && c > 48 && c <= 72 ? 12 : field_n(c);
+}
 template <typename F>
-void pick_field(int c, F&& f) {
-  switch (field_n(c)) {
+void pick_field(int n, F&& f) {
+  switch (n) {
     case 1: return f(Int<1>());
     case 2: return f(Int<2>());
     case 3: return f(Int<3>());
@@ -995,8 +1007,9 @@ void pick_field(int c, F&& f) {
     default: return f(Int<16>());
   }
 }
+
 // Points to a lane.  Forward: 4 (8 of a half type, whole 16-byte loads, spill: 8 x 64 x 512^2 bf16
-// 202 us against 140).  Backward, with twice the registers: 2 (4: 496 us against 322 on
+// 202 us against 141).  Backward, with twice the registers: 2 (4: 496 us against 322 on
 // 8 x 64 x 512^2 float32, before streaming stores), 1 beyond 10 channels a wave.
 template <typename T>
 constexpr int kFwdVec = 4;
@@ -1017,7 +1030,7 @@ FieldShape field_shape(const NormArgs& a, int n, int wide) {
   s.waves = (int)ceil_div(a.channels, n);
   s.per_entry = ceil_div(a.npts, 64 * vec);
   s.tiles = s.flat ? ceil_div(a.batch * a.npts, 64) : a.batch * s.per_entry;
-  s.lds = s.waves > 1 ? sizeof(float) * 2 * s.waves * 2 * 64 * vec : 0;
+  s.lds = s.waves > 1 ? sizeof(float) * (1 + s.waves) * 2 * 64 * vec : 0;
   return s;
 }
 int field_bwd_groups(const FieldShape& s) { return (int)cut(s.tiles, ceil_div(8192, s.waves)); }
@@ -1056,7 +1069,7 @@ hipError_t fwd_t(NormArgs a, const T* x, const float* gamma, const float* beta, 
                          beta, y, stats);
       break;
     case kField:
-      pick_field(a.channels, [&](auto n) {
+      pick_field(field_fwd_n<T>(a.channels), [&](auto n) {
         const FieldShape f = field_shape(a, n.value, kFwdVec<T>);
         const dim3 grid(cut(f.tiles, 1 << 20)), block(64 * f.waves);
         if (f.flat)
@@ -1087,7 +1100,7 @@ int groups_t(const NormArgs& a) {
     }
     case kField: {
       int n = 0;
-      pick_field(a.channels, [&](auto c) {
+      pick_field(field_n(a.channels), [&](auto c) {
         n = field_bwd_groups(field_shape(a, c.value, kBwdVec<T, c.value>));
       });
       return n;
@@ -1154,7 +1167,7 @@ hipError_t bwd_t(NormArgs a, const T* x, const float* gamma, const float* stats,
       });
       break;
     case kField:
-      pick_field(a.channels, [&](auto n) {
+      pick_field(field_n(a.channels), [&](auto n) {
         constexpr int N = n.value, kWide = kBwdVec<T, N>;
         const FieldShape f = field_shape(a, N, kWide);
         const auto go = [&](auto vec, auto flat) {
