@@ -18,9 +18,10 @@
 //   rows    8192 x 4096 bf16       forward  24 us (5.6 TB/s)   backward  40 us (5.1)
 //           8192 x 4096 float32    forward  42 us (6.4)        backward  69 us (5.8)
 //           16384 x 1024 bf16      forward  14 us (4.8)        backward  23 us (4.4)
-//   fields  8 x 64 x 512^2 float32 forward 193 us (5.7)        backward 288 us (5.7)
-//           2 x 20 x 128^3 float32 forward 140 us (5.0)        backward 200 us (5.2)
+//   fields  8 x 64 x 512^2 float32 forward 186 us (5.9)        backward 288 us (5.7)
+//           2 x 20 x 128^3 float32 forward 135 us (5.2)        backward 200 us (5.2)
 //           8 x 64 x 512^2 bf16    forward 123 us (4.5)        backward 166 us (5.0)
+#include <algorithm>
 #include <type_traits>
 
 #include "train_device.h"
@@ -980,20 +981,16 @@ int bwd_rows_groups(int64_t rows) {
   return (int)cut(ceil_div(rows, kBwdBlock / TPR), 256);
 }
 
-// Fields: channels to a wave, at most 8 for up to 64 channels (and so at most 8 waves).
+// Fields: channels to a wave, at most 8 for up to 64 channels (and so at most 8 waves).  Float32
+// forward with up to 12 from 49 channels on: 4 x 64 x 300000 126 us against 123, 2 x 64 x 1024^2 200
+// against 193, 8 x 50 x 512^2 149 against 148.
 int field_n(int c) {
   if (c <= 64) return (int)ceil_div(c, ceil_div(c, 8));
   return c <= 100 ? 10 : c <= 120 ? 12 : 16;
 }
-// The float32 forward goes on with six waves of up to 12 from 49 channels on (8 x 64 x 512^2: 193 us
-// against 206 as eight waves of 8; bf16 130 against 123).
-template <typename T>
-int field_fwd_n(int c) {
-  return sizeof(T) == 4 && c > 48 && c <= 72 ? 12 : field_n(c);
-}
 template <typename F>
-void pick_field(int n, F&& f) {
-  switch (n) {
+void pick_field(int c, F&& f) {
+  switch (field_n(c)) {
     case 1: return f(Int<1>());
     case 2: return f(Int<2>());
     case 3: return f(Int<3>());
@@ -1049,6 +1046,17 @@ bool stream_out(const NormArgs& a, const T* out, int64_t stride) {
          reinterpret_cast<uintptr_t>(out) % 128 == 0;
 }
 
+// Dynamic LDS that keeps a compute unit (160 KB) from holding more work-groups than make up
+// `most` waves.  The float32 forward that streams its output does better with 16 waves than with the
+// 24 to 28 that fit: 8 x 64 x 512^2 186 us against 205, 8 x 72 x 512^2 216 against 228, 2 x 20 x 128^3
+// 135 against 140, 32 x 64 x 256^2 186 against 185, 1 x 64 x 2^21 198 against 193.  Outputs that the
+// cache takes, and half ones, want all the waves: 16 x 32 x 256^2 49.2 against 48.5, 8 x 20 x 300001 75
+// against 72, 8 x 64 x 512^2 bf16 134 against 123.
+size_t lds_for_waves(int waves, int most) {
+  const size_t groups = (size_t)ceil_div(most, waves), total = 160 << 10;
+  return std::min(total / (groups + 1) / 512 * 512 + 512, (size_t)64 << 10);
+}
+
 template <typename T>
 hipError_t fwd_t(NormArgs a, const T* x, const float* gamma, const float* beta, T* y,
                  float* stats, hipStream_t s) {
@@ -1069,8 +1077,9 @@ hipError_t fwd_t(NormArgs a, const T* x, const float* gamma, const float* beta, 
                          beta, y, stats);
       break;
     case kField:
-      pick_field(field_fwd_n<T>(a.channels), [&](auto n) {
-        const FieldShape f = field_shape(a, n.value, kFwdVec<T>);
+      pick_field(a.channels, [&](auto n) {
+        FieldShape f = field_shape(a, n.value, kFwdVec<T>);
+        if (sizeof(T) == 4 && a.stream) f.lds = std::max(f.lds, lds_for_waves(f.waves, 16));
         const dim3 grid(cut(f.tiles, 1 << 20)), block(64 * f.waves);
         if (f.flat)
           hipLaunchKernelGGL((k_ln_fwd_field<T, n.value, 1, true>), grid, block, f.lds, s, a,
@@ -1100,7 +1109,7 @@ int groups_t(const NormArgs& a) {
     }
     case kField: {
       int n = 0;
-      pick_field(field_n(a.channels), [&](auto c) {
+      pick_field(a.channels, [&](auto c) {
         n = field_bwd_groups(field_shape(a, c.value, kBwdVec<T, c.value>));
       });
       return n;
@@ -1167,7 +1176,7 @@ hipError_t bwd_t(NormArgs a, const T* x, const float* gamma, const float* stats,
       });
       break;
     case kField:
-      pick_field(field_n(a.channels), [&](auto n) {
+      pick_field(a.channels, [&](auto n) {
         constexpr int N = n.value, kWide = kBwdVec<T, N>;
         const FieldShape f = field_shape(a, N, kWide);
         const auto go = [&](auto vec, auto flat) {

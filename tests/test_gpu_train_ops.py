@@ -122,6 +122,35 @@ def test_layer_norm(shape, dtype):
     assert all(torch.equal(got[k], again[k]) for k in got)
 
 
+# widths and extents at which another kernel, vector width or number of waves takes over
+EDGES = [(3, d) for d in (7, 8, 9, 15, 16, 63, 128, 129, 512, 513, 2048, 4097, 8191, 8193, 12288,
+                          16383, 16385)] + \
+    [(n, 96) for n in (511, 512, 513)] + \
+    [(2, c, p) for c in (8, 9, 48, 49, 72, 73, 101, 120, 121, 255) for p in (255, 256, 261)] + \
+    [(1, 20, 21503), (1, 20, 21505), (3, 24, 255), (13, 24, 255), (1, 3, 1), (6, 257, 2)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("shape", EDGES, ids=str)
+def test_layer_norm_edges(shape, dtype):
+    L = _L()
+    announce("layer_norm edges", shape, dtype)
+    g = _gen(sum(shape))
+    x, gy = (_randn(g, *shape) - 0.4).to(dtype), _randn(g, *shape).to(dtype)
+    gamma, beta = 1 + 0.3 * _randn(g, shape[1]), 0.3 * _randn(g, shape[1])
+    y, stats = L.layer_norm_fwd(x, gamma, beta, EPS)
+    _check_fwd(x, gamma, beta, y, stats)
+    _check_bwd(x, gamma, gy, L.layer_norm_bwd(x, gamma, stats, gy))
+    # in place, and the weight gradients alone: the same bits
+    want = L.layer_norm_bwd(x, gamma, stats, gy)
+    alone = L.layer_norm_bwd(x, gamma, stats, gy, want=("gamma", "beta"))
+    over = gy.clone()
+    got = L.layer_norm_bwd(x, gamma, stats, over, out={"x": over})
+    assert torch.equal(over, want["x"])
+    for k in ("gamma", "beta"):
+        assert torch.equal(got[k], want[k]) and torch.equal(alone[k], want[k])
+
+
 @pytest.mark.parametrize("shape", [(37, 257), (5, 4100), (3, 20, 130), (2, 300, 70)], ids=str)
 def test_layer_norm_optional_arguments(shape):
     L = _L()
