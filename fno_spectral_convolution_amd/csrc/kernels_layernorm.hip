@@ -20,7 +20,7 @@
 //           16384 x 1024 bf16      forward  14 us (4.8)        backward  23 us (4.4)
 //   fields  8 x 64 x 512^2 float32 forward 186 us (5.9)        backward 288 us (5.7)
 //           2 x 20 x 128^3 float32 forward 135 us (5.2)        backward 200 us (5.2)
-//           8 x 64 x 512^2 bf16    forward 123 us (4.5)        backward 166 us (5.0)
+//           8 x 64 x 512^2 bf16    forward 124 us (4.4)        backward 166 us (5.0)
 #include <algorithm>
 #include <type_traits>
 
