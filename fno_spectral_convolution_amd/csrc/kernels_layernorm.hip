@@ -1046,12 +1046,14 @@ bool stream_out(const NormArgs& a, const T* out, int64_t stride) {
          reinterpret_cast<uintptr_t>(out) % 128 == 0;
 }
 
-// Dynamic LDS that keeps a compute unit (160 KB) from holding more work-groups than make up
-// `most` waves.  The float32 forward that streams its output does better with 16 waves than with the
-// 24 to 28 that fit: 8 x 64 x 512^2 186 us against 205, 8 x 72 x 512^2 216 against 228, 2 x 20 x 128^3
-// 135 against 140, 32 x 64 x 256^2 186 against 185, 1 x 64 x 2^21 198 against 193.  Outputs that the
-// cache takes, and half ones, want all the waves: 16 x 32 x 256^2 49.2 against 48.5, 8 x 20 x 300001 75
-// against 72, 8 x 64 x 512^2 bf16 134 against 123.
+// Dynamic LDS that keeps a compute unit (160 KB) from holding more work-groups than make up `most`
+// waves.  The float32 forward that streams its output does better with 16 waves than with the 24 to
+// 28 that fit: 8 x 64 x 512^2 186 us against 205, 8 x 72 x 512^2 216 against 228, 2 x 20 x 128^3 135
+// against 140, 8 x 32 x 500000 180 against 187, but 1 x 64 x 2^21 198 against 193 and 8 x 32 x 2^19
+// 244 against 229 (planes a power of two apart share memory channels).  12 and 8 waves gain nothing
+// more and cost narrow fields up to 15%.  The backward's registers limit its waves already.  Outputs
+// that the cache takes, and half ones, want all the waves: 16 x 32 x 256^2 49.2 against 48.5, 8 x 20
+// x 300001 75 against 72, 8 x 64 x 512^2 bf16 134 against 123.
 size_t lds_for_waves(int waves, int most) {
   const size_t groups = (size_t)ceil_div(most, waves), total = 160 << 10;
   return std::min(total / (groups + 1) / 512 * 512 + 512, (size_t)64 << 10);
@@ -1066,8 +1068,11 @@ hipError_t fwd_t(NormArgs a, const T* x, const float* gamma, const float* beta, 
       pick_rows<T>(a.channels, [&](auto vec, auto tpr, auto nv) {
         constexpr int kBlock = tpr.value < 256 ? 256 : tpr.value;
         constexpr auto kernel = k_ln_fwd_rows<T, vec.value, tpr.value, nv.value, kBlock>;
-        const int64_t need = ceil_div(a.batch, kBlock / tpr.value), most = resident<kernel>(kBlock);
-        // as many rounds as that takes, shared out evenly
+        // As many rounds as the resident work-groups take, shared out evenly; half of them where the
+        // output streams to memory: 65536 x 4096 bf16 177 us against 191, 262144 x 1024 176 against
+        // 197, 16384 x 8192 float32 183 against 189, 131072 x 1024 196 against 195.
+        const int64_t need = ceil_div(a.batch, kBlock / tpr.value);
+        const int64_t most = resident<kernel>(kBlock) / (a.stream ? 2 : 1);
         const int64_t groups = ceil_div(need, ceil_div(need, most));
         hipLaunchKernelGGL(kernel, dim3(groups), dim3(kBlock), 0, s, a, x, gamma, beta, y, stats);
       });

@@ -324,6 +324,44 @@ def test_layer_norm_offsets_past_32_bits():
     assert torch.equal(y[:, :, :4096], y0) and torch.equal(y[:, :, -4096:], y0)
 
 
+@pytest.mark.parametrize("shape,dtype", [
+    ((70_001, 2048), torch.bfloat16), ((17_001, 4096), torch.float32), ((140_003, 512), torch.float32),
+    ((5, 64, 262_144), torch.float32), ((3, 20, 1_200_032), torch.float32), ((9, 17, 500_000), torch.float32),
+    ((3, 40, 1_200_064), torch.bfloat16)], ids=str)
+def test_layer_norm_outputs_past_the_cache(shape, dtype):
+    """Outputs over 256 MB, which go past the caches: the bits of calls on parts of the batch."""
+    L = _L()
+    announce("layer_norm large", shape, dtype)
+    g = _gen(sum(shape))
+    x, gy = (_randn(g, *shape) - 0.4).to(dtype), _randn(g, *shape).to(dtype)
+    assert x.numel() * x.element_size() > 256 << 20
+    gamma, beta = 1 + 0.3 * _randn(g, shape[1]), 0.3 * _randn(g, shape[1])
+    y, stats = L.layer_norm_fwd(x, gamma, beta, EPS)
+    got = L.layer_norm_bwd(x, gamma, stats, gy)
+    sums = {k: torch.zeros(shape[1], dtype=torch.float64, device="cuda") for k in ("gamma", "beta")}
+    mags = {k: torch.zeros_like(v) for k, v in sums.items()}
+    step = max(1, shape[0] // 3)
+    for at in range(0, shape[0], step):
+        part = slice(at, min(at + step, shape[0]))
+        yp, sp = L.layer_norm_fwd(x[part], gamma, beta, EPS)
+        assert torch.equal(y[part], yp)
+        assert all(torch.equal(a[part], b) for a, b in zip(stats, sp))
+        assert torch.equal(got["x"][part], L.layer_norm_bwd(x[part], gamma, sp, gy[part], want=("x",))["x"])
+        few = slice(at, min(at + 1, shape[0])) if x.dim() > 2 else slice(at, at + 100)
+        _check_fwd(x[few], gamma, beta, y[few], [v[few] for v in stats])
+        for b in range(part.start, part.stop, 1 if x.dim() > 2 else 10_000):
+            c = slice(b, min(b + (1 if x.dim() > 2 else 10_000), part.stop))
+            _, _, _, h, kappa = _norm64(x[c], gamma, beta, EPS)
+            up = gy[c].double()
+            rows = [0] + list(range(2, x.dim()))
+            sums["gamma"] += (up * h).sum(rows)
+            mags["gamma"] += (up.abs() * (h.abs() + kappa)).sum(rows)
+            sums["beta"] += up.sum(rows)
+            mags["beta"] += up.abs().sum(rows)
+    for k in ("gamma", "beta"):
+        _close("grad_" + k, got[k], sums[k], 128 * U * mags[k])
+
+
 # ---- tensor lists ------------------------------------------------------------------------------
 def _norm_of(ts):
     return math.sqrt(sum(float((t.abs() if t.is_complex() else t).double().square().sum())
@@ -431,6 +469,27 @@ def test_grad_norm_complex_and_repeated():
     want = w * (0.5 / _norm_of([w]))
     L.clip_grad_norm([w], 0.5)
     assert float((w - want).abs().max()) <= 8 * U * float(want.abs().max())
+
+
+@pytest.mark.parametrize("dtype,wide", [(torch.float32, False), (torch.bfloat16, False),
+                                        (torch.float16, True)], ids=str)
+def test_clip_past_the_cache(dtype, wide):
+    """Outputs over 256 MB, which go past the caches."""
+    L = _L()
+    announce("clip large", dtype, wide)
+    g = _gen(9)
+    ts = [(_randn(g, n) * 0.1).to(dtype) for n in (50_000_003, 1, 90_000_001, 4097)]
+    outs = [torch.empty(t.shape, dtype=torch.float32 if wide else dtype, device="cuda") for t in ts]
+    assert sum(o.numel() * o.element_size() for o in outs) > 256 << 20
+    norm = _norm_of(ts)
+    rec = L.clip_grad_norm(ts, norm / 2, 8.0, out=outs).double().tolist()
+    # norm / 8 stays below norm / 2: the factor is the scale's, exact
+    assert abs(rec[0] - norm / 8) <= 4 * U * norm / 8 and rec[1] == 0.125
+    for t, o in zip(ts, outs):
+        assert torch.equal(o, (t.float() * 0.125).to(o.dtype))
+    L.clip_grad_norm(ts, norm / 2, 8.0)
+    for t, o in zip(ts, outs):
+        assert torch.equal(t, o.to(dtype))
 
 
 def test_grad_norm_past_32_bits():
