@@ -12,10 +12,10 @@
 // nothing (float32 sums measured the same).  Its order is fixed by the list and the work-groups.
 //
 // Measured on an MI355X whose large copies run at 4.9 TB/s:
-//   norm   300 MB of half gradients 57 us (5.2 TB/s), 400 MB of float32 73 us (5.5)
+//   norm   300 MB of half gradients 50 us (6.0 TB/s), 400 MB of float32 65 us (6.2)
 //   clip   301 half tensors, 150 million entries, into float32, with its norm 217 us (its own 900 MB
 //          163 us, 5.5 TB/s; the norm reads 300 MB before)
-//   AdamW  52 million float32 entries 276 us (5.3 TB/s), with the norm before it 351 us: what the
+//   AdamW  52 million float32 entries 276 us (5.3 TB/s), with the norm before it 342 us: what the
 //          update wrote last is still on its way out of the 256 MB cache while the next norm reads
 #include <algorithm>
 
@@ -78,7 +78,7 @@ __device__ __forceinline__ void each_span(const TensorTable& t, F&& f) {
 }
 
 // Elements of a span until one lies on a 128-byte line: vectors from there on do not straddle
-// lines (reads of half gradients packed at odd places 66 -> 57 us for 300 MB), and what is written
+// lines (reads of half gradients packed at odd places 66 -> 58 us for 300 MB), and what is written
 // goes in whole lines.
 template <typename T>
 __device__ __forceinline__ int lead_of(Global<T> p, int n) {
@@ -99,7 +99,7 @@ __device__ __forceinline__ double squares(const Raw<T, V>& q) {
   return a;
 }
 
-template <typename T>
+template <typename T, bool Stream>
 __device__ __forceinline__ double sum_squares(Global<const T> p, int n) {
   constexpr int V = 16 / (int)sizeof(T);
   double a[kAhead] = {};
@@ -116,25 +116,26 @@ __device__ __forceinline__ double sum_squares(Global<const T> p, int n) {
   for (; i + (kAhead - 1) * kThreads < nv; i += kAhead * kThreads) {
     Raw<T, V> q[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) q[u] = load_global<T, V>(p + (i + u * kThreads) * V);
+    for (int u = 0; u < kAhead; ++u) q[u] = load_global<T, V, Stream>(p + (i + u * kThreads) * V);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) a[u] += squares<T, V>(q[u]);
   }
-  for (; i < nv; i += kThreads) a[0] += squares<T, V>(load_global<T, V>(p + i * V));
+  for (; i < nv; i += kThreads) a[0] += squares<T, V>(load_global<T, V, Stream>(p + i * V));
   double s = 0.0;
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) s += a[u];
   return s;
 }
 
+template <bool Stream>
 __global__ __launch_bounds__(kThreads) void k_norm_part(TensorTable t, double* part) {
   __shared__ double s_red[kThreads / 64];
   double a = 0.0;
   each_span(t, [&](uint32_t k, int64_t at, int n) {
     const uint32_t d = uniform((uint32_t)t.entry[k].dtype);
-    if (d == FNO_DTYPE_F32) a += sum_squares<float>(data_of<const float>(t, k, at), n);
-    else if (d == FNO_DTYPE_BF16) a += sum_squares<__bf16>(data_of<const __bf16>(t, k, at), n);
-    else a += sum_squares<_Float16>(data_of<const _Float16>(t, k, at), n);
+    if (d == FNO_DTYPE_F32) a += sum_squares<float, Stream>(data_of<const float>(t, k, at), n);
+    else if (d == FNO_DTYPE_BF16) a += sum_squares<__bf16, Stream>(data_of<const __bf16>(t, k, at), n);
+    else a += sum_squares<_Float16, Stream>(data_of<const _Float16>(t, k, at), n);
   });
   a = group_sum(a, s_red);
   if (threadIdx.x == 0) part[blockIdx.x] = a;
@@ -304,8 +305,15 @@ int write_groups(const TensorTable& t, bool stream) {
 
 }  // namespace
 
-hipError_t launch_norm_part(const TensorTable& t, int groups, double* part, hipStream_t s) {
-  hipLaunchKernelGGL(k_norm_part, dim3(groups), dim3(kThreads), 0, s, t, part);
+// A norm by itself reads a list of more than 128 MB past the caches: 300 MB of half gradients 50 us
+// against 58, 600 MB of float32 93 against 107, and so with the AdamW update behind it (52 million
+// float32 entries 339 against 346, 150 million 948 against 977; at 100 MB 165 against 162, at 40 MB 74
+// against 71).  Where a clip reads the same gradients next, it finds a part of them in the caches:
+// 150 million half entries into float32 211 us with plain loads, 233 without.
+hipError_t launch_norm_part(const TensorTable& t, int groups, double* part, bool again,
+                            hipStream_t s) {
+  const auto kernel = !again && t.bytes > ((int64_t)128 << 20) ? k_norm_part<true> : k_norm_part<false>;
+  hipLaunchKernelGGL(kernel, dim3(groups), dim3(kThreads), 0, s, t, part);
   return hipGetLastError();
 }
 

@@ -1885,9 +1885,10 @@ size_t norm_parts_bytes(const fno_tensor_list* l) {
   return align_up(sizeof(double) * (size_t)std::max(norm_groups(l), 1));
 }
 
-// Checks of the norm's arguments, and the partial sums into the workspace.
+// Checks of the norm's arguments, and the partial sums into the workspace; again: the gradients are
+// read once more by the same call.
 fno_status norm_parts(const fno_tensor_list* grads, float max_norm, float grad_scale,
-                      const float* record, void* ws, size_t ws_bytes, hipStream_t s,
+                      const float* record, void* ws, size_t ws_bytes, bool again, hipStream_t s,
                       fno::NormRecord* r) {
   if (!(max_norm > 0.0f)) return fail(FNO_ERR_INVALID_ARGUMENT, "max_norm must be > 0");
   if (!(grad_scale > 0.0f) || !std::isfinite(grad_scale))
@@ -1899,14 +1900,15 @@ fno_status norm_parts(const fno_tensor_list* grads, float max_norm, float grad_s
   *r = {norm_groups(grads), max_norm, grad_scale};
   if (r->nparts > 0)
     LAUNCH("grad_norm", s,
-           fno::launch_norm_part(grads->table, r->nparts, static_cast<double*>(ws), s));
+           fno::launch_norm_part(grads->table, r->nparts, static_cast<double*>(ws), again, s));
   return FNO_OK;
 }
 
 fno_status finish_norm(const fno_tensor_list* grads, float max_norm, float grad_scale,
                        float* record, void* ws, size_t ws_bytes, hipStream_t s) {
   fno::NormRecord r;
-  const fno_status st = norm_parts(grads, max_norm, grad_scale, record, ws, ws_bytes, s, &r);
+  const fno_status st =
+      norm_parts(grads, max_norm, grad_scale, record, ws, ws_bytes, false, s, &r);
   if (st != FNO_OK) return st;
   LAUNCH("grad_norm_finish", s,
          fno::launch_norm_finish(static_cast<const double*>(ws), r, record, s));
@@ -2082,7 +2084,7 @@ fno_status fno_clip_grad_norm(const fno_tensor_list* grads, const fno_tensor_lis
   if (grads->table.chunks == 0)
     return finish_norm(grads, max_norm, grad_scale, record, ws, ws_bytes, s);
   fno::NormRecord r;
-  st = norm_parts(grads, max_norm, grad_scale, record, ws, ws_bytes, s, &r);
+  st = norm_parts(grads, max_norm, grad_scale, record, ws, ws_bytes, true, s, &r);
   if (st != FNO_OK) return st;
   LAUNCH("grad_clip", s,
          fno::launch_clip(grads->table, out->table, static_cast<const double*>(ws), r, record, s));

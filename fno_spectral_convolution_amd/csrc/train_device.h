@@ -84,10 +84,11 @@ __device__ __forceinline__ void store_pack(T* p, const float (&f)[N], bool strea
 // as such they would be read with flat instructions, which also occupy the LDS.
 template <typename T>
 using Global = T __attribute__((address_space(1)))*;
-template <typename T, int N>
+template <typename T, int N, bool Stream = false>
 __device__ __forceinline__ Raw<T, N> load_global(Global<const T> p) {
   typedef typename RawVector<T, N>::unaligned V;
-  return *(Global<const V>)p;
+  if constexpr (Stream) return __builtin_nontemporal_load((Global<const V>)p);
+  else return *(Global<const V>)p;
 }
 template <typename T, int N>
 __device__ __forceinline__ void store_global(Global<T> p, const float (&f)[N], bool stream) {

@@ -51,8 +51,10 @@ struct NormRecord {
 // most partial sums of the norm: eight work-groups of four waves fill a compute unit
 constexpr int kNormParts = 2048;
 
-// one partial sum of squares per work-group into part[0 .. groups)
-hipError_t launch_norm_part(const TensorTable& t, int groups, double* part, hipStream_t s);
+// one partial sum of squares per work-group into part[0 .. groups); again: the call's next launch
+// reads the tensors once more
+hipError_t launch_norm_part(const TensorTable& t, int groups, double* part, bool again,
+                            hipStream_t s);
 hipError_t launch_norm_finish(const double* part, const NormRecord& r, float* record,
                               hipStream_t s);
 // writes the record too
