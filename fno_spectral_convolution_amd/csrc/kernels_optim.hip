@@ -15,8 +15,8 @@
 //   norm   300 MB of half gradients 50 us (6.0 TB/s), 400 MB of float32 65 us (6.2)
 //   clip   301 half tensors, 150 million entries, into float32, with its norm 217 us (its own 900 MB
 //          163 us, 5.5 TB/s; the norm reads 300 MB before)
-//   AdamW  52 million float32 entries 276 us (5.3 TB/s), with the norm before it 342 us: what the
-//          update wrote last is still on its way out of the 256 MB cache while the next norm reads
+//   AdamW  52 million float32 entries 304 us (4.8 TB/s), with the norm before it 342 us: what the
+//          update before wrote last leaves the 256 MB cache meanwhile
 #include <algorithm>
 
 #include "train_device.h"
