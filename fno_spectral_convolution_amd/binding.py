@@ -835,6 +835,12 @@ def _vector(t, shape, index, name):
     return t.data_ptr()
 
 
+def _workspace(ws, index):
+    """A caller's workspace: the library sees its address and size alone."""
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"ws: needs packed memory on cuda:{index}")
+
+
 class _NormShape:
     """What a layer norm call needs to know of the shapes and strides of its fields: worked out
     once for each combination, as a plan's is."""
@@ -909,8 +915,8 @@ def layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, out=None, stats=None, wan
 
 def layer_norm_bwd(x, gamma, stats, grad_y, want=("x", "gamma", "beta"), out=None, ws=None):
     """Gradients of layer_norm_fwd from its x and stats: dict(x, gamma, beta), None where not
-    asked.  out: tensors to write instead of new ones (out["x"] may be grad_y itself).  ws: uint8
-    workspace of fno_layer_norm_workspace_bytes (allocated when None)."""
+    asked.  out: tensors to write instead of new ones (out["x"] may be grad_y itself).  ws: packed
+    workspace of fno_layer_norm_workspace_bytes on x's device (allocated when None)."""
     gy_strides = _like_x(grad_y, x, "grad_y")
     o = out or {}
     gx = o["x"] if "x" in o else x.new_empty(x.shape) if "x" in want else None
@@ -919,8 +925,10 @@ def layer_norm_bwd(x, gamma, stats, grad_y, want=("x", "gamma", "beta"), out=Non
     index = _on_gpu(x)
     gg, gb = (o[k] if k in o else x.new_empty(n.channels, dtype=_torch.float32) if k in want
               else None for k in ("gamma", "beta"))
-    if ws is None and n.ws_bytes:
-        ws = x.new_empty(n.ws_bytes, dtype=_torch.uint8)
+    if ws is None:
+        ws = x.new_empty(n.ws_bytes, dtype=_torch.uint8) if n.ws_bytes else None
+    else:
+        _workspace(ws, index)
     _check(_on_stream(index, _lib.fno_layer_norm_bwd, n.ptr, x.data_ptr(),
                       _vector(gamma, n.channels, index, "gamma"),
                       _vector(stats, n.stats, index, "stats"), grad_y.data_ptr(), _ptr(gx),
@@ -992,8 +1000,8 @@ def _norm_buffers(gl, record, ws):
         _vector(record, _RECORD, gl.index, "record")
     if ws is None:
         ws = gl.table.new_empty(gl.norm_ws_bytes)
-    elif ws.get_device() != gl.index or not ws.is_contiguous():
-        raise ValueError(f"ws: needs packed memory on {gl.device}")
+    else:
+        _workspace(ws, gl.index)
     return record, ws
 
 

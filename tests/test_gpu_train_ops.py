@@ -704,3 +704,15 @@ def test_graph_replays_match_eager():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(_outputs(eager), _outputs(cap))), k
+
+
+def test_norm_workspace_refused():
+    """A workspace that is not packed memory of the fields' device; no call goes out."""
+    L = _L()
+    announce("layer_norm workspace refusals")
+    x, st = torch.zeros(2, 8, 1 << 16, device="cuda"), torch.zeros(2, 2, 1 << 16, device="cuda")
+    for ws in (torch.zeros(1 << 20, dtype=torch.uint8),
+               torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 20),
+               torch.zeros(2 << 20, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="ws"):
+            L.layer_norm_bwd(x, None, st, x, ws=ws)

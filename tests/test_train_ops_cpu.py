@@ -175,3 +175,32 @@ def test_binding_refuses():
         L.TensorList([x])
     with pytest.raises(ValueError, match="GPU"):
         L.grad_norm([x])
+
+
+@pytest.mark.parametrize("ws", [
+    torch.zeros(1, dtype=torch.uint8).expand(1 << 20),  # more elements than it has memory
+    torch.zeros(2 << 20, dtype=torch.uint8)[::2],
+], ids=["expanded", "strided"])
+def test_norm_workspace_is_packed_memory_of_the_device(ws, monkeypatch):
+    """The library sees an address and a size alone: whether they are memory of the device is the
+    binding's to ask.  CPU tensors stand for the GPU's, and no call goes out."""
+    calls = []
+    monkeypatch.setattr(L, "_on_gpu", lambda x: x.get_device())
+    monkeypatch.setattr(L, "_on_stream", lambda index, fn, *args: calls.append(args) or L.FNO_OK)
+    x, stats = torch.zeros(2, 8, 1 << 16), torch.zeros(2, 2, 1 << 16)
+    good = torch.zeros(1 << 20, dtype=torch.uint8)
+    L.layer_norm_bwd(x, None, stats, x, ws=good)
+    assert len(calls) == 1
+    with pytest.raises(ValueError, match="ws"):
+        L.layer_norm_bwd(x, None, stats, x, ws=ws)
+    assert len(calls) == 1
+
+
+def test_norm_workspace_on_another_device(monkeypatch):
+    calls = []
+    monkeypatch.setattr(L, "_on_gpu", lambda x: 0)
+    monkeypatch.setattr(L, "_on_stream", lambda index, fn, *args: calls.append(args) or L.FNO_OK)
+    x = torch.zeros(2, 8, 1 << 16)
+    with pytest.raises(ValueError, match="ws"):
+        L.layer_norm_bwd(x, None, None, x, want=("x",), ws=torch.zeros(1 << 20, dtype=torch.uint8))
+    assert not calls
