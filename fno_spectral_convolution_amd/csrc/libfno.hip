@@ -1790,12 +1790,14 @@ fno_status norm_args(const fno_layer_norm_desc* d, fno::NormArgs* a) {
     return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: eps must be finite and >= 0");
   if (d->channels >= (int64_t)1 << 31)
     return fail(FNO_ERR_UNSUPPORTED, "layer norm: channels >= 2^31");
-  // every byte offset into every operand fits 62 bits
+  // every byte offset into every operand fits 62 bits, and so do the bytes of all elements (strides
+  // of 0 keep offsets below those)
   const int64_t lim = (int64_t)1 << 60;
-  int64_t per, rows, span;
+  int64_t per, rows, all, span;
   const int64_t st = std::max(std::max(d->x_stride, d->y_stride), d->grad_x_stride);
   if (__builtin_mul_overflow(d->channels, d->npts, &per) || per > lim ||
       __builtin_mul_overflow(d->batch, d->npts, &rows) || rows > lim ||
+      __builtin_mul_overflow(rows, d->channels, &all) || all > lim ||
       __builtin_mul_overflow(d->batch, st, &span) || span > lim)
     return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: sizes overflow");
   a->batch = d->batch;

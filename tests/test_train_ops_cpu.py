@@ -204,3 +204,17 @@ def test_norm_workspace_on_another_device(monkeypatch):
     with pytest.raises(ValueError, match="ws"):
         L.layer_norm_bwd(x, None, None, x, want=("x",), ws=torch.zeros(1 << 20, dtype=torch.uint8))
     assert not calls
+
+
+@pytest.mark.parametrize("kw", [
+    dict(batch=1 << 40, channels=1 << 20, npts=1 << 20),
+    dict(batch=1 << 31, channels=(1 << 31) - 1, npts=1),
+    dict(batch=1 << 58, channels=8, npts=1),
+])
+def test_layer_norm_of_too_many_elements_refused(kw):
+    """Strides of 0 keep every offset small: the number of elements has its own limit, 2^60."""
+    d = _desc(x_stride=0, y_stride=0, grad_x_stride=0, **kw)
+    n = ctypes.c_size_t()
+    assert L._lib.fno_layer_norm_workspace_bytes(d, ctypes.byref(n)) == BAD
+    assert _fwd(d) == BAD and _bwd(d, gx=None) == BAD
+    assert "overflow" in L.last_error_message()
