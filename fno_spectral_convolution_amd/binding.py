@@ -1036,7 +1036,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.999), eps=
           weight_decay=0.01, record=None):
     """One AdamW update, number `step` (from 1), of float32 (or complex64, as pairs) parameters in
     place, from gradients times the factor of `record` (grad_norm's; None: as they are).  A factor
-    that is not finite leaves parameters and moments as they are."""
+    that is not finite leaves parameters and moments as they are.  A captured call replays this
+    step's number and lr."""
     pl, gl, ml, vl = (_tensor_list(params), _tensor_list(grads), _tensor_list(exp_avg),
                       _tensor_list(exp_avg_sq))
     d = fno_adamw_desc(lr, betas[0], betas[1], eps, weight_decay, step)

@@ -27,6 +27,11 @@ class AdamW:
         self.record = torch.zeros(2, dtype=torch.float32, device=self._params.device)
         self.steps = 0
 
+    @staticmethod
+    def _capturing(stream):
+        import torch
+        return torch.cuda.is_current_stream_capturing()
+
     @property
     def grad_norm(self):
         """The gradients' global norm at the last step, without the loss scale (a device tensor)."""
@@ -35,7 +40,11 @@ class AdamW:
     def step(self, grad_scale=1.0):
         """One update from the gradients in their buffers, which carry the loss scale grad_scale.
         Where their norm is not finite, parameters and moments stay as they are (and the step
-        still counts in the bias corrections)."""
+        still counts in the bias corrections).  Not during a stream capture: the update's number and
+        the learning rate are values of the launch, and a replay would repeat them."""
+        if L._on_stream(self._params.index, self._capturing):
+            raise RuntimeError("AdamW.step cannot be captured: a replay would repeat this step's "
+                               "number and learning rate")
         self.steps += 1
         L.grad_norm(self._grads, self.max_norm, grad_scale, record=self.record)
         L.adamw(self._params, self._grads, self._m, self._v, self.steps, self.lr, self.betas,

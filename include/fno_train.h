@@ -111,9 +111,10 @@ typedef struct fno_adamw_desc {
  *   g' = factor g (record[1] of fno_grad_norm; record NULL: g' = g)
  *   m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
  *   p = p - lr weight_decay p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
- * (m = exp_avg, v = exp_avg_sq, float32).  When record's factor is not finite the update is
- * skipped: nothing is written, so that a loss-scaled run needs no synchronisation to drop such a
- * step. */
+ * (m = exp_avg, v = exp_avg_sq, float32).  What desc holds goes into the launch as values: a
+ * captured call replays this one update, number, rate and all.  When record's factor is not finite
+ * the update is skipped: nothing is written, so that a loss-scaled run needs no synchronisation to
+ * drop such a step. */
 fno_status fno_adamw(const fno_tensor_list* params, const fno_tensor_list* grads,
                      const fno_tensor_list* exp_avg, const fno_tensor_list* exp_avg_sq,
                      const fno_adamw_desc* desc, const float* record, void* stream);

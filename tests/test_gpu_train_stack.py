@@ -175,3 +175,27 @@ def test_norm_parameters_are_seeded():
     assert "gamma" not in a[0] and a[1]["gamma"].dtype == np.float32
     assert np.array_equal(a[2]["gamma"], b[2]["gamma"])
     assert not np.array_equal(a[1]["gamma"], a[2]["gamma"])
+
+
+def test_optimiser_step_refused_during_capture():
+    """A captured step would replay one update's number and learning rate: it is refused, and the
+    optimiser goes on as if it had not been asked."""
+    import torch
+
+    from fno_spectral_convolution_amd.optim import AdamW
+    announce("optimiser step during capture")
+    p, g = torch.ones(3000, device="cuda"), torch.ones(3000, device="cuda")
+    opt = AdamW([p], [g], 1e-2)
+    opt.step()
+    torch.cuda.synchronize()
+    before, graph, x = p.clone(), torch.cuda.CUDAGraph(), torch.zeros(64, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        x += 1
+        with pytest.raises(RuntimeError, match="captur"):
+            opt.step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert opt.steps == 1 and torch.equal(p, before) and float(x[0]) == 1.0
+    opt.step()
+    assert opt.steps == 2 and bool((p < before).all())

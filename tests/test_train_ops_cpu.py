@@ -218,3 +218,24 @@ def test_layer_norm_of_too_many_elements_refused(kw):
     assert L._lib.fno_layer_norm_workspace_bytes(d, ctypes.byref(n)) == BAD
     assert _fwd(d) == BAD and _bwd(d, gx=None) == BAD
     assert "overflow" in L.last_error_message()
+
+
+def test_optimiser_step_refused_during_capture(monkeypatch):
+    """The step's number and learning rate go into its launches as values: a replay would repeat one
+    update.  No GPU here: the calls are recorded, and the stream's answer is made up."""
+    from fno_spectral_convolution_amd.optim import AdamW
+    calls, capturing = [], [True]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(L, "_on_stream", lambda index, fn, *args: fn(*args, 0))
+    monkeypatch.setattr(L, "grad_norm", lambda *a, **k: calls.append("grad_norm"))
+    monkeypatch.setattr(L, "adamw", lambda *a, **k: calls.append("adamw"))
+    opt = AdamW.__new__(AdamW)
+    opt.lr, opt.betas, opt.eps, opt.weight_decay, opt.max_norm = 1e-3, (0.9, 0.99), 1e-8, 0.0, 1.0
+    opt._params = opt._grads = opt._m = opt._v = type("List", (), {"index": 0})()
+    opt.record, opt.steps = None, 4
+    with pytest.raises(RuntimeError, match="captur"):
+        opt.step()
+    assert not calls and opt.steps == 4
+    capturing[0] = False
+    opt.step()
+    assert calls == ["grad_norm", "adamw"] and opt.steps == 5
