@@ -904,24 +904,28 @@ __global__ __launch_bounds__(256) void k_ln_cols_points(NormArgs a, const T* x, 
 }
 
 // ---- the weight gradients: sums of the parts' rows [nparts][2][channels] -------------------------
-// COLS columns to a work-group, 256 / COLS threads down each.
+// COLS columns to a work-group at a time, 256 / COLS threads down each.
 template <int COLS>
 __global__ __launch_bounds__(256) void k_ln_finish(int channels, int nparts, const float* part,
                                                    float* ggamma, float* gbeta) {
   constexpr int kSlices = 256 / COLS;
   __shared__ float s_red[kSlices][COLS];
   const int col = threadIdx.x % COLS, slice = threadIdx.x / COLS;
-  const int64_t width = 2 * (int64_t)channels, i = (int64_t)blockIdx.x * COLS + col;
-  float s = 0.f;
-  if (i < width)
+  const int64_t width = 2 * (int64_t)channels, step = (int64_t)gridDim.x * COLS;
+  for (int64_t base = (int64_t)blockIdx.x * COLS; base < width; base += step) {
+    const int64_t i = base + col;
+    float s = 0.f;
+    if (i < width)
 #pragma unroll 8
-    for (int k = slice; k < nparts; k += kSlices) s += part[k * width + i];
-  s_red[slice][col] = s;
-  __syncthreads();
-  if (slice == 0 && i < width) {
-    for (int w = 1; w < kSlices; ++w) s += s_red[w][col];
-    float* out = i < channels ? ggamma : gbeta;
-    if (out) out[i < channels ? i : i - channels] = s;
+      for (int k = slice; k < nparts; k += kSlices) s += part[k * width + i];
+    s_red[slice][col] = s;
+    __syncthreads();
+    if (slice == 0 && i < width) {
+      for (int w = 1; w < kSlices; ++w) s += s_red[w][col];
+      float* out = i < channels ? ggamma : gbeta;
+      if (out) out[i < channels ? i : i - channels] = s;
+    }
+    __syncthreads();
   }
 }
 
@@ -1126,9 +1130,11 @@ int groups_t(const NormArgs& a) {
 hipError_t finish(const NormArgs& a, int parts, const float* part, float* ggamma, float* gbeta,
                   hipStream_t s) {
   const int64_t width = 2 * (int64_t)a.channels;
+  // a launch has fewer than 2^32 threads: 2^22 work-groups go over more columns in turn (with more
+  // the runtime starts only a part of them, and says nothing)
   const auto go = [&](auto cols) {
-    hipLaunchKernelGGL(k_ln_finish<cols.value>, dim3(ceil_div(width, cols.value)), dim3(256), 0, s,
-                       a.channels, parts, part, ggamma, gbeta);
+    hipLaunchKernelGGL(k_ln_finish<cols.value>, dim3(cut(ceil_div(width, cols.value), 1 << 22)),
+                       dim3(256), 0, s, a.channels, parts, part, ggamma, gbeta);
     return hipGetLastError();
   };
   return width >= 8192 ? go(Int<64>()) : width >= 1024 ? go(Int<16>()) : go(Int<4>());

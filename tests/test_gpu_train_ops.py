@@ -716,3 +716,30 @@ def test_norm_workspace_refused():
                torch.zeros(2 << 20, dtype=torch.uint8, device="cuda")[::2]):
         with pytest.raises(ValueError, match="ws"):
             L.layer_norm_bwd(x, None, st, x, ws=ws)
+
+
+def test_layer_norm_more_channels_than_a_launch_has_threads():
+    """From 2^29 channels on the weight gradients have more columns than a launch of 64 to a work-group
+    has threads for (2^32); the header allows up to 2^31."""
+    L = _L()
+    announce("layer_norm very long rows")
+    c = (1 << 29) + 67
+    out = {"gamma": torch.full((c,), 9.0, device="cuda")}
+    none = torch.empty((0, c), dtype=torch.bfloat16, device="cuda")
+    L.layer_norm_bwd(none, None, none.new_empty((2, 0), dtype=torch.float32), none, want=(), out=out)
+    assert not out["gamma"].any()
+    part = torch.randn(1 << 20, generator=_gen(3), device="cuda").bfloat16()
+    x = torch.empty((1, c), dtype=torch.bfloat16, device="cuda")
+    gy = torch.empty_like(x)
+    ends = (slice(0, 1 << 20), slice(c - (1 << 20), c))
+    x.zero_(), gy.zero_()
+    for s in ends:
+        x[0, s], gy[0, s] = part, part.flip(0)
+    stats = torch.tensor([[0.25], [2.0]], device="cuda")
+    got = L.layer_norm_bwd(x, None, stats, gy, want=("beta",), out=out)
+    for s in ends:
+        # one row: each sum is one product, of exact factors but for the rounding of x - mean
+        want = part.flip(0).double() * (part.double() - 0.25) * 2.0
+        _close("grad_gamma", got["gamma"][s], want, 4 * U * want.abs())
+        assert torch.equal(got["beta"][s], part.flip(0).float())
+    assert not got["beta"][1 << 20:c - (1 << 20)].any()
