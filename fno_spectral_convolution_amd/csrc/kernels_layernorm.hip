@@ -492,7 +492,7 @@ __global__ __launch_bounds__(256) void k_ln_cols_long(NormArgs a, const T* x, co
   for (int i = 0; i < VEC; ++i)
     if (i >= lo) {
       part[i] = dg[i];
-      part[d + i] = db[i];
+      part[(int64_t)d + i] = db[i];
     }
 }
 
@@ -880,7 +880,7 @@ __global__ __launch_bounds__(256) void k_ln_cols_points(NormArgs a, const T* x, 
   __shared__ float s_red[2][4];
   const int64_t rows = a.batch * a.npts;
   const int tid = threadIdx.x;
-  for (int c = blockIdx.y; c < a.channels; c += gridDim.y) {
+  for (int64_t c = blockIdx.y; c < a.channels; c += gridDim.y) {
     float sg = 0.f, sb = 0.f;
     for (int64_t r = (int64_t)blockIdx.x * 256 + tid; r < rows; r += (int64_t)gridDim.x * 256) {
       const int64_t b = r / a.npts, at = (r - b * a.npts) + c * a.npts;

@@ -743,3 +743,22 @@ def test_layer_norm_more_channels_than_a_launch_has_threads():
         _close("grad_gamma", got["gamma"][s], want, 4 * U * want.abs())
         assert torch.equal(got["beta"][s], part.flip(0).float())
     assert not got["beta"][1 << 20:c - (1 << 20)].any()
+
+
+def test_layer_norm_most_channels():
+    """One row of 2^31 - 1 entries, the most there may be: an index of its last vector's bias sums
+    passes 31 bits."""
+    L = _L()
+    announce("layer_norm longest row")
+    c = (1 << 31) - 1
+    part = torch.randn(1 << 20, generator=_gen(5), device="cuda").bfloat16()
+    x = torch.zeros((1, c), dtype=torch.bfloat16, device="cuda")
+    gy = torch.zeros_like(x)
+    ends = (slice(0, 1 << 20), slice(c - (1 << 20), c))
+    for s in ends:
+        gy[0, s] = part
+    stats = torch.tensor([[0.25], [2.0]], device="cuda")
+    got = L.layer_norm_bwd(x, None, stats, gy, want=("beta",))["beta"]
+    for s in ends:
+        assert torch.equal(got[s], part.float())
+    assert int(got.count_nonzero()) == 2 * int(part.count_nonzero())
