@@ -2118,7 +2118,7 @@ fno_status fno_adamw(const fno_tensor_list* params, const fno_tensor_list* grads
   a.beta2 = (float)d->beta2;
   a.one_minus_beta1 = (float)(1.0 - d->beta1);
   a.one_minus_beta2 = (float)(1.0 - d->beta2);
-  a.decay = (float)(1.0 - d->lr * d->weight_decay);
+  a.decay = (float)(d->lr * d->weight_decay);
   a.step_size = (float)(d->lr / (1.0 - std::pow(d->beta1, (double)d->step)));
   a.inv_bias2 = (float)(1.0 / std::sqrt(1.0 - std::pow(d->beta2, (double)d->step)));
   a.eps = (float)d->eps;

@@ -63,7 +63,7 @@ hipError_t launch_clip(const TensorTable& t, const TensorTable& out, const doubl
 
 struct AdamArgs {
   float beta1, beta2, one_minus_beta1, one_minus_beta2;
-  float decay;       // 1 - lr weight_decay
+  float decay;       // lr weight_decay
   float step_size;   // lr / (1 - beta1^t)
   float inv_bias2;   // 1 / sqrt(1 - beta2^t)
   float eps;

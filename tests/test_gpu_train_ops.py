@@ -762,3 +762,27 @@ def test_layer_norm_most_channels():
     for s in ends:
         assert torch.equal(got[s], part.float())
     assert int(got.count_nonzero()) == 2 * int(part.count_nonzero())
+
+
+@pytest.mark.parametrize("lr,wd", [(2e-6, 0.01), (1e-5, 0.01), (3e-5, 0.02)])
+def test_adamw_small_decay_counts(lr, wd):
+    """A decay below a parameter's rounding still counts on average: rounding p - lr wd p - step once
+    is as often up as down, where a factor 1 - lr wd, rounded to float32 by itself, is off by up to
+    2^-25 for every parameter alike (at lr wd = 2e-8 by all of it).  Each result is off by its own
+    rounding, at most 2^-24 (parameters in [1, 2)) and independent between parameters, since the
+    steps spread over many roundings: the mean of n errors stays within six times
+    2^-24 / sqrt(3 n), plus the steps' own float32 roundings, which are relative to them."""
+    L = _L()
+    announce("adamw decay", lr, wd)
+    g = _gen(31)
+    n = 1 << 20
+    p = 1 + torch.rand(n, generator=g, device="cuda")
+    gr, m = _randn(g, n), _randn(g, n)
+    v = _randn(g, n).square() + 0.5
+    b1, b2, eps = 0.9, 0.99, 1e-8
+    want, _, _, up = _adamw64(p, gr, m, v, 5, lr, b1, b2, eps, wd, 1.0)
+    L.adamw([p], [gr], [m], [v], 5, lr, (b1, b2), eps, wd)
+    mean = float((p.double() - want).mean())
+    bound = 6 * 2.0 ** -24 / math.sqrt(3 * n) + 24 * U * (lr * float(up.abs().mean()) + 2 * lr * wd)
+    print(f"    mean error {mean:.3e}, bound {bound:.3e}, decay {lr * wd * 1.5:.3e}", flush=True)
+    assert abs(mean) <= bound
