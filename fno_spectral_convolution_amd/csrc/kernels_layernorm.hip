@@ -1050,17 +1050,21 @@ bool stream_out(const NormArgs& a, const T* out, int64_t stride) {
          reinterpret_cast<uintptr_t>(out) % 128 == 0;
 }
 
-// Dynamic LDS that keeps a compute unit (160 KB) from holding more work-groups than make up `most`
-// waves.  The float32 forward that streams its output does better with 16 waves than with the 24 to
-// 28 that fit: 8 x 64 x 512^2 186 us against 205, 8 x 72 x 512^2 216 against 228, 2 x 20 x 128^3 135
-// against 140, 8 x 32 x 500000 180 against 187, but 1 x 64 x 2^21 198 against 193 and 8 x 32 x 2^19
-// 244 against 229 (planes a power of two apart share memory channels).  12 and 8 waves gain nothing
-// more and cost narrow fields up to 15%.  The backward's registers limit its waves already.  Outputs
-// that the cache takes, and half ones, want all the waves: 16 x 32 x 256^2 49.2 against 48.5, 8 x 20
-// x 300001 75 against 72, 8 x 64 x 512^2 bf16 134 against 123.
-size_t lds_for_waves(int waves, int most) {
-  const size_t groups = (size_t)ceil_div(most, waves), total = 160 << 10;
-  return std::min(total / (groups + 1) / 512 * 512 + 512, (size_t)64 << 10);
+// Dynamic LDS with which a compute unit (160 KB) holds at most as many of the float32 forward's
+// work-groups as make up 16 waves, rounded up to whole ones, where its output streams; 0: no limit.
+// Time with it over time without, 8 to 256 channels, 64 to 200 million entries:
+//   up to 8 waves, planes of 2^16 to 500000 points    0.92 to 1.02, 0.986 in the mean
+//   planes a multiple of 2 MB apart (2^19, 2^21)      0.96 to 1.12, 1.001
+//   9 to 16 waves                                     0.99 to 1.01, 1.000
+// 5 x 64 x 512^2 119 us against 130 and 11 x 16 x 500000 124 against 130, but 5 x 32 x 2^19 165 against
+// 147: only the first kind takes it.  12 and 8 waves gain nothing more and cost narrow fields up to
+// 15%.  The backward's registers limit its waves already.  Outputs that the cache takes, and half
+// ones, want all the waves: 16 x 32 x 256^2 49.2 against 48.5, 8 x 20 x 300001 75 against 72,
+// 8 x 64 x 512^2 bf16 134 against 123.
+size_t lds_for_16_waves(int waves, int64_t npts) {
+  if (waves > 8 || npts * 4 % (2 << 20) == 0) return 0;
+  const int groups = (int)ceil_div(16, waves), total = 160 << 10;
+  return total / (groups + 1) / 512 * 512 + 512;
 }
 
 template <typename T>
@@ -1088,7 +1092,7 @@ hipError_t fwd_t(NormArgs a, const T* x, const float* gamma, const float* beta, 
     case kField:
       pick_field(a.channels, [&](auto n) {
         FieldShape f = field_shape(a, n.value, kFwdVec<T>);
-        if (sizeof(T) == 4 && a.stream) f.lds = std::max(f.lds, lds_for_waves(f.waves, 16));
+        if (sizeof(T) == 4 && a.stream) f.lds = std::max(f.lds, lds_for_16_waves(f.waves, a.npts));
         const dim3 grid(cut(f.tiles, 1 << 20)), block(64 * f.waves);
         if (f.flat)
           hipLaunchKernelGGL((k_ln_fwd_field<T, n.value, 1, true>), grid, block, f.lds, s, a,

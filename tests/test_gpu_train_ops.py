@@ -786,3 +786,9 @@ def test_adamw_small_decay_counts(lr, wd):
     bound = 6 * 2.0 ** -24 / math.sqrt(3 * n) + 24 * U * (lr * float(up.abs().mean()) + 2 * lr * wd)
     print(f"    mean error {mean:.3e}, bound {bound:.3e}, decay {lr * wd * 1.5:.3e}", flush=True)
     assert abs(mean) <= bound
+
+
+@pytest.mark.parametrize("shape", [(3, 64, 1 << 19), (5, 32, 1 << 19), (2, 100, 1 << 19)], ids=str)
+def test_layer_norm_outputs_past_the_cache_planes_2mb_apart(shape):
+    """As above, where the forward keeps all its waves."""
+    test_layer_norm_outputs_past_the_cache(shape, torch.float32)
