@@ -39,7 +39,7 @@ class AdamW:
 
     def step(self, grad_scale=1.0):
         """One update from the gradients in their buffers, which carry the loss scale grad_scale.
-        Where their norm is not finite, parameters and moments stay as they are (and the step
+        Where one of them is infinite or NaN, parameters and moments stay as they are (and the step
         still counts in the bias corrections).  Not during a stream capture: the update's number and
         the learning rate are values of the launch, and a replay would repeat them."""
         if L._on_stream(self._params.index, self._capturing):

@@ -82,19 +82,21 @@ fno_status fno_grad_norm_workspace_bytes(const fno_tensor_list* grads, size_t* b
 
 /* The global norm of a list of gradients that carry the loss scale grad_scale (1 without one):
  *   norm = sqrt(sum over all elements of g^2) / grad_scale,
- *   factor = min(1, max_norm / norm) / grad_scale   (NaN when norm is infinite or NaN),
- * written to the device floats record[0] = norm, record[1] = factor.  The sum is taken in float64
- * (no float32 gradient over- or underflows it) in a fixed order.  max_norm > 0, INFINITY for no
- * clipping; grad_scale finite and > 0.  A tensor that is listed twice counts twice (but what a
- * call writes, clipped gradients, parameters or moments, may be listed once only). */
+ *   factor = min(1, max_norm / norm) / grad_scale   (NaN when a gradient is infinite or NaN),
+ * written to the device floats record[0] = norm, record[1] = factor.  The sum, the norm and the
+ * factor are taken in float64 (no float32 gradient over- or underflows them) in a fixed order and
+ * rounded at the end: the norm of finite gradients may come out as infinity, above float32's
+ * range, beside a factor that is right.  max_norm > 0, INFINITY for no clipping; grad_scale finite
+ * and > 0.  A tensor that is listed twice counts twice (but what a call writes, clipped gradients,
+ * parameters or moments, may be listed once only). */
 fno_status fno_grad_norm(const fno_tensor_list* grads, float max_norm, float grad_scale,
                          float* record, void* workspace, size_t workspace_bytes, void* stream);
 
 /* fno_grad_norm, then out = factor * g for every tensor.  out lists as many tensors of the same
  * elems, each of its gradient's dtype or float32 (where half gradients lose their loss scale
  * without underflow), each its gradient itself or apart from all gradients.  With a factor of
- * exactly 1 a tensor that is its own output is left as it is; a non-finite norm makes every
- * output NaN. */
+ * exactly 1 a tensor that is its own output is left as it is; a gradient that is infinite or NaN
+ * makes every output NaN. */
 fno_status fno_clip_grad_norm(const fno_tensor_list* grads, const fno_tensor_list* out,
                               float max_norm, float grad_scale, float* record, void* workspace,
                               size_t workspace_bytes, void* stream);

@@ -792,3 +792,21 @@ def test_adamw_small_decay_counts(lr, wd):
 def test_layer_norm_outputs_past_the_cache_planes_2mb_apart(shape):
     """As above, where the forward keeps all its waves."""
     test_layer_norm_outputs_past_the_cache(shape, torch.float32)
+
+
+def test_adamw_takes_finite_gradients_of_a_norm_above_float32():
+    """The recorded norm is infinity, the factor 5e-41 (subnormal: to 2^-149 / 5e-41 = 3e-5 of
+    itself), and the update is made."""
+    L = _L()
+    announce("adamw, norm above float32")
+    grad = torch.full((5000,), 3e38, device="cuda")
+    p, m, v = torch.ones(5000, device="cuda"), torch.zeros(5000, device="cuda"), \
+        torch.zeros(5000, device="cuda")
+    rec = L.grad_norm([grad], 1.0)
+    assert rec[0] == math.inf and bool(rec[1].isfinite())
+    L.adamw([p], [grad], [m], [v], 1, 1e-2, (0.9, 0.99), 1e-8, 0.0, record=rec)
+    want = 0.1 / math.sqrt(5000)
+    _close("exp_avg", m, torch.full_like(m, want, dtype=torch.float64),
+           torch.full_like(m, 4e-5 * want, dtype=torch.float64))
+    _close("param", p, torch.full_like(p, 0.99, dtype=torch.float64),
+           torch.full_like(p, 4 * U, dtype=torch.float64))
