@@ -810,3 +810,55 @@ def test_adamw_takes_finite_gradients_of_a_norm_above_float32():
            torch.full_like(m, 4e-5 * want, dtype=torch.float64))
     _close("param", p, torch.full_like(p, 0.99, dtype=torch.float64),
            torch.full_like(p, 4 * U, dtype=torch.float64))
+
+
+def _call_each(L, s, rec, ws):
+    """Every operator once, outputs of its own but for the gradient list, which is s's."""
+    y, stats = L.layer_norm_fwd(s["x"], s["gamma"], s["beta"], EPS)
+    gr = L.layer_norm_bwd(s["x"], s["gamma"], stats, s["x"])
+    L.grad_norm(s["list"], 0.5, record=rec[0], ws=ws[0])
+    clipped = [torch.empty_like(t) for t in s["grads"]]
+    L.clip_grad_norm(s["list"], 0.5, out=clipped, record=rec[1], ws=ws[1])
+    p, m, v = ([torch.full_like(t, one) for t in s["grads"]] for one in (1.0, 0.0, 0.0))
+    L.adamw(p, s["list"], m, v, 1, 1e-2, record=rec[0])
+    return [y, stats, *gr.values(), *rec, *clipped, *p, *m, *v]
+
+
+def test_calls_run_on_the_current_stream():
+    """Each stream's inputs are written on it behind some milliseconds of other work, with no
+    synchronisation: a call that went out on another stream would read what was there before.  Both
+    streams use one tensor list, each with its own workspace and record."""
+    L = _L()
+    announce("train ops behind a stream's own work")
+    g = _gen(12)
+    new = {"x": _randn(g, 3, 20, 4001), "gamma": 1 + 0.1 * _randn(g, 20), "beta": _randn(g, 20),
+           "grads": [_randn(g, n) for n in (20_011, 5, 70_003)]}
+    s = {k: [torch.ones_like(t) for t in v] if isinstance(v, list) else torch.ones_like(v)
+         for k, v in new.items()}
+    s["list"] = L.TensorList(s["grads"])
+    recs = [[torch.zeros(2, device="cuda") for _ in range(2)] for _ in range(3)]
+    wss = [[torch.empty(1 << 16, dtype=torch.uint8, device="cuda") for _ in range(2)]
+           for _ in range(3)]
+    busy = torch.ones(1 << 28, device="cuda")
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(a):
+        for _ in range(20):
+            busy.mul_(1.0)  # 2 GB each
+        for k, v in new.items():
+            for d, src in zip(s[k], v) if isinstance(v, list) else [(s[k], v)]:
+                d.copy_(src)
+        ready = torch.cuda.Event()
+        ready.record()
+        got_a = _call_each(L, s, recs[0], wss[0])
+    still_busy = not ready.query()
+    with torch.cuda.stream(b):
+        b.wait_event(ready)
+        got_b = _call_each(L, s, recs[1], wss[1])
+    torch.cuda.synchronize()
+    assert still_busy, "the other work was too short to tell streams apart"
+    want_new = _call_each(L, s, recs[2], wss[2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(s[k], new[k]) for k in ("x", "gamma", "beta"))
+    for got in (got_a, got_b):
+        assert len(got) == len(want_new) and all(torch.equal(p, q) for p, q in zip(got, want_new))
