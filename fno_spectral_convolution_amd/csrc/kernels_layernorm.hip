@@ -7,7 +7,8 @@
 //
 // Each pass reads its fields once and writes once; memory bounds it (8 and 14 operations an element
 // against 8 and 12 bytes in float32).  A row or point is therefore held in registers from its load
-// to its store, and only the sums over channels leave a lane.  All sums and statistics are float32.
+// to its store, and only the sums over channels leave a lane.  All sums and statistics are float32 or
+// wider.
 // The variance comes from deviations about a mean, never from E[x^2] - E[x]^2; where several waves
 // share a row or point, each takes its own mean and the squared deviations about it, and they join
 // as M2 = sum_w (M2_w + n_w (mean_w - mean)^2), which needs one exchange where two sweeps need two.
@@ -120,7 +121,7 @@ __global__ __launch_bounds__(BLOCK) void k_ln_fwd_rows(NormArgs a, const T* x, c
   partial = __any(partial);
   const int other = t % kWaves;  // the wave whose part of a joint sum this lane reads
   const float n = wave_count<VEC, TPR, NV>(wave, d), n_other = wave_count<VEC, TPR, NV>(other, d);
-  const float inv_n = TPR > 64 ? 1.0f / fmaxf(n, 1.f) : inv_d;
+  const float inv_n = TPR > 64 ? 1.0f / fmaxf(n, 1.f) : inv_d, share_other = n_other * inv_d;
   const int64_t rows = a.batch, step = (int64_t)gridDim.x * kGroups;
   int64_t base = (int64_t)blockIdx.x * kGroups;
   Raw<T, VEC> next[NV];
@@ -152,10 +153,12 @@ __global__ __launch_bounds__(BLOCK) void k_ln_fwd_rows(NormArgs a, const T* x, c
           const float c = f[k][i] - mean;
           sum2 += !masked.value || i >= lo[k] ? c * c : 0.f;
         }
-      sq = lane_sum<kLanes>(sum2);
+      sq = lane_sum<kLanes>(sum2) * inv_d;
     });
     if (TPR > 64) {
-      // the waves' means and squared deviations join: M2 = sum M2_w + n_w (mean_w - mean)^2
+      // the waves' means and squared deviations join: var = sum (M2_w + n_w (mean_w - mean)^2) / d,
+      // divided before the sum, which passes float32's range where the variance is far from it.  In
+      // this order of products a wave without entries adds 0, whatever the mean.
       if (t % 64 == 0) {
         s_stat[flip][group][wave][0] = mean;
         s_stat[flip][group][wave][1] = sq;
@@ -163,9 +166,9 @@ __global__ __launch_bounds__(BLOCK) void k_ln_fwd_rows(NormArgs a, const T* x, c
       __syncthreads();
       const float m = s_stat[flip][group][other][0], q2 = s_stat[flip][group][other][1];
       mean = wave_sum<kWaves>(n_other * m) * inv_d;
-      sq = wave_sum<kWaves>(q2 + n_other * (m - mean) * (m - mean));
+      sq = wave_sum<kWaves>(q2 + (share_other * (m - mean)) * (m - mean));
     }
-    const float rstd = rsqrtf(sq * inv_d + a.eps);
+    const float rstd = rsqrtf(sq + a.eps);
     const int64_t row = base + group;
     if (row < rows) {
       T* o = y + row * a.y_stride;
@@ -383,25 +386,31 @@ __global__ __launch_bounds__(kLong) void k_ln_fwd_long(NormArgs a, const T* x, c
   constexpr int VEC = kVec<T>;
   __shared__ float s_red[kLong / 64];
   const int tid = threadIdx.x, d = a.channels, nvec = (int)(((int64_t)d + VEC - 1) / VEC);
+  const double inv_d = 1.0 / d;
   for (int64_t row = blockIdx.x; row < a.batch; row += gridDim.x) {
     const T* p = x + row * a.x_stride;
     T* q = y + row * a.y_stride;
-    float f[VEC], sum = 0.f, sq = 0.f;
+    float f[VEC];
+    double sum = 0.0, sq = 0.0;
     int st, lo;
     for (int j = tid; j < nvec; j += kLong) {
       place<VEC>(j, d, st, lo);
       load_pack<T, VEC>(p + st, f);
+      float v = 0.f;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) sum += i >= lo ? f[i] : 0.f;
+      for (int i = 0; i < VEC; ++i) v += i >= lo ? f[i] : 0.f;
+      sum += v;
     }
-    const float mean = group_sum(sum, s_red) / (float)d;
+    const float mean = group_sum((float)sum, s_red) / (float)d;
     for (int j = tid; j < nvec; j += kLong) {
       place<VEC>(j, d, st, lo);
       load_pack<T, VEC>(p + st, f);
+      float v = 0.f;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) sq += i >= lo ? (f[i] - mean) * (f[i] - mean) : 0.f;
+      for (int i = 0; i < VEC; ++i) v += i >= lo ? (f[i] - mean) * (f[i] - mean) : 0.f;
+      sq += v;
     }
-    const float rstd = rsqrtf(group_sum(sq, s_red) / (float)d + a.eps);
+    const float rstd = rsqrtf(group_sum((float)(sq * inv_d), s_red) + a.eps);
     // in place the vector that overlaps its neighbour must not read what that one wrote: the last
     // vector stores only its own elements, one by one
     for (int j = tid; j < nvec; j += kLong) {
@@ -435,22 +444,26 @@ __global__ __launch_bounds__(kLong) void k_ln_bwd_long(NormArgs a, const T* x, c
     const T* r = gy + row * a.y_stride;
     T* q = gx + row * a.gx_stride;
     const float mean = stats[row], rstd = stats[a.batch + row];
-    float h[VEC], g[VEC], ga[VEC], s1 = 0.f, s2 = 0.f;
+    float h[VEC], g[VEC], ga[VEC];
+    double sum1 = 0.0, sum2 = 0.0;
     int st, lo;
     for (int j = tid; j < nvec; j += kLong) {
       place<VEC>(j, d, st, lo);
       load_pack<T, VEC>(p + st, h);
       load_pack<T, VEC>(r + st, g);
       load_weight<VEC>(gamma, st, 1.f, ga);
+      float v1 = 0.f, v2 = 0.f;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         const float v = g[i] * ga[i];
-        s1 += i >= lo ? v : 0.f;
-        s2 += i >= lo ? v * ((h[i] - mean) * rstd) : 0.f;
+        v1 += i >= lo ? v : 0.f;
+        v2 += i >= lo ? v * ((h[i] - mean) * rstd) : 0.f;
       }
+      sum1 += v1;
+      sum2 += v2;
     }
-    s1 = group_sum(s1, s_red) / (float)d;
-    s2 = group_sum(s2, s_red) / (float)d;
+    const float s1 = group_sum((float)sum1, s_red) / (float)d;
+    const float s2 = group_sum((float)sum2, s_red) / (float)d;
     for (int j = tid; j < nvec; j += kLong) {
       place<VEC>(j, d, st, lo);
       load_pack<T, VEC>(p + st, h);
@@ -818,6 +831,9 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_field_few(NormArgs a, int64_t t
 }
 
 // Fields of more channels than a work-group holds: one thread to a point, sweeps over the channels.
+// What a thread adds up in one chain, here and in the long rows (there vector by vector), is float64:
+// a float32 chain of 9000 channels is off by more than the rest of the arithmetic together, and its
+// squares overflow where the variance does not.
 template <typename T>
 __global__ __launch_bounds__(256) void k_ln_fwd_points(NormArgs a, const T* x, const float* gamma,
                                                        const float* beta, T* y, float* stats) {
@@ -827,14 +843,14 @@ __global__ __launch_bounds__(256) void k_ln_fwd_points(NormArgs a, const T* x, c
     const int64_t b = r / a.npts, p = r - b * a.npts;
     const T* xr = x + b * a.x_stride + p;
     T* yr = y + b * a.y_stride + p;
-    float sum = 0.f, sq = 0.f;
+    double sum = 0.0, sq = 0.0;
     for (int c = 0; c < a.channels; ++c) sum += to_float(xr[c * a.npts]);
-    const float mean = sum / (float)a.channels;
+    const float mean = (float)(sum / a.channels);
     for (int c = 0; c < a.channels; ++c) {
-      const float d = to_float(xr[c * a.npts]) - mean;
+      const double d = to_float(xr[c * a.npts]) - mean;
       sq += d * d;
     }
-    const float rstd = rsqrtf(sq / (float)a.channels + a.eps);
+    const float rstd = rsqrtf((float)(sq / a.channels) + a.eps);
     for (int c = 0; c < a.channels; ++c) {
       const float h = (to_float(xr[c * a.npts]) - mean) * rstd;
       yr[c * a.npts] = from_float<T>((gamma ? gamma[c] : 1.f) * h + (beta ? beta[c] : 0.f));
@@ -857,14 +873,13 @@ __global__ __launch_bounds__(256) void k_ln_bwd_points(NormArgs a, const T* x, c
     const T* gr = gy + b * a.y_stride + p;
     T* o = gx + b * a.gx_stride + p;
     const float mean = stats[r], rstd = stats[rows + r];
-    float s1 = 0.f, s2 = 0.f;
+    double sum1 = 0.0, sum2 = 0.0;
     for (int c = 0; c < a.channels; ++c) {
       const float g = to_float(gr[c * a.npts]) * (gamma ? gamma[c] : 1.f);
-      s1 += g;
-      s2 += g * ((to_float(xr[c * a.npts]) - mean) * rstd);
+      sum1 += g;
+      sum2 += (double)g * ((to_float(xr[c * a.npts]) - mean) * rstd);
     }
-    s1 /= (float)a.channels;
-    s2 /= (float)a.channels;
+    const float s1 = (float)(sum1 / a.channels), s2 = (float)(sum2 / a.channels);
     for (int c = 0; c < a.channels; ++c) {
       const float g = to_float(gr[c * a.npts]) * (gamma ? gamma[c] : 1.f);
       const float h = (to_float(xr[c * a.npts]) - mean) * rstd;

@@ -862,3 +862,23 @@ def test_calls_run_on_the_current_stream():
     assert all(torch.equal(s[k], new[k]) for k in ("x", "gamma", "beta"))
     for got in (got_a, got_b):
         assert len(got) == len(want_new) and all(torch.equal(p, q) for p, q in zip(got, want_new))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("shape", [(3, w) for w in (1025, 1032, 1536, 2049, 5000, 9000, 20000)]
+                         + [(2, 20, 300), (1, 256, 300), (1, 9000, 5)], ids=str)
+def test_layer_norm_of_large_means(shape, dtype):
+    """Rows whose mean's square passes float32's range, and from 9000 entries on the sum of their
+    squared deviations too, while their variance does not.  Waves that hold none of a row's entries
+    (the last one at 1025 to 1536, the half types) add nothing to the joined deviations."""
+    L = _L()
+    announce("layer_norm large means", shape, dtype)
+    g = _gen(shape[1])
+    big = 30000.0 if dtype == torch.float16 else 2.5e19
+    x = (big * (1 + 0.01 * _randn(g, *shape))).to(dtype)
+    gamma, beta = 1 + 0.3 * _randn(g, shape[1]), 0.3 * _randn(g, shape[1])
+    gy = _randn(g, *shape).to(dtype)
+    y, stats = L.layer_norm_fwd(x, gamma, beta, EPS)
+    assert bool(torch.isfinite(y).all())
+    _check_fwd(x, gamma, beta, y, stats)
+    _check_bwd(x, gamma, gy, L.layer_norm_bwd(x, gamma, stats, gy))
