@@ -1067,17 +1067,21 @@ bool stream_out(const NormArgs& a, const T* out, int64_t stride) {
 
 // Dynamic LDS with which a compute unit (160 KB) holds at most as many of the float32 forward's
 // work-groups as make up 16 waves, rounded up to whole ones, where its output streams; 0: no limit.
-// Time with it over time without, 8 to 256 channels, 64 to 200 million entries:
-//   up to 8 waves, planes of 2^16 to 500000 points    0.92 to 1.02, 0.986 in the mean
-//   planes a multiple of 2 MB apart (2^19, 2^21)      0.96 to 1.12, 1.001
-//   9 to 16 waves                                     0.99 to 1.01, 1.000
-// 5 x 64 x 512^2 119 us against 130 and 11 x 16 x 500000 124 against 130, but 5 x 32 x 2^19 165 against
-// 147: only the first kind takes it.  12 and 8 waves gain nothing more and cost narrow fields up to
-// 15%.  The backward's registers limit its waves already.  Outputs that the cache takes, and half
-// ones, want all the waves: 16 x 32 x 256^2 49.2 against 48.5, 8 x 20 x 300001 75 against 72,
-// 8 x 64 x 512^2 bf16 134 against 123.
+// Time with the limit over time without, 4 to 256 channels, 64 to 200 million entries:
+//   planes of 2^16 to 500000 points, up to 8 waves     0.92 to 1.02, 0.986 in the mean
+//   planes a multiple of 2 MB apart (2^19 points)
+//     2 to 4 waves (9 to 32 channels), 2^21 and more   0.85 to 1.02, 0.956
+//     the same, fewer points                           0.96 to 1.15, 1.012
+//     1 and 5 to 8 waves                               0.91 to 1.06, 0.999
+//   9 to 16 waves                                      0.99 to 1.01, 1.000
+// The first two kinds take it: 5 x 64 x 512^2 119 us against 130, 2 x 20 x 128^3 135 against 140, but
+// 5 x 32 x 2^19 165 against 147.  12 and 8 waves gain nothing more and cost narrow fields up to 15%.
+// The backward's registers limit its waves already.  Outputs that the cache takes, and half ones, want
+// all the waves: 16 x 32 x 256^2 49.2 against 48.5, 8 x 20 x 300001 75 against 72, 8 x 64 x 512^2 bf16
+// 134 against 123.
 size_t lds_for_16_waves(int waves, int64_t npts) {
-  if (waves > 8 || npts * 4 % (2 << 20) == 0) return 0;
+  const bool apart = npts * 4 % (2 << 20) == 0;
+  if (waves > 8 || (apart && (waves == 1 || waves > 4 || npts < 1 << 21))) return 0;
   const int groups = (int)ceil_div(16, waves), total = 160 << 10;
   return total / (groups + 1) / 512 * 512 + 512;
 }
