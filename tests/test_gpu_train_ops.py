@@ -841,9 +841,10 @@ def test_calls_run_on_the_current_stream():
            for _ in range(3)]
     busy = torch.ones(1 << 28, device="cuda")
     a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    _call_each(L, s, recs[2], wss[2])  # what a process's first calls take is done
     torch.cuda.synchronize()
     with torch.cuda.stream(a):
-        for _ in range(20):
+        for _ in range(60):
             busy.mul_(1.0)  # 2 GB each
         for k, v in new.items():
             for d, src in zip(s[k], v) if isinstance(v, list) else [(s[k], v)]:
