@@ -14,7 +14,7 @@ import ctypes
 import functools
 import os
 from ctypes import (POINTER, byref, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t,
-                    c_uint32, c_void_p)
+                    c_uint32, c_uint64, c_void_p)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # FNO_LIBRARY names another build of libfno (e.g. the host-sanitized one for CPU checks)
@@ -30,6 +30,10 @@ FNO_ERR_INTERNAL = 5
 FNO_DTYPE_F32 = 0
 FNO_DTYPE_BF16 = 1
 FNO_DTYPE_F16 = 2
+
+FNO_ACT_NONE = 0
+FNO_ACT_GELU = 1
+FNO_ACT_SILU = 2
 
 FNO_FLAG_TANH_PREACT = 1
 FNO_FLAG_GELU = 2
@@ -56,6 +60,8 @@ EXPORTS = [
 # the training operators of fno_train.h
 TRAIN_EXPORTS = [
     "fno_layer_norm_fwd", "fno_layer_norm_workspace_bytes", "fno_layer_norm_bwd",
+    "fno_dropout_fwd", "fno_dropout_bwd",
+    "fno_group_norm_workspace_bytes", "fno_group_norm_fwd", "fno_group_norm_bwd",
     "fno_tensor_list_bytes", "fno_tensor_list_create", "fno_tensor_list_destroy",
     "fno_grad_norm_workspace_bytes", "fno_grad_norm", "fno_clip_grad_norm", "fno_adamw",
 ]
@@ -70,6 +76,22 @@ class fno_plan_desc(ctypes.Structure):
 class fno_layer_norm_desc(ctypes.Structure):
     _fields_ = [("dtype", c_int32), ("reserved", c_int32), ("batch", c_int64),
                 ("channels", c_int64), ("npts", c_int64), ("x_stride", c_int64),
+                ("y_stride", c_int64), ("grad_x_stride", c_int64), ("eps", c_double)]
+
+
+class fno_dropout(ctypes.Structure):
+    _fields_ = [("p", c_double), ("seed", c_uint64), ("draw", c_uint64), ("counter", c_void_p)]
+
+
+class fno_dropout_desc(ctypes.Structure):
+    _fields_ = [("dtype", c_int32), ("reserved", c_int32), ("batch", c_int64), ("elems", c_int64),
+                ("x_stride", c_int64), ("residual_stride", c_int64), ("y_stride", c_int64)]
+
+
+class fno_group_norm_desc(ctypes.Structure):
+    _fields_ = [("dtype", c_int32), ("channels_last", c_int32), ("activation", c_int32),
+                ("reserved", c_int32), ("batch", c_int64), ("channels", c_int64),
+                ("groups", c_int64), ("npts", c_int64), ("x_stride", c_int64),
                 ("y_stride", c_int64), ("grad_x_stride", c_int64), ("eps", c_double)]
 
 
@@ -143,6 +165,14 @@ def _load():
                                                    POINTER(c_size_t)]),
         "fno_layer_norm_bwd": (c_int, [POINTER(fno_layer_norm_desc), P, P, P, P, P, P, P, P,
                                        c_size_t, P]),
+        "fno_dropout_fwd": (c_int, [POINTER(fno_dropout_desc), POINTER(fno_dropout), P, P, P, P]),
+        "fno_dropout_bwd": (c_int, [POINTER(fno_dropout_desc), POINTER(fno_dropout), P, P, P]),
+        "fno_group_norm_workspace_bytes": (c_int, [POINTER(fno_group_norm_desc),
+                                                   POINTER(c_size_t), POINTER(c_size_t)]),
+        "fno_group_norm_fwd": (c_int, [POINTER(fno_group_norm_desc), POINTER(fno_dropout),
+                                       P, P, P, P, P, P, c_size_t, P]),
+        "fno_group_norm_bwd": (c_int, [POINTER(fno_group_norm_desc), POINTER(fno_dropout),
+                                       P, P, P, P, P, P, P, P, P, c_size_t, P]),
         "fno_tensor_list_bytes": (c_int, [c_int64, P, POINTER(c_size_t)]),
         "fno_tensor_list_create": (c_int, [c_int64, P, P, c_size_t, P, POINTER(c_void_p)]),
         "fno_tensor_list_destroy": (c_int, [P]),
@@ -307,6 +337,36 @@ def fno_layer_norm_bwd(desc, x, gamma, stats, grad_y, grad_x, grad_gamma, grad_b
                        stream):
     _check(_lib.fno_layer_norm_bwd(byref(desc), x, gamma, stats, grad_y, grad_x, grad_gamma,
                                    grad_beta, ws, ws_bytes, stream), "fno_layer_norm_bwd")
+
+
+def fno_dropout_fwd(desc, drop, x, residual, y, stream):
+    _check(_lib.fno_dropout_fwd(byref(desc), byref(drop), x, residual, y, stream),
+           "fno_dropout_fwd")
+
+
+def fno_dropout_bwd(desc, drop, grad_y, grad_x, stream):
+    _check(_lib.fno_dropout_bwd(byref(desc), byref(drop), grad_y, grad_x, stream),
+           "fno_dropout_bwd")
+
+
+def fno_group_norm_workspace_bytes(desc):
+    """Bytes of workspace of the forward and of the backward."""
+    f, b = c_size_t(), c_size_t()
+    _check(_lib.fno_group_norm_workspace_bytes(byref(desc), byref(f), byref(b)),
+           "fno_group_norm_workspace_bytes")
+    return f.value, b.value
+
+
+def fno_group_norm_fwd(desc, drop, x, gamma, beta, y, stats, ws, ws_bytes, stream):
+    _check(_lib.fno_group_norm_fwd(byref(desc), None if drop is None else byref(drop), x, gamma,
+                                   beta, y, stats, ws, ws_bytes, stream), "fno_group_norm_fwd")
+
+
+def fno_group_norm_bwd(desc, drop, x, gamma, beta, stats, grad_y, grad_x, grad_gamma, grad_beta,
+                       ws, ws_bytes, stream):
+    _check(_lib.fno_group_norm_bwd(byref(desc), None if drop is None else byref(drop), x, gamma,
+                                   beta, stats, grad_y, grad_x, grad_gamma, grad_beta, ws, ws_bytes,
+                                   stream), "fno_group_norm_bwd")
 
 
 def fno_tensor_list_bytes(count, tensors) -> int:
@@ -935,6 +995,175 @@ def layer_norm_bwd(x, gamma, stats, grad_y, want=("x", "gamma", "beta"), out=Non
                       _vector(gg, n.channels, index, "grad_gamma"),
                       _vector(gb, n.channels, index, "grad_beta"), _ptr(ws),
                       0 if ws is None else ws.numel() * ws.element_size()), "fno_layer_norm_bwd")
+    return {"x": gx, "gamma": gg, "beta": gb}
+
+
+class Dropout:
+    """A dropout mask, which is a function of these numbers and an element's index and is never
+    stored (see fno_dropout): each element is dropped with probability p, in steps of 2^-16.  seed:
+    of the run, 64 bits; draw: of this layer and step.  counter: an int64 or uint64 tensor of one
+    element on the GPU that is added to draw when a call runs, for captured graphs to move on between
+    their replays.  A backward pass takes its forward's Dropout with the counter as it was then."""
+
+    __slots__ = ("desc", "ptr", "counter", "index")
+
+    def __init__(self, p, seed, draw=0, counter=None):
+        if not (0.0 <= p and round(p * 65536) <= 65535):
+            raise ValueError(f"dropout: p must be in [0, 1) and not round to 1, not {p!r}")
+        for name, v in (("seed", seed), ("draw", draw)):
+            if v < 0 or v >> 64:
+                raise ValueError(f"dropout: {name} must be in [0, 2^64), not {v!r}")
+        self.counter, self.index, at = counter, None, None
+        if counter is not None:
+            if counter.numel() != 1 or counter.dtype not in (_torch.int64, _torch.uint64):
+                raise ValueError("dropout: counter is one int64 or uint64")
+            self.index, at = _on_gpu(counter), counter.data_ptr()
+        self.desc = fno_dropout(p, seed, draw, at)
+        self.ptr = byref(self.desc)
+
+
+def _mask(drop, index):
+    """The C form of a call's Dropout, None for none."""
+    if drop is None:
+        return None
+    if drop.index is not None and drop.index != index:
+        raise ValueError(f"dropout: its counter is on cuda:{drop.index}, the data on cuda:{index}")
+    return drop.ptr
+
+
+class _DropShape:
+    def __init__(self, dtype, shape, x_stride, r_stride, y_stride):
+        if dtype not in _KINDS:
+            raise ValueError(f"float32, bfloat16 or float16 data expected, not {dtype}")
+        if not shape:
+            raise ValueError("dropout: x is [batch, ...]")
+        per = 1
+        for n in shape[1:]:
+            per *= n
+        st = [_NormShape._batch_stride(shape, s, name) for s, name in
+              ((x_stride, "x or grad_y"), (r_stride, "residual"), (y_stride, "out"))]
+        self.desc = fno_dropout_desc(_KINDS[dtype], 0, shape[0], per, *st)
+        self.ptr = byref(self.desc)
+
+
+_drop_shape = functools.lru_cache(maxsize=256)(_DropShape)
+
+
+def _out_like(x, out):
+    """An output of x's shape, new and packed if none is given, and its strides."""
+    if out is None:
+        out = _torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return out, out.stride()
+    return out, _like_x(out, x, "out")
+
+
+def dropout_fwd(x, drop, residual=None, out=None):
+    """residual + x with what `drop` (a Dropout) drops set to 0 and the rest scaled up (residual None:
+    0), for x of any shape [batch, ...] whose entries are packed.  out may be x or residual."""
+    out, y_strides = _out_like(x, out)
+    strides = x.stride()
+    r_strides = y_strides if residual is None else _like_x(residual, x, "residual")
+    n = _drop_shape(x.dtype, x.shape, strides, r_strides, y_strides)
+    index = _on_gpu(x)
+    _check(_on_stream(index, _lib.fno_dropout_fwd, n.ptr, _mask(drop, index), x.data_ptr(),
+                      _ptr(residual), out.data_ptr()), "fno_dropout_fwd")
+    return out
+
+
+def dropout_bwd(grad_y, drop, out=None):
+    """The gradient of dropout_fwd at its x (at its residual it is grad_y).  out may be grad_y."""
+    out, y_strides = _out_like(grad_y, out)
+    n = _drop_shape(grad_y.dtype, grad_y.shape, grad_y.stride(), y_strides, y_strides)
+    index = _on_gpu(grad_y)
+    _check(_on_stream(index, _lib.fno_dropout_bwd, n.ptr, _mask(drop, index), grad_y.data_ptr(),
+                      out.data_ptr()), "fno_dropout_bwd")
+    return out
+
+
+_ACTS = {None: FNO_ACT_NONE, "gelu": FNO_ACT_GELU, "silu": FNO_ACT_SILU}
+
+
+class _GroupShape:
+    """As _NormShape, for a group norm."""
+
+    def __init__(self, dtype, shape, groups, act, last, x_stride, y_stride, gx_stride, eps):
+        if len(shape) < 2:
+            raise ValueError("group norm: x is [batch, channels, *grid], or [batch, *grid, channels] "
+                             "with channels_last")
+        if dtype not in _KINDS:
+            raise ValueError(f"float32, bfloat16 or float16 data expected, not {dtype}")
+        if act not in _ACTS:
+            raise ValueError(f"group norm: act must be one of {list(_ACTS)}, not {act!r}")
+        channels = shape[-1] if last else shape[1]
+        npts = 1
+        for n in shape[1:-1] if last else shape[2:]:
+            npts *= n
+        batch = [_NormShape._batch_stride(shape, st, name) for st, name in
+                 ((x_stride, "x"), (y_stride, "y or grad_y"), (gx_stride, "grad_x"))]
+        self.desc = fno_group_norm_desc(_KINDS[dtype], 1 if last else 0, _ACTS[act], 0, shape[0],
+                                        channels, groups, npts, *batch, eps)
+        self.ptr = byref(self.desc)
+        self.channels = _torch.Size([channels])
+        self.stats = _torch.Size([2, shape[0], groups])
+        self.fwd_bytes, self.bwd_bytes = fno_group_norm_workspace_bytes(self.desc)
+
+
+_group_shape = functools.lru_cache(maxsize=256)(_GroupShape)
+
+
+def _space(ws, need, x, index):
+    """A workspace's address and size: the caller's, or a new one of `need` bytes."""
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = _torch.empty(need, dtype=_torch.uint8, device=x.device)
+    else:
+        _workspace(ws, index)
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def group_norm_fwd(x, groups, gamma=None, beta=None, act=None, eps=1e-5, channels_last=False,
+                   drop=None, out=None, stats=None, want_stats=True, ws=None):
+    """Group norm of a field [B, C, *grid] (channels_last: [B, *grid, C]) over each of `groups` runs of
+    C / groups channels and all points of an entry, times gamma plus beta (float32 [C]; None: 1 and
+    0), then the activation act (None, "gelu" or "silu") and a Dropout, in one pass.  [rows, C] is
+    tokens with a norm for each head.  Returns (y, stats); stats, float32 [2, B, groups], holds the
+    means and the reciprocal deviations for group_norm_bwd (None without want_stats).  ws: packed
+    workspace of fno_group_norm_workspace_bytes on x's device (allocated when None)."""
+    out, y_strides = _out_like(x, out)
+    n = _group_shape(x.dtype, x.shape, groups, act, channels_last, x.stride(), y_strides, y_strides,
+                     eps)
+    index = _on_gpu(x)
+    if stats is None and want_stats:
+        stats = _torch.empty(n.stats, dtype=_torch.float32, device=x.device)
+    ws, at, size = _space(ws, n.fwd_bytes, x, index)
+    _check(_on_stream(index, _lib.fno_group_norm_fwd, n.ptr, _mask(drop, index), x.data_ptr(),
+                      _vector(gamma, n.channels, index, "gamma"),
+                      _vector(beta, n.channels, index, "beta"), out.data_ptr(),
+                      _vector(stats, n.stats, index, "stats"), at, size), "fno_group_norm_fwd")
+    return out, stats
+
+
+def group_norm_bwd(x, groups, gamma, beta, stats, grad_y, act=None, channels_last=False, drop=None,
+                   want=("x", "gamma", "beta"), out=None, ws=None):
+    """Gradients of group_norm_fwd from its x, stats, activation and Dropout: dict(x, gamma, beta),
+    None where not asked.  out: tensors to write instead of new ones (out["x"] may be grad_y itself).
+    ws: as in group_norm_fwd."""
+    gy_strides = _like_x(grad_y, x, "grad_y")
+    o = out or {}
+    gx = o["x"] if "x" in o else         _torch.empty(x.shape, dtype=x.dtype, device=x.device) if "x" in want else None
+    n = _group_shape(x.dtype, x.shape, groups, act, channels_last, x.stride(), gy_strides,
+                     gy_strides if gx is None else _like_x(gx, x, "grad_x"), 0.0)
+    index = _on_gpu(x)
+    gg, gb = (o[k] if k in o else _torch.empty(n.channels, dtype=_torch.float32, device=x.device)
+              if k in want else None for k in ("gamma", "beta"))
+    ws, at, size = _space(ws, n.bwd_bytes, x, index)
+    _check(_on_stream(index, _lib.fno_group_norm_bwd, n.ptr, _mask(drop, index), x.data_ptr(),
+                      _vector(gamma, n.channels, index, "gamma"),
+                      _vector(beta, n.channels, index, "beta"),
+                      _vector(stats, n.stats, index, "stats"), grad_y.data_ptr(), _ptr(gx),
+                      _vector(gg, n.channels, index, "grad_gamma"),
+                      _vector(gb, n.channels, index, "grad_beta"), at, size), "fno_group_norm_bwd")
     return {"x": gx, "gamma": gg, "beta": gb}
 
 

@@ -1,0 +1,88 @@
+// Dropout masks from a counter: nothing is stored, the backward makes the forward's mask again.
+//
+// Element i of a tensor has 16 bits of its own and is dropped where they are below the threshold
+// T = round(65536 p); what is kept is multiplied by 65536 / (65536 - T), the inverse of the share
+// that is kept in fact.  The bits come from Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel
+// random numbers: as easy as 1, 2, 3", SC 2011): ten rounds on the counter (i / 8, draw), 64 bits
+// each, under the key `seed` give four words, eight elements' bits.  16 bits and not 32: ten rounds
+// cost about 110 vector cycles, and four elements to a block would hold half-precision fields to
+// the vector units' rate instead of the memory's.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "train_ops.h"
+
+namespace fno {
+
+struct Words {
+  uint32_t w[4];
+};
+
+__device__ __forceinline__ Words philox4x32(uint64_t block, uint64_t draw, uint32_t k0,
+                                            uint32_t k1) {
+  uint32_t a = (uint32_t)block, b = (uint32_t)(block >> 32), c = (uint32_t)draw,
+           d = (uint32_t)(draw >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t p = (uint64_t)a * 0xD2511F53u, q = (uint64_t)c * 0xCD9E8D57u;
+    a = (uint32_t)(q >> 32) ^ b ^ k0;
+    b = (uint32_t)q;
+    c = (uint32_t)(p >> 32) ^ d ^ k1;
+    d = (uint32_t)p;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return {{a, b, c, d}};
+}
+
+// A draw's mask: what a kernel makes of DropArgs once.
+struct Dropper {
+  uint32_t top, k0, k1;  // top: the threshold as the upper half of a word
+  float scale;
+  uint64_t draw;
+
+  __device__ __forceinline__ explicit Dropper(const DropArgs& a)
+      : top(a.threshold << 16), k0((uint32_t)a.seed), k1((uint32_t)(a.seed >> 32)),
+        scale(a.scale), draw(a.draw) {
+    if (a.counter) draw += *a.counter;
+  }
+  __device__ __forceinline__ Words block(uint64_t k) const { return philox4x32(k, draw, k0, k1); }
+  // element 2 j (+ 1) of a block that has the word w there
+  __device__ __forceinline__ bool keep_even(uint32_t w) const { return w << 16 >= top; }
+  __device__ __forceinline__ bool keep_odd(uint32_t w) const { return w >= top; }
+  // bit e: whether element e of block k is kept
+  __device__ __forceinline__ uint32_t bits(uint64_t k) const {
+    const Words w = block(k);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      m |= (keep_even(w.w[j]) ? 1u << 2 * j : 0u) | (keep_odd(w.w[j]) ? 2u << 2 * j : 0u);
+    return m;
+  }
+  // v: elements i .. i + N - 1 (N <= 8); aligned: i is a multiple of N, as all of the wave's are.
+  // What is dropped is 0, whatever it was.
+  template <int N>
+  __device__ __forceinline__ void apply(float (&v)[N], uint64_t i, bool aligned) const {
+    if ((N == 8 || N == 4) && aligned) {
+      const Words w = block(i >> 3);
+      const bool upper = N == 4 && (i & 4);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        const uint32_t u = N == 4 ? (upper ? w.w[j + 2] : w.w[j]) : w.w[j];
+        v[2 * j] = keep_even(u) ? v[2 * j] * scale : 0.f;
+        v[2 * j + 1] = keep_odd(u) ? v[2 * j + 1] * scale : 0.f;
+      }
+      return;
+    }
+    const int at = (int)(i & 7);
+    uint32_t m = bits(i >> 3);
+    if (at + N > 8) m |= bits((i >> 3) + 1) << 8;
+    m >>= at;
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = m >> e & 1 ? v[e] * scale : 0.f;
+  }
+};
+
+}  // namespace fno

@@ -1267,6 +1267,13 @@ hipError_t launch_layer_norm_fwd(const NormArgs& a, int dtype, const void* x, co
   return dtype == FNO_DTYPE_BF16 ? go((__bf16)0.f) : go((_Float16)0.f);
 }
 
+hipError_t launch_weight_sums(int channels, int parts, const float* part, float* ggamma,
+                              float* gbeta, hipStream_t s) {
+  NormArgs a{};
+  a.channels = channels;
+  return finish(a, parts, part, ggamma, gbeta, s);
+}
+
 int layer_norm_parts(const NormArgs& a, int dtype) {
   const auto parts = [&](auto t) {
     typedef decltype(t) T;

@@ -1818,6 +1818,104 @@ size_t norm_workspace(const fno::NormArgs& a, int32_t dtype) {
   return align_up(sizeof(float) * 2 * (size_t)a.channels * (size_t)fno::layer_norm_parts(a, dtype));
 }
 
+fno_status drop_args(const fno_dropout* d, fno::DropArgs* a) {
+  *a = {0, 1.0f, 0, 0, nullptr};
+  if (!d) return FNO_OK;
+  if (!(d->p >= 0.0 && d->p <= 1.0))
+    return fail(FNO_ERR_INVALID_ARGUMENT, "dropout: p must be in [0, 1)");
+  const uint32_t t = (uint32_t)nearbyint(d->p * 65536.0);  // ties to even
+  if (t > 65535) return fail(FNO_ERR_INVALID_ARGUMENT, "dropout: p rounds to 1 (in 65536ths)");
+  OPT_AT(d->counter, "dropout counter", sizeof(uint64_t));
+  if (t > 0) *a = {t, (float)(65536.0 / (65536.0 - t)), d->seed, d->draw, d->counter};
+  return FNO_OK;
+}
+
+fno_status dropout_args(const fno_dropout_desc* d, const fno_dropout* drop, fno::DropoutArgs* a) {
+  if (!d || !drop) return fail(FNO_ERR_INVALID_ARGUMENT, "dropout descriptor is NULL");
+  if (!known_dtype(d->dtype)) return fail(FNO_ERR_INVALID_ARGUMENT, "dropout: unknown dtype");
+  if (d->reserved != 0) return fail(FNO_ERR_INVALID_ARGUMENT, "dropout: reserved must be 0");
+  if (d->batch < 0 || d->elems < 0)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "dropout: batch and elems must be >= 0");
+  if (d->x_stride < 0 || d->residual_stride < 0 || d->y_stride < 0)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "dropout: strides must be >= 0");
+  if (d->batch > 1 && d->y_stride < d->elems)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "dropout: y_stride < elems");
+  const int64_t lim = (int64_t)1 << 60;
+  const int64_t st = std::max(std::max(d->x_stride, d->residual_stride), d->y_stride);
+  int64_t all, span;
+  if (__builtin_mul_overflow(d->batch, d->elems, &all) || all > lim ||
+      __builtin_mul_overflow(d->batch, st, &span) || span > lim || d->batch > lim || d->elems > lim)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "dropout: sizes overflow");
+  const fno_status s = drop_args(drop, &a->drop);
+  a->batch = d->batch;
+  a->per = d->elems;
+  a->x_stride = d->x_stride;
+  a->r_stride = d->residual_stride;
+  a->y_stride = d->y_stride;
+  return s;
+}
+
+fno_status dropout(const char* name, const fno_dropout_desc* d, const fno_dropout* drop,
+                   const void* x, const void* residual, void* y, hipStream_t s) {
+  fno::DropoutArgs a;
+  const fno_status st = dropout_args(d, drop, &a);
+  if (st != FNO_OK) return st;
+  if (a.batch == 0 || a.per == 0) return FNO_OK;
+  const size_t w = dtype_bytes(d->dtype);
+  REQ_AT(x, "x", w);
+  REQ_AT(y, "y", w);
+  OPT_AT(residual, "residual", w);
+  if (a.batch > 1 &&
+      ((y == x && a.y_stride != a.x_stride) || (y == residual && a.y_stride != a.r_stride)))
+    return fail(FNO_ERR_INVALID_ARGUMENT, "dropout in place needs equal strides");
+  LAUNCH(name, s, fno::launch_dropout(a, d->dtype, x, residual, y, s));
+  return FNO_OK;
+}
+
+fno_status group_args(const fno_group_norm_desc* d, const fno_dropout* drop, fno::GroupArgs* a) {
+  if (!d) return fail(FNO_ERR_INVALID_ARGUMENT, "group norm descriptor is NULL");
+  if (!known_dtype(d->dtype)) return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: unknown dtype");
+  if (d->reserved != 0) return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: reserved must be 0");
+  if (d->channels_last != 0 && d->channels_last != 1)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: channels_last must be 0 or 1");
+  if (d->activation != FNO_ACT_NONE && d->activation != FNO_ACT_GELU &&
+      d->activation != FNO_ACT_SILU)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: unknown activation");
+  if (d->batch < 0 || d->npts < 0 || d->channels < 1)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: batch, npts >= 0 and channels >= 1");
+  if (d->groups < 1 || d->channels % d->groups != 0)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: groups must divide channels");
+  if (d->x_stride < 0 || d->y_stride < 0 || d->grad_x_stride < 0)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: strides must be >= 0");
+  if (!(d->eps >= 0.0) || !std::isfinite(d->eps))
+    return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: eps must be finite and >= 0");
+  if (d->channels >= (int64_t)1 << 30 || d->batch >= (int64_t)1 << 31)
+    return fail(FNO_ERR_UNSUPPORTED, "group norm: channels >= 2^30 or batch >= 2^31");
+  // as in the layer norm: every byte offset and the bytes of all elements fit 62 bits
+  const int64_t lim = (int64_t)1 << 60;
+  int64_t per, all, span;
+  const int64_t st = std::max(std::max(d->x_stride, d->y_stride), d->grad_x_stride);
+  if (__builtin_mul_overflow(d->channels, d->npts, &per) || per > lim ||
+      __builtin_mul_overflow(d->batch, per, &all) || all > lim ||
+      __builtin_mul_overflow(d->batch, st, &span) || span > lim)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: sizes overflow");
+  a->batch = d->batch;
+  a->npts = d->npts;
+  a->channels = (int)d->channels;
+  a->groups = (int)d->groups;
+  a->last = d->channels_last != 0;
+  a->act = d->activation;
+  a->x_stride = d->x_stride;
+  a->y_stride = d->y_stride;
+  a->gx_stride = d->grad_x_stride;
+  a->eps = (float)d->eps;
+  return drop_args(drop, &a->drop);
+}
+
+bool group_writes_overlap(const fno::GroupArgs& a, int64_t stride) {
+  return a.batch > 1 && stride < (int64_t)a.channels * a.npts;
+}
+
 constexpr int64_t kMaxElems = (int64_t)1 << 36;
 
 // A list's tensors checked; the chunks that they make.
@@ -1985,6 +2083,93 @@ fno_status fno_layer_norm_bwd(const fno_layer_norm_desc* desc, const void* x, co
   LAUNCH("layer_norm_bwd", s,
          fno::launch_layer_norm_bwd(a, desc->dtype, x, gamma, stats, grad_y, grad_x, grad_gamma,
                                     grad_beta, static_cast<float*>(ws), s));
+  return FNO_OK;
+}
+
+fno_status fno_dropout_fwd(const fno_dropout_desc* desc, const fno_dropout* drop, const void* x,
+                           const void* residual, void* y, void* stream) {
+  return dropout("dropout_fwd", desc, drop, x, residual, y, static_cast<hipStream_t>(stream));
+}
+
+fno_status fno_dropout_bwd(const fno_dropout_desc* desc, const fno_dropout* drop,
+                           const void* grad_y, void* grad_x, void* stream) {
+  return dropout("dropout_bwd", desc, drop, grad_y, nullptr, grad_x,
+                 static_cast<hipStream_t>(stream));
+}
+
+fno_status fno_group_norm_workspace_bytes(const fno_group_norm_desc* desc, size_t* fwd,
+                                          size_t* bwd) {
+  fno::GroupArgs a;
+  const fno_status st = group_args(desc, nullptr, &a);
+  if (st != FNO_OK) return st;
+  if (fwd) *fwd = fno::group_norm_fwd_bytes(a, desc->dtype);
+  if (bwd) *bwd = fno::group_norm_bwd_bytes(a, desc->dtype);
+  return FNO_OK;
+}
+
+fno_status fno_group_norm_fwd(const fno_group_norm_desc* desc, const fno_dropout* drop,
+                              const void* x, const float* gamma, const float* beta, void* y,
+                              float* stats, void* ws, size_t ws_bytes, void* stream) {
+  fno::GroupArgs a;
+  const fno_status st = group_args(desc, drop, &a);
+  if (st != FNO_OK) return st;
+  if (group_writes_overlap(a, a.y_stride))
+    return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: y_stride < channels * npts");
+  if (a.batch == 0 || a.npts == 0) return FNO_OK;
+  const size_t w = dtype_bytes(desc->dtype);
+  REQ_AT(x, "x", w);
+  REQ_AT(y, "y", w);
+  OPT_AT(gamma, "gamma", sizeof(float));
+  OPT_AT(beta, "beta", sizeof(float));
+  OPT_AT(stats, "stats", sizeof(float));
+  if (x == y && a.batch > 1 && a.x_stride != a.y_stride)
+    return fail(FNO_ERR_INVALID_ARGUMENT, "group norm in place needs x_stride == y_stride");
+  const size_t need = fno::group_norm_fwd_bytes(a, desc->dtype);
+  if (need > 0) {
+    REQ(ws, "workspace");
+    if (ws_bytes < need) return fail(FNO_ERR_INVALID_ARGUMENT, "workspace too small");
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LAUNCH("group_norm_fwd", s,
+         fno::launch_group_norm_fwd(a, desc->dtype, x, gamma, beta, y, stats, ws, s));
+  return FNO_OK;
+}
+
+fno_status fno_group_norm_bwd(const fno_group_norm_desc* desc, const fno_dropout* drop,
+                              const void* x, const float* gamma, const float* beta,
+                              const float* stats, const void* grad_y, void* grad_x,
+                              float* grad_gamma, float* grad_beta, void* ws, size_t ws_bytes,
+                              void* stream) {
+  fno::GroupArgs a;
+  const fno_status st = group_args(desc, drop, &a);
+  if (st != FNO_OK) return st;
+  if (grad_x && group_writes_overlap(a, a.gx_stride))
+    return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: grad_x_stride < channels * npts");
+  OPT_AT(grad_gamma, "grad_gamma", sizeof(float));
+  OPT_AT(grad_beta, "grad_beta", sizeof(float));
+  const bool weights = grad_gamma || grad_beta, none = a.batch == 0 || a.npts == 0;
+  if ((none && !weights) || (!weights && !grad_x)) return FNO_OK;
+  if (!none) {
+    const size_t w = dtype_bytes(desc->dtype);
+    REQ_AT(x, "x", w);
+    REQ_AT(grad_y, "grad_y", w);
+    REQ_AT(stats, "stats", sizeof(float));
+    OPT_AT(gamma, "gamma", sizeof(float));
+    OPT_AT(beta, "beta", sizeof(float));
+    OPT_AT(grad_x, "grad_x", w);
+    if (a.batch > 1 && ((grad_x == x && a.gx_stride != a.x_stride) ||
+                        (grad_x == grad_y && a.gx_stride != a.y_stride)))
+      return fail(FNO_ERR_INVALID_ARGUMENT, "group norm in place needs equal strides");
+    const size_t need = fno::group_norm_bwd_bytes(a, desc->dtype);
+    if (need > 0) {
+      REQ(ws, "workspace");
+      if (ws_bytes < need) return fail(FNO_ERR_INVALID_ARGUMENT, "workspace too small");
+    }
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LAUNCH("group_norm_bwd", s,
+         fno::launch_group_norm_bwd(a, desc->dtype, x, gamma, beta, stats, grad_y, grad_x,
+                                    grad_gamma, grad_beta, ws, s));
   return FNO_OK;
 }
 

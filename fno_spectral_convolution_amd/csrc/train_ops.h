@@ -27,6 +27,46 @@ hipError_t launch_layer_norm_bwd(const NormArgs& a, int dtype, const void* x, co
                                  const float* stats, const void* gy, void* gx, float* ggamma,
                                  float* gbeta, float* part, hipStream_t s);
 
+// the sums over `parts` rows [2][channels] of partial sums, in a fixed order: row 0's to ggamma, row
+// 1's to gbeta (nullable)
+hipError_t launch_weight_sums(int channels, int parts, const float* part, float* ggamma,
+                              float* gbeta, hipStream_t s);
+
+// ---- dropout (kernels_dropout.hip) -----------------------------------------------------------
+struct DropArgs {
+  uint32_t threshold;  // of 65536; 0: nothing is dropped
+  float scale;         // 65536 / (65536 - threshold)
+  uint64_t seed, draw;
+  const uint64_t* counter;  // on the device, added to draw; nullable
+};
+struct DropoutArgs {
+  DropArgs drop;
+  int64_t batch, per;                   // entries, elements of an entry
+  int64_t x_stride, r_stride, y_stride; // elements between entries
+  bool stream;                          // the output goes past the caches (set by the launch)
+};
+hipError_t launch_dropout(const DropoutArgs& a, int dtype, const void* x, const void* residual,
+                          void* y, hipStream_t s);
+
+// ---- group norm (kernels_groupnorm.hip) ------------------------------------------------------
+struct GroupArgs {
+  int64_t batch, npts;
+  int channels, groups;
+  bool last;  // channels last: [batch][npts][channels]
+  int act;    // fno_activation
+  int64_t x_stride, y_stride, gx_stride;  // elements between batch entries
+  float eps;
+  DropArgs drop;
+};
+size_t group_norm_fwd_bytes(const GroupArgs& a, int dtype);
+size_t group_norm_bwd_bytes(const GroupArgs& a, int dtype);
+hipError_t launch_group_norm_fwd(const GroupArgs& a, int dtype, const void* x, const float* gamma,
+                                 const float* beta, void* y, float* stats, void* ws,
+                                 hipStream_t s);
+hipError_t launch_group_norm_bwd(const GroupArgs& a, int dtype, const void* x, const float* gamma,
+                                 const float* beta, const float* stats, const void* gy, void* gx,
+                                 float* ggamma, float* gbeta, void* ws, hipStream_t s);
+
 // ---- tensor lists (kernels_optim.hip) --------------------------------------------------------
 // A list's device table: its entries, then the entry that holds each chunk.  Chunks are kChunk
 // elements of one tensor (its last one fewer); they are the grain at which work is shared out.

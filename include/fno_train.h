@@ -1,8 +1,9 @@
 /*
  * libfno's training operators: what a training run takes beside the blocks of fno.h.
  *
- * A layer norm between blocks with its gradients, the global norm and clipping of the gradients
- * that the blocks return, and the AdamW update.  They need no plan.  Ownership, streams, the timer
+ * A layer norm, a group norm with its activation, and dropout between blocks, each with its
+ * gradients, the global norm and clipping of the gradients that the blocks return, and the AdamW
+ * update.  They need no plan.  Ownership, streams, the timer
  * and errors are fno.h's.  Unlike its calls these accept data pointers at any multiple of the
  * element size (fields cut out of larger ones, parameters packed into one buffer); float32 vectors
  * (gamma, beta, the statistics and the record) at 4 bytes, workspaces and tables at 16.  float32,
@@ -52,6 +53,92 @@ fno_status fno_layer_norm_workspace_bytes(const fno_layer_norm_desc* desc, size_
  * when there are no rows), and the same bits run to run.  grad_x may be grad_y or x (the same
  * pointer and stride). */
 fno_status fno_layer_norm_bwd(const fno_layer_norm_desc* desc, const void* x, const float* gamma,
+                              const float* stats, const void* grad_y, void* grad_x,
+                              float* grad_gamma, float* grad_beta, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Dropout from a counter: the mask is a function of the numbers here and of each element's index,
+ * so that nothing is stored and a backward pass drops what its forward dropped.  With
+ * T = round(65536 p), element i of a tensor (counted through the packed tensor in memory order,
+ * wherever its entries lie) is dropped, 0, where its 16 bits are below T, and is multiplied by
+ * 65536 / (65536 - T) elsewhere.  Its bits are half (the lower for even i) of word (i % 8) / 2 of
+ * Philox4x32-10 of the counter (i / 8, draw + *counter) under the key seed, each 64 bits with the
+ * low word first.  Different draws under a seed are different masks. */
+typedef struct fno_dropout {
+  double p;                 /* 0 <= p, T <= 65535; T = 0 drops nothing                        */
+  uint64_t seed;
+  uint64_t draw;            /* of this layer and step                                         */
+  const uint64_t* counter;  /* on the device, read when the call runs, 8-byte aligned: what a */
+                            /* captured graph moves on between its replays; NULL: 0           */
+} fno_dropout;
+
+typedef struct fno_dropout_desc {
+  int32_t dtype;            /* fno_dtype of x, residual and y                                 */
+  int32_t reserved;         /* must be 0                                                      */
+  int64_t batch, elems;     /* >= 0: entries, packed elements of an entry                     */
+  int64_t x_stride;         /* elements between entries of x, of grad_y in the backward: >= 0 */
+  int64_t residual_stride;  /* of residual: >= 0                                              */
+  int64_t y_stride;         /* of y, of grad_x in the backward: >= elems                      */
+} fno_dropout_desc;
+
+/* y = residual + dropped x (residual NULL: 0).  y may be x or residual (the same pointer and
+ * stride). */
+fno_status fno_dropout_fwd(const fno_dropout_desc* desc, const fno_dropout* drop, const void* x,
+                           const void* residual, void* y, void* stream);
+/* grad_x = dropped grad_y (the residual's gradient is grad_y itself); grad_x may be grad_y. */
+fno_status fno_dropout_bwd(const fno_dropout_desc* desc, const fno_dropout* drop,
+                           const void* grad_y, void* grad_x, void* stream);
+
+typedef enum fno_activation {
+  FNO_ACT_NONE = 0,
+  FNO_ACT_GELU = 1, /* u/2 (1 + erf(u/sqrt 2)) */
+  FNO_ACT_SILU = 2  /* u / (1 + e^-u)          */
+} fno_activation;
+
+/* Group norm over fields [batch][channels][npts], or channels last [batch][npts][channels], with an
+ * activation and dropout in the same pass.  For each entry and each of the `groups` runs of
+ * channels / groups channels, over all points, m = npts channels / groups entries:
+ *   mu = sum x / m;  r = 1 / sqrt(sum (x - mu)^2 / m + eps);
+ *   y = drop(act(gamma[c] (x - mu) r + beta[c]))
+ * npts = 1 (the same memory either way) is the form of tokens with a norm for each head.  Strides
+ * as in fno_layer_norm_desc. */
+typedef struct fno_group_norm_desc {
+  int32_t dtype;          /* fno_dtype of x, y, grad_y, grad_x                    */
+  int32_t channels_last;  /* 0 or 1                                              */
+  int32_t activation;     /* fno_activation                                      */
+  int32_t reserved;       /* must be 0                                           */
+  int64_t batch;          /* >= 0, below 2^31; without entries or points: no rows */
+  int64_t channels;       /* >= 1, below 2^30                                    */
+  int64_t groups;         /* >= 1, divides channels                              */
+  int64_t npts;           /* >= 0                                                */
+  int64_t x_stride;       /* of x                                                */
+  int64_t y_stride;       /* of y (forward), of grad_y (backward)                */
+  int64_t grad_x_stride;  /* of grad_x (the forward does not look at it)         */
+  double eps;             /* finite, >= 0                                        */
+} fno_group_norm_desc;
+
+/* Bytes of workspace of the two calls on this descriptor (either may be 0, its workspace then
+ * NULL; fwd and bwd nullable). */
+fno_status fno_group_norm_workspace_bytes(const fno_group_norm_desc* desc, size_t* fwd,
+                                          size_t* bwd);
+
+/* drop NULL: no dropout.  gamma and beta (float32 [channels]) may be NULL: 1 and 0.  stats
+ * (nullable) receives float32 [2][batch][groups]: mu, then r, for the backward.  y may be x (the
+ * same pointer and stride).  A non-finite x makes its own group of its entry non-finite, where that
+ * is not dropped, and no other. */
+fno_status fno_group_norm_fwd(const fno_group_norm_desc* desc, const fno_dropout* drop,
+                              const void* x, const float* gamma, const float* beta, void* y,
+                              float* stats, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward from the forward's x, stats and mask.  With h = (x - mu) r and
+ * g = act'(gamma h + beta) drop(grad_y):
+ *   grad_x = r (gamma g - sum(gamma g) / m - h sum(gamma g h) / m)  (sums over the group),
+ *   grad_gamma[c] = sum g h,  grad_beta[c] = sum g  (over batch and npts; float32).
+ * Outputs may be NULL to skip them; they are overwritten (grad_gamma and grad_beta with zeros when
+ * there are no rows), and the same bits run to run.  grad_x may be grad_y or x (the same pointer
+ * and stride). */
+fno_status fno_group_norm_bwd(const fno_group_norm_desc* desc, const fno_dropout* drop,
+                              const void* x, const float* gamma, const float* beta,
                               const float* stats, const void* grad_y, void* grad_x,
                               float* grad_gamma, float* grad_beta, void* workspace,
                               size_t workspace_bytes, void* stream);
