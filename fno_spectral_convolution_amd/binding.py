@@ -1052,7 +1052,7 @@ _drop_shape = functools.lru_cache(maxsize=256)(_DropShape)
 def _out_like(x, out):
     """An output of x's shape, new and packed if none is given, and its strides."""
     if out is None:
-        out = _torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
         return out, out.stride()
     return out, _like_x(out, x, "out")
 
@@ -1116,7 +1116,7 @@ def _space(ws, need, x, index):
     if ws is None:
         if not need:
             return None, None, 0
-        ws = _torch.empty(need, dtype=_torch.uint8, device=x.device)
+        ws = x.new_empty(need, dtype=_torch.uint8)
     else:
         _workspace(ws, index)
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
@@ -1135,7 +1135,7 @@ def group_norm_fwd(x, groups, gamma=None, beta=None, act=None, eps=1e-5, channel
                      eps)
     index = _on_gpu(x)
     if stats is None and want_stats:
-        stats = _torch.empty(n.stats, dtype=_torch.float32, device=x.device)
+        stats = x.new_empty(n.stats, dtype=_torch.float32)
     ws, at, size = _space(ws, n.fwd_bytes, x, index)
     _check(_on_stream(index, _lib.fno_group_norm_fwd, n.ptr, _mask(drop, index), x.data_ptr(),
                       _vector(gamma, n.channels, index, "gamma"),
@@ -1155,8 +1155,8 @@ def group_norm_bwd(x, groups, gamma, beta, stats, grad_y, act=None, channels_las
     n = _group_shape(x.dtype, x.shape, groups, act, channels_last, x.stride(), gy_strides,
                      gy_strides if gx is None else _like_x(gx, x, "grad_x"), 0.0)
     index = _on_gpu(x)
-    gg, gb = (o[k] if k in o else _torch.empty(n.channels, dtype=_torch.float32, device=x.device)
-              if k in want else None for k in ("gamma", "beta"))
+    gg, gb = (o[k] if k in o else x.new_empty(n.channels, dtype=_torch.float32) if k in want
+              else None for k in ("gamma", "beta"))
     ws, at, size = _space(ws, n.bwd_bytes, x, index)
     _check(_on_stream(index, _lib.fno_group_norm_bwd, n.ptr, _mask(drop, index), x.data_ptr(),
                       _vector(gamma, n.channels, index, "gamma"),

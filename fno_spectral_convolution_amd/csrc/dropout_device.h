@@ -48,38 +48,37 @@ struct Dropper {
         scale(a.scale), draw(a.draw) {
     if (a.counter) draw += *a.counter;
   }
-  __device__ __forceinline__ Words block(uint64_t k) const { return philox4x32(k, draw, k0, k1); }
-  // element 2 j (+ 1) of a block that has the word w there
-  __device__ __forceinline__ bool keep_even(uint32_t w) const { return w << 16 >= top; }
-  __device__ __forceinline__ bool keep_odd(uint32_t w) const { return w >= top; }
+  __device__ __forceinline__ Words block(uint64_t k) const {
+    // the rounds' keys are sums on the scalar unit, made where they are used: kept through a loop
+    // they would take twenty registers and more
+    uint32_t a = k0, b = k1;
+    asm volatile("" : "+s"(a), "+s"(b));
+    return philox4x32(k, draw, a, b);
+  }
   // bit e: whether element e of block k is kept
   __device__ __forceinline__ uint32_t bits(uint64_t k) const {
     const Words w = block(k);
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      m |= (keep_even(w.w[j]) ? 1u << 2 * j : 0u) | (keep_odd(w.w[j]) ? 2u << 2 * j : 0u);
+      m |= (w.w[j] << 16 >= top ? 1u << 2 * j : 0u) | (w.w[j] >= top ? 2u << 2 * j : 0u);
     return m;
   }
-  // v: elements i .. i + N - 1 (N <= 8); aligned: i is a multiple of N, as all of the wave's are.
+  // the same for the N elements from i on (N <= 8), which may lie in two blocks
+  template <int N>
+  __device__ __forceinline__ uint32_t mask(uint64_t i) const {
+    const int at = (int)(i & 7), blocks = N > 1 && at + N > 8 ? 2 : 1;
+    uint32_t m = 0;
+#pragma unroll 1
+    for (int j = 0; j < blocks; ++j) m |= bits((i >> 3) + j) << 8 * j;
+    m >>= at;
+    // made before the elements are touched: the generator's registers are free again by then
+    asm volatile("" : "+v"(m));
+    return m;
+  }
   // What is dropped is 0, whatever it was.
   template <int N>
-  __device__ __forceinline__ void apply(float (&v)[N], uint64_t i, bool aligned) const {
-    if ((N == 8 || N == 4) && aligned) {
-      const Words w = block(i >> 3);
-      const bool upper = N == 4 && (i & 4);
-#pragma unroll
-      for (int j = 0; j < N / 2; ++j) {
-        const uint32_t u = N == 4 ? (upper ? w.w[j + 2] : w.w[j]) : w.w[j];
-        v[2 * j] = keep_even(u) ? v[2 * j] * scale : 0.f;
-        v[2 * j + 1] = keep_odd(u) ? v[2 * j + 1] * scale : 0.f;
-      }
-      return;
-    }
-    const int at = (int)(i & 7);
-    uint32_t m = bits(i >> 3);
-    if (at + N > 8) m |= bits((i >> 3) + 1) << 8;
-    m >>= at;
+  __device__ __forceinline__ void apply(float (&v)[N], uint32_t m) const {
 #pragma unroll
     for (int e = 0; e < N; ++e) v[e] = m >> e & 1 ? v[e] * scale : 0.f;
   }

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void k_dropout(DropoutArgs a, const T* x, cons
       float f[8], add[8];
       load8(p, f);
       if (r) load8(r, add);
-      if (a.drop.threshold) drop.apply<8>(f, (uint64_t)block << 3, true);
+      if (a.drop.threshold) drop.apply<8>(f, drop.bits(block));
       if (r) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] += add[e];

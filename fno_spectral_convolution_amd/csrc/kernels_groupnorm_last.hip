@@ -1,0 +1,642 @@
+// Group norm of channels-last data [batch][npts][channels] (and of rows of one point that are longer
+// than a work-group holds, the same memory).  groupnorm_device.h has the mathematics.
+#include "groupnorm_device.h"
+
+namespace fno {
+namespace {
+
+// ---- channels last -------------------------------------------------------------------------------
+// EVEN: vectors are whole, and each lies in one group (its mean and r are then one register each).
+// A row is one point's channels.  A work-group takes a block of `cols` channels (tc vectors) and a
+// tile of rows, tr of them at a time: a thread keeps to its vector's channels.  The part of a group
+// that lies in a block is a segment; group g and block k make segment g + k, so that a group's
+// segments are neighbours (numbers that no pair has stay unused).
+struct Tiles {
+  int cols, blocks, tc, tr;  // channels of a block, blocks, vectors of a block, rows at a time
+  int cg, tiles;             // channels of a group, tiles
+  int64_t rows, segments;    // rows of a tile, segments
+  Divider by_tc, by_tr, by_cols, by_cg, by_blocks, by_tiles;
+};
+template <int VEC>
+Tiles tiles_of(const GroupArgs& a, int least) {
+  Tiles p;
+  p.cg = a.channels / a.groups;
+  const int64_t nvec = ceil_div(a.channels, VEC);
+  p.blocks = (int)ceil_div(nvec, 32);
+  p.tc = (int)ceil_div(nvec, p.blocks);
+  p.cols = p.tc * VEC;
+  p.blocks = (int)ceil_div(a.channels, p.cols);
+  p.tr = kBlock / p.tc;
+  p.segments = (int64_t)a.groups + p.blocks;
+  // enough work-groups for the card, with `least` rows to a thread at least.  About 2048: 8 x 256^2 x
+  // 128 bf16 forward 87 us at 512, 79 at 1024 to 4096, 95 at 8192; backward 155, 132, 135, 147, 146.
+  const int64_t want = ceil_div(2048, std::max<int64_t>(1, a.batch * p.blocks));
+  const int64_t tiles =  // (rows of a tile fit 31 bits)
+      std::max(ceil_div(a.npts, (int64_t)1 << 30),
+               std::min(ceil_div(a.npts, (int64_t)p.tr * least), want));
+  p.rows = std::max<int64_t>(1, ceil_div(a.npts, tiles));
+  p.tiles = (int)std::max<int64_t>(1, ceil_div(a.npts, p.rows));
+  p.by_tc = Divider(p.tc);
+  p.by_tr = Divider(p.tr);
+  p.by_cols = Divider(p.cols);
+  p.by_cg = Divider(p.cg);
+  p.by_blocks = Divider(p.blocks);
+  p.by_tiles = Divider(p.tiles);
+  return p;
+}
+// Whether the forward's second pass joins the parts for itself, which saves a launch: few enough for
+// a work-group's threads.
+bool joins(const Tiles& p) {
+  const int64_t in_block = std::min<int64_t>(p.cols, (p.cols + p.cg - 1) / p.cg + 1);
+  const int64_t in_group = std::min<int64_t>(p.blocks, (p.cg + p.cols - 1) / p.cols + 1);
+  return in_block * in_group * p.tiles <= 1024;
+}
+
+struct Block {
+  int64_t b, row0;     // entry, first row
+  int k, tile, rows;   // column block, tile, rows of it
+  int c0, c1, g0, segs;  // channels, first group, groups that it touches
+};
+__device__ __forceinline__ Block block_of(int64_t w, const GroupArgs& a, const Tiles& p) {
+  Block q;
+  const int64_t rest = p.by_blocks.of(w);
+  q.k = (int)(w - rest * p.blocks);
+  q.b = p.by_tiles.of(rest);
+  q.tile = (int)(rest - q.b * p.tiles);
+  q.row0 = q.tile * p.rows;
+  q.rows = (int)(p.rows < a.npts - q.row0 ? p.rows : a.npts - q.row0);
+  q.c0 = q.k * p.cols;
+  q.c1 = q.c0 + p.cols < a.channels ? q.c0 + p.cols : a.channels;
+  q.g0 = (int)p.by_cg.of((uint32_t)q.c0);
+  q.segs = (int)p.by_cg.of((uint32_t)q.c1 - 1) - q.g0 + 1;
+  return q;
+}
+// A thread's vector in a block: its first channel, and its own elements (as Items).
+template <int VEC>
+__device__ __forceinline__ void vector_of(const Block& q, const Tiles& p, int channels, int& r,
+                                          int& c, int& lo) {
+  r = (int)p.by_tc.of((uint32_t)threadIdx.x);
+  const int at = q.c0 + (threadIdx.x - r * p.tc) * VEC;
+  c = at < channels - VEC ? at : channels - VEC;
+  lo = r < p.tr && at < channels ? at - c : VEC;
+}
+
+// Rows r, r + tr, ... of a tile, K at a time: all(at), and one(at) for the last ones; `at` is the
+// element that slot 0's row begins with, the same for the whole work-group, so that a thread has one
+// offset of its own for all its rows.
+template <int K, typename All, typename One>
+__device__ __forceinline__ void tile_rows(const Tiles& p, const Block& q, int r, int channels,
+                                          All&& all, One&& one) {
+  int i = 0;
+  for (; i + K * p.tr <= q.rows; i += K * p.tr) all((q.row0 + i) * channels);
+  for (; i < q.rows; i += p.tr)
+    if (i + r < q.rows) one((q.row0 + i) * channels);
+}
+template <typename T, int VEC, int K>
+__device__ __forceinline__ void load_rows(const T* p, int64_t step, int64_t own,
+                                          Raw<T, VEC> (&raw)[K]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) raw[k] = load_raw<T, VEC, true>(p + k * step + own);
+}
+
+// Lanes to a segment of at most `width` channels: a power of two, so that the segments take the
+// work-group between them.
+__device__ __forceinline__ int lanes_of(int segs, int width) {
+  int l = 64;
+  while (l > 1 && (l * segs > kBlock || l / 2 >= width)) l >>= 1;
+  return l;
+}
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+  for (int m = 1; m < lanes; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+// Calls f(segment, its first channel in the block, its width, lane, lanes) in the lanes of each.
+template <typename F>
+__device__ __forceinline__ void each_segment(const Tiles& p, const Block& q, F&& f) {
+  const int lanes = lanes_of(q.segs, min(p.cg, p.cols)), lane = threadIdx.x & (lanes - 1);
+  for (int s = threadIdx.x / lanes; s < q.segs; s += kBlock / lanes) {
+    const int g = q.g0 + s, from = max(q.c0, g * p.cg), to = min(q.c1, (g + 1) * p.cg);
+    f(s, from - q.c0, to - from, lane, lanes);
+  }
+}
+// The threads of a block's channels, in sets that share the row slots.
+struct Columns {
+  int sets, set, c;  // set >= sets: none
+  __device__ __forceinline__ explicit Columns(const Tiles& p) {
+    sets = max(1, min((int)p.by_cols.of((uint32_t)kBlock), p.tr));
+    set = (int)p.by_cols.of((uint32_t)threadIdx.x);
+    c = threadIdx.x - set * p.cols;
+  }
+};
+
+// part [batch][segments][tiles]: mean, squared deviations over m
+template <typename T, int VEC, int K>
+__global__ __launch_bounds__(kBlock) void k_gn_stats_last(GroupArgs a, Tiles p, int64_t total,
+                                                          const T* x, float2* part) {
+  __shared__ float2 s_mom[kBlock * VEC];  // [tr][cols]
+  __shared__ float s_set[kBlock], s_mean[32 * VEC];
+  const float inv_m = 1.0f / ((float)p.cg * (float)a.npts);
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+    const Block q = block_of(w, a, p);
+    int r, c, lo;
+    vector_of<VEC>(q, p, a.channels, r, c, lo);
+    float n = 0.f, mean[VEC], var[VEC];
+    fill(mean, 0.f);
+    fill(var, 0.f);
+    if (lo < VEC) {
+      const T* from = x + q.b * a.x_stride;
+      const int64_t own = (int64_t)r * a.channels + c;
+      const auto add = [&](const auto& raw) {
+        constexpr int N = sizeof(raw) / sizeof(raw[0]);
+        const float all = n + N, share = N * __builtin_amdgcn_rcpf(all);
+        const float between = share * (n * inv_m);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float sum = 0.f, sq = 0.f;
+#pragma unroll
+          for (int k = 0; k < N; ++k) sum += element<T, VEC>(raw[k], e);
+          const float m = sum * (1.0f / N);
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            const float d = element<T, VEC>(raw[k], e) - m;
+            sq += d * d;
+          }
+          const float d = m - mean[e];
+          mean[e] += d * share;
+          var[e] += sq * inv_m + (d * between) * d;
+        }
+        n = all;
+      };
+      tile_rows<K>(
+          p, q, r, a.channels,
+          [&](int64_t at) {
+            Raw<T, VEC> raw[K];
+            load_rows<T, VEC, K>(from + at, (int64_t)p.tr * a.channels, own, raw);
+            add(raw);
+          },
+          [&](int64_t at) {
+            const Raw<T, VEC> raw[1] = {load_raw<T, VEC, true>(from + at + own)};
+            add(raw);
+          });
+    }
+    __syncthreads();
+    if (lo < VEC)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e >= lo) s_mom[r * p.cols + c + e - q.c0] = make_float2(mean[e], var[e]);
+    __syncthreads();
+    // the row slots' moments of a segment: their mean first, then the deviations about it
+    const Columns col(p);
+    const int slots = min(p.tr, q.rows), width = q.c1 - q.c0;
+    const bool mine = col.set < col.sets && col.c < width;
+    // rows that slot i has seen: all rounds, and the last one where it is in it
+    const int rounds = (int)p.by_tr.of((uint32_t)q.rows), more = q.rows - rounds * p.tr;
+    const auto seen = [&](int i) { return (float)(rounds + (i < more)); };
+    float sum = 0.f;
+    if (mine) {
+      for (int i = col.set; i < slots; i += col.sets)
+        sum += seen(i) * s_mom[i * p.cols + col.c].x;
+      s_set[threadIdx.x] = sum;
+    }
+    __syncthreads();
+    each_segment(p, q, [&](int s, int from, int wide, int lane, int lanes) {
+      float v = 0.f;
+      for (int i = 0; i < col.sets; ++i)
+        for (int k = lane; k < wide; k += lanes) v += s_set[i * p.cols + from + k];
+      v = lanes_sum(v, lanes);
+      if (lane == 0) s_mean[s] = v / ((float)q.rows * (float)wide);
+    });
+    __syncthreads();
+    if (mine) {
+      const float m = s_mean[(int)p.by_cg.of((uint32_t)(q.c0 + col.c)) - q.g0];
+      sum = 0.f;
+      for (int i = col.set; i < slots; i += col.sets) {
+        const float2 v = s_mom[i * p.cols + col.c];
+        sum += v.y + ((v.x - m) * (seen(i) * inv_m)) * (v.x - m);
+      }
+      s_set[threadIdx.x] = sum;
+    }
+    __syncthreads();
+    each_segment(p, q, [&](int s, int from, int wide, int lane, int lanes) {
+      float v = 0.f;
+      for (int i = 0; i < col.sets; ++i)
+        for (int k = lane; k < wide; k += lanes) v += s_set[i * p.cols + from + k];
+      v = lanes_sum(v, lanes);
+      if (lane == 0)
+        part[(q.b * p.segments + q.g0 + s + q.k) * p.tiles + q.tile] = make_float2(s_mean[s], v);
+    });
+  }
+}
+
+// The column blocks that group g lies in.
+struct Span {
+  int first, blocks;
+};
+__device__ __forceinline__ Span span_of(const Tiles& p, int g) {
+  const int k0 = (int)p.by_cols.of((uint32_t)(g * p.cg));
+  const int k1 = (int)p.by_cols.of((uint32_t)((g + 1) * p.cg) - 1);
+  return {k0, k1 - k0 + 1};
+}
+// The parts of group g of entry b, one a tile for each of its segments.
+__device__ __forceinline__ const float2* parts_of(const Tiles& p, const float2* part, int64_t b,
+                                                  int g, const Span& sp) {
+  return part + (b * p.segments + g + sp.first) * p.tiles;
+}
+// Mean and r of group g of entry b from its parts, in `lanes` lanes.
+__device__ __forceinline__ float2 join_parts(const GroupArgs& a, const Tiles& p, const float2* part,
+                                             int64_t b, int g, int lane, int lanes) {
+  const float inv = 1.0f / ((float)p.cg * (float)a.npts);
+  const Span sp = span_of(p, g);
+  const float2* from = parts_of(p, part, b, g, sp);
+  const auto share = [&](int i) {  // of the group's entries in part i
+    const int k = (int)p.by_tiles.of((uint32_t)i), block = sp.first + k;
+    const int width = (int)(min((int64_t)(block + 1) * p.cols, (int64_t)(g + 1) * p.cg) -
+                            max((int64_t)block * p.cols, (int64_t)g * p.cg));
+    const int64_t row0 = (i - k * p.tiles) * p.rows;
+    const int64_t rows = p.rows < a.npts - row0 ? p.rows : a.npts - row0;
+    return (float)rows * inv * (float)width;
+  };
+  float mean = 0.f, var = 0.f;
+  for (int i = lane; i < sp.blocks * p.tiles; i += lanes) mean += share(i) * from[i].x;
+  mean = lanes_sum(mean, lanes);
+  for (int i = lane; i < sp.blocks * p.tiles; i += lanes) {
+    const float2 v = from[i];
+    var += v.y + ((v.x - mean) * share(i)) * (v.x - mean);
+  }
+  return make_float2(mean, rsqrtf(lanes_sum(var, lanes) + a.eps));
+}
+
+// stats [2][batch * groups] from the parts, a wave to a group
+__global__ __launch_bounds__(kBlock) void k_gn_finish_last(GroupArgs a, Tiles p,
+                                                           Divider by_groups, const float2* part,
+                                                           float* stats) {
+  const int64_t sides = a.batch * a.groups;
+  for (int64_t i = (int64_t)blockIdx.x * kWaves + threadIdx.x / 64; i < sides;
+       i += (int64_t)gridDim.x * kWaves) {
+    const int64_t b = by_groups.of(i);
+    const float2 st = join_parts(a, p, part, b, (int)(i - b * a.groups), threadIdx.x % 64, 64);
+    if (threadIdx.x % 64 == 0) {
+      stats[i] = st.x;
+      stats[sides + i] = st.y;
+    }
+  }
+}
+
+// What s holds for the groups of a thread's channels.
+template <int VEC, bool EVEN>
+__device__ __forceinline__ void by_group(const Tiles& p, const Block& q, int c, const float2* s,
+                                         float (&u)[VEC], float (&v)[VEC]) {
+  if (EVEN) {
+    const float2 t = s[(int)p.by_cg.of((uint32_t)c) - q.g0];
+    fill(u, t.x);
+    fill(v, t.y);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    const float2 t = s[max((int)p.by_cg.of((uint32_t)(c + e)) - q.g0, 0)];
+    u[e] = t.x;
+    v[e] = t.y;
+  }
+}
+// a thread's channels' mean, r, gamma and beta
+template <int VEC, bool EVEN>
+__device__ __forceinline__ void channel_terms(const Tiles& p, const Block& q, int c,
+                                              const float* gamma, const float* beta,
+                                              const float2* s_st, float (&mu)[VEC],
+                                              float (&rs)[VEC], float (&ga)[VEC],
+                                              float (&be)[VEC]) {
+  by_group<VEC, EVEN>(p, q, c, s_st, mu, rs);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    ga[e] = gamma ? gamma[c + e] : 1.f;
+    be[e] = beta ? beta[c + e] : 0.f;
+  }
+}
+
+// the statistics of the groups that a block touches, as they are, into LDS
+__device__ __forceinline__ void given_stats(const GroupArgs& a, const Block& q, const float* stats,
+                                            float2* s_st) {
+  for (int s = threadIdx.x; s < q.segs; s += kBlock)
+    s_st[s] = make_float2(stats[q.b * a.groups + q.g0 + s],
+                          stats[(a.batch + q.b) * a.groups + q.g0 + s]);
+}
+
+// stats: given (part NULL), or made here from the parts and, nullable, written
+template <typename T, int VEC, int K, bool EVEN>
+__global__ __launch_bounds__(kBlock) void k_gn_apply_last(GroupArgs a, Tiles p, int64_t total,
+                                                          bool stream, const T* x,
+                                                          const float* gamma, const float* beta,
+                                                          const float2* part, T* y, float* stats) {
+  __shared__ float2 s_st[32 * VEC];
+  const Dropper drop(a.drop);
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+    const Block q = block_of(w, a, p);
+    int r, c, lo;
+    vector_of<VEC>(q, p, a.channels, r, c, lo);
+    __syncthreads();
+    if (part) {
+      each_segment(p, q, [&](int s, int, int, int lane, int lanes) {
+        const float2 st = join_parts(a, p, part, q.b, q.g0 + s, lane, lanes);
+        if (lane != 0) return;
+        s_st[s] = st;
+        // the block that has the group's first channel
+        if (stats && q.tile == 0 && (q.g0 + s) * (int64_t)p.cg >= q.c0) {
+          stats[q.b * a.groups + q.g0 + s] = st.x;
+          stats[(a.batch + q.b) * a.groups + q.g0 + s] = st.y;
+        }
+      });
+    } else {
+      given_stats(a, q, stats, s_st);
+    }
+    __syncthreads();
+    if (lo >= VEC) continue;
+    float mu[VEC], by[VEC], ga[VEC], be[VEC];
+    channel_terms<VEC, EVEN>(p, q, c, gamma, beta, s_st, mu, by, ga, be);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) by[e] *= ga[e];
+    const T* from = x + q.b * a.x_stride;
+    T* to = y + q.b * a.y_stride;
+    const int64_t index = q.b * a.npts * a.channels, own = (int64_t)r * a.channels + c;
+    const int64_t step = (int64_t)p.tr * a.channels;
+    const auto put = [&](const Raw<T, VEC>& raw, int64_t at) {
+      const uint32_t mask = a.drop.threshold ? drop.mask<VEC>((uint64_t)(index + at + own)) : 0;
+      float f[VEC];
+      unpack<T, VEC>(raw, f);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) f[e] = fmaf(f[e] - mu[e], by[e], be[e]);
+      activate(f, a.act);
+      if (a.drop.threshold) drop.apply<VEC>(f, mask);
+      store_own<T, VEC>(to + at + own, f, EVEN ? 0 : lo, stream);
+    };
+    tile_rows<K>(
+        p, q, r, a.channels,
+        [&](int64_t at) {
+          Raw<T, VEC> raw[K];
+          load_rows<T, VEC, K>(from + at, step, own, raw);
+#pragma unroll
+          for (int k = 0; k < K; ++k) put(raw[k], at + k * step);
+        },
+        [&](int64_t at) { put(load_raw<T, VEC, true>(from + at + own), at); });
+  }
+}
+
+// part: rows [batch * tiles] of [2][channels], sums of g h and g; seg [batch][segments][tiles]: sums
+// of gamma g and gamma g h
+template <typename T, int VEC, int K, bool EVEN>
+__global__ __launch_bounds__(kBlock) void k_gn_sums_last(GroupArgs a, Tiles p, int64_t total,
+                                                         const T* x, const float* gamma,
+                                                         const float* beta, const float* stats,
+                                                         const T* gy, float* part, float2* seg) {
+  __shared__ float2 s_st[32 * VEC], s_sum[kBlock * VEC], s_set[kBlock];
+  const Dropper drop(a.drop);
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+    const Block q = block_of(w, a, p);
+    int r, c, lo;
+    vector_of<VEC>(q, p, a.channels, r, c, lo);
+    __syncthreads();
+    given_stats(a, q, stats, s_st);
+    __syncthreads();
+    if (lo < VEC) {
+      float mu[VEC], rs[VEC], ga[VEC], be[VEC], sg[VEC], sb[VEC];
+      fill(sg, 0.f);
+      fill(sb, 0.f);
+      channel_terms<VEC, EVEN>(p, q, c, gamma, beta, s_st, mu, rs, ga, be);
+      const T* px = x + q.b * a.x_stride;
+      const T* pg = gy + q.b * a.y_stride;
+      const int64_t index = q.b * a.npts * a.channels, own = (int64_t)r * a.channels + c;
+      const int64_t step = (int64_t)p.tr * a.channels;
+      const auto add = [&](const Raw<T, VEC>& rx, const Raw<T, VEC>& rg, int64_t at) {
+        float h[VEC], g[VEC];
+        backward_terms<T, VEC>(a, drop, rx, rg, mu, rs, ga, be, (uint64_t)(index + at + own), h,
+                               g);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          sg[e] += g[e] * h[e];
+          sb[e] += g[e];
+        }
+      };
+      tile_rows<K>(
+          p, q, r, a.channels,
+          [&](int64_t at) {
+            Raw<T, VEC> rx[K], rg[K];
+            load_rows<T, VEC, K>(px + at, step, own, rx);
+            load_rows<T, VEC, K>(pg + at, step, own, rg);
+#pragma unroll
+            for (int k = 0; k < K; ++k) add(rx[k], rg[k], at + k * step);
+          },
+          [&](int64_t at) {
+            add(load_raw<T, VEC, true>(px + at + own), load_raw<T, VEC, true>(pg + at + own), at);
+          });
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e >= lo) s_sum[r * p.cols + c + e - q.c0] = make_float2(sg[e], sb[e]);
+    }
+    __syncthreads();
+    const Columns col(p);
+    const int slots = min(p.tr, q.rows), width = q.c1 - q.c0;
+    if (col.set < col.sets && col.c < width) {
+      float2 v = make_float2(0.f, 0.f);
+      for (int i = col.set; i < slots; i += col.sets) {
+        v.x += s_sum[i * p.cols + col.c].x;
+        v.y += s_sum[i * p.cols + col.c].y;
+      }
+      s_set[threadIdx.x] = v;
+    }
+    __syncthreads();
+    float* row = part + (q.b * p.tiles + q.tile) * 2 * a.channels + q.c0;
+    if ((int)threadIdx.x < width) {  // (a block has at most 256 channels)
+      float2 v = s_set[threadIdx.x];
+      for (int i = 1; i < col.sets; ++i) {
+        v.x += s_set[i * p.cols + threadIdx.x].x;
+        v.y += s_set[i * p.cols + threadIdx.x].y;
+      }
+      row[threadIdx.x] = v.x;
+      row[a.channels + threadIdx.x] = v.y;
+      const float weight = gamma ? gamma[q.c0 + threadIdx.x] : 1.f;
+      s_set[threadIdx.x] = make_float2(weight * v.y, weight * v.x);
+    }
+    __syncthreads();
+    each_segment(p, q, [&](int s, int from, int wide, int lane, int lanes) {
+      float u = 0.f, v = 0.f;
+      for (int k = lane; k < wide; k += lanes) {
+        u += s_set[from + k].x;
+        v += s_set[from + k].y;
+      }
+      u = lanes_sum(u, lanes);
+      v = lanes_sum(v, lanes);
+      if (lane == 0)
+        seg[(q.b * p.segments + q.g0 + s + q.k) * p.tiles + q.tile] = make_float2(u, v);
+    });
+  }
+}
+
+template <typename T, int VEC, int K, bool EVEN>
+__global__ __launch_bounds__(kBlock) void k_gn_grad_last(GroupArgs a, Tiles p, int64_t total,
+                                                         bool stream, const T* x,
+                                                         const float* gamma, const float* beta,
+                                                         const float* stats, const T* gy,
+                                                         const float2* means, T* gx) {
+  __shared__ float2 s_st[32 * VEC], s_m[32 * VEC];
+  const Dropper drop(a.drop);
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+    const Block q = block_of(w, a, p);
+    int r, c, lo;
+    vector_of<VEC>(q, p, a.channels, r, c, lo);
+    __syncthreads();
+    given_stats(a, q, stats, s_st);
+    for (int s = threadIdx.x; s < q.segs; s += kBlock)
+      s_m[s] = means[q.b * a.groups + q.g0 + s];
+    __syncthreads();
+    if (lo >= VEC) continue;
+    float mu[VEC], rs[VEC], ga[VEC], be[VEC], m1[VEC], m2[VEC];
+    channel_terms<VEC, EVEN>(p, q, c, gamma, beta, s_st, mu, rs, ga, be);
+    by_group<VEC, EVEN>(p, q, c, s_m, m1, m2);
+    const T* px = x + q.b * a.x_stride;
+    const T* pg = gy + q.b * a.y_stride;
+    T* to = gx + q.b * a.gx_stride;
+    const int64_t index = q.b * a.npts * a.channels, own = (int64_t)r * a.channels + c;
+    const int64_t step = (int64_t)p.tr * a.channels;
+    const auto put = [&](const Raw<T, VEC>& rx, const Raw<T, VEC>& rg, int64_t at) {
+      float h[VEC], g[VEC];
+      backward_terms<T, VEC>(a, drop, rx, rg, mu, rs, ga, be, (uint64_t)(index + at + own), h, g);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g[e] = rs[e] * fmaf(ga[e], g[e], -fmaf(h[e], m2[e], m1[e]));
+      store_own<T, VEC>(to + at + own, g, EVEN ? 0 : lo, stream);
+    };
+    tile_rows<K>(
+        p, q, r, a.channels,
+        [&](int64_t at) {
+          Raw<T, VEC> rx[K], rg[K];
+          load_rows<T, VEC, K>(px + at, step, own, rx);
+          load_rows<T, VEC, K>(pg + at, step, own, rg);
+#pragma unroll
+          for (int k = 0; k < K; ++k) put(rx[k], rg[k], at + k * step);
+        },
+        [&](int64_t at) {
+          put(load_raw<T, VEC, true>(px + at + own), load_raw<T, VEC, true>(pg + at + own), at);
+        });
+  }
+}
+
+__global__ __launch_bounds__(kBlock) void k_gn_between_last(GroupArgs a, Tiles p, Between z,
+                                                            const float2* seg) {
+  between(a, z, [&](int64_t b, int g) {
+    const Span sp = span_of(p, g);
+    const float2* from = parts_of(p, seg, b, g, sp);
+    float2 v = make_float2(0.f, 0.f);
+    for (int k = threadIdx.x; k < sp.blocks * p.tiles; k += kBlock) {
+      v.x += from[k].x;
+      v.y += from[k].y;
+    }
+    return v;
+  });
+}
+
+// ---- launches ------------------------------------------------------------------------------------
+// Four elements to a vector: eight halves, whose weights and sums each thread keeps for all its rows,
+// need twice the registers.  K rows to a thread at a time, 64 bytes of each field.
+constexpr int kVecLast = 4;
+template <typename T, int VEC>
+constexpr int kRowsAhead = VEC * (int)sizeof(T) == 8 ? 8 : 4;
+// rows of a tile for each thread, at least.  In the backward a tile's sums are written and read again.
+constexpr int kLeastFwd = 8, kLeastBwd = 16;
+bool even(const GroupArgs& a) { return a.channels / a.groups % kVecLast == 0; }
+
+template <typename F>
+auto pick(const GroupArgs& a, F&& f) {
+  return by_vector<kVecLast>(a.channels, f);
+}
+
+template <typename T>
+hipError_t fwd(const GroupArgs& a, const T* x, const float* gamma, const float* beta, T* y,
+               float* stats, void* ws, hipStream_t s) {
+  pick(a, [&](auto vec) {
+    constexpr int V = vec.value, K = kRowsAhead<T, V>;
+    const Tiles p = tiles_of<V>(a, kLeastFwd);
+    const int64_t total = a.batch * p.tiles * p.blocks;
+    float2* part = static_cast<float2*>(ws);
+    hipLaunchKernelGGL((k_gn_stats_last<T, V, K>), grid_of(total), dim3(kBlock), 0, s, a, p, total,
+                       x, part);
+    if (!joins(p)) {
+      const int64_t sides = a.batch * a.groups;
+      if (!stats)
+        stats = reinterpret_cast<float*>(
+            static_cast<char*>(ws) + up((int64_t)sizeof(float2) * a.batch * p.segments * p.tiles));
+      hipLaunchKernelGGL(k_gn_finish_last, grid_of(ceil_div(sides, kWaves)), dim3(kBlock), 0, s, a,
+                         p, Divider(a.groups), part, stats);
+      part = nullptr;
+    }
+    const auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid_of(total), dim3(kBlock), 0, s, a, p, total, stream_out<T>(a), x,
+                         gamma, beta, part, y, stats);
+    };
+    if (V > 1 && even(a)) go(k_gn_apply_last<T, V, K, V != 1>);
+    else go(k_gn_apply_last<T, V, K, false>);
+  });
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t bwd(const GroupArgs& a, const T* x, const float* gamma, const float* beta,
+               const float* stats, const T* gy, T* gx, float* ggamma, float* gbeta, void* ws,
+               hipStream_t s) {
+  pick(a, [&](auto vec) {
+    constexpr int V = vec.value, K = 4;
+    const Tiles p = tiles_of<V>(a, kLeastBwd);
+    const int64_t total = a.batch * p.tiles * p.blocks;
+    const Space z(a, a.batch * p.tiles, a.batch * p.segments * p.tiles);
+    const Between q = z.between(a, ws, gx != nullptr, ggamma, gbeta);
+    const auto go = [&](auto first, auto second) {
+      hipLaunchKernelGGL(first, grid_of(total), dim3(kBlock), 0, s, a, p, total, x, gamma, beta,
+                         stats, gy, static_cast<float*>(ws), z.segments_at(ws));
+      hipLaunchKernelGGL(k_gn_between_last, Space::grid(a, q), dim3(kBlock), 0, s, a, p, q,
+                         z.segments_at(ws));
+      if (gx)
+        hipLaunchKernelGGL(second, grid_of(total), dim3(kBlock), 0, s, a, p, total, stream_out<T>(a),
+                           x, gamma, beta, stats, gy, z.means_at(ws), gx);
+    };
+    if (V > 1 && even(a)) go(k_gn_sums_last<T, V, K, V != 1>, k_gn_grad_last<T, V, K, V != 1>);
+    else go(k_gn_sums_last<T, V, K, false>, k_gn_grad_last<T, V, K, false>);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t group_norm_last_fwd_bytes(const GroupArgs& a) {
+  return pick(a, [&](auto vec) {
+    const Tiles p = tiles_of<vec.value>(a, kLeastFwd);
+    return up((int64_t)sizeof(float2) * a.batch * p.segments * p.tiles) +
+           (joins(p) ? 0 : up((int64_t)sizeof(float) * 2 * a.batch * a.groups));
+  });
+}
+
+size_t group_norm_last_bwd_bytes(const GroupArgs& a) {
+  return pick(a, [&](auto vec) {
+    const Tiles p = tiles_of<vec.value>(a, kLeastBwd);
+    return Space(a, a.batch * p.tiles, a.batch * p.segments * p.tiles).bytes();
+  });
+}
+
+hipError_t launch_group_norm_last_fwd(const GroupArgs& a, int dtype, const void* x,
+                                      const float* gamma, const float* beta, void* y, float* stats,
+                                      void* ws, hipStream_t s) {
+  return by_type(dtype, [&](auto t) {
+    typedef decltype(t) T;
+    return fwd<T>(a, static_cast<const T*>(x), gamma, beta, static_cast<T*>(y), stats, ws, s);
+  });
+}
+
+hipError_t launch_group_norm_last_bwd(const GroupArgs& a, int dtype, const void* x,
+                                      const float* gamma, const float* beta, const float* stats,
+                                      const void* gy, void* gx, float* ggamma, float* gbeta,
+                                      void* ws, hipStream_t s) {
+  return by_type(dtype, [&](auto t) {
+    typedef decltype(t) T;
+    return bwd<T>(a, static_cast<const T*>(x), gamma, beta, stats, static_cast<const T*>(gy),
+                  static_cast<T*>(gx), ggamma, gbeta, ws, s);
+  });
+}
+
+}  // namespace fno
