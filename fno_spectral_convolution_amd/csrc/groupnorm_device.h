@@ -75,6 +75,18 @@ __device__ __forceinline__ float2 block_sum(float a, float b, float2* s) {
   return t;
 }
 
+// Sum over aligned groups of `lanes` lanes, a power of two that all lanes agree on, in each of them
+// (as lane_sum).
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+  if (lanes >= 2) v += dpp<0xb1>(v);
+  if (lanes >= 4) v += dpp<0x4e>(v);
+  if (lanes >= 8) v += dpp<0x141>(v);
+  if (lanes >= 16) v += dpp<0x140>(v);
+  if (lanes >= 32) v = add_across<16>(v);
+  if (lanes >= 64) v = add_across<32>(v);
+  return v;
+}
+
 // Count, mean, and the sum of squared deviations over the m entries of the whole group: a share of
 // its variance, which stays in range where the sum by itself would pass float32's.
 struct Moments {
@@ -139,14 +151,14 @@ __device__ __forceinline__ void store_own(T* o, const float (&f)[VEC], int lo,
   }
 }
 
-// What both backward passes need of an element: h = (x - mu) r, g = act'(u) drop(grad_y).
+// What both backward passes need of an element: h = (x - mu) r, g = act'(u) drop(grad_y), by its mask.
 template <typename T, int VEC>
 __device__ __forceinline__ void backward_terms(const GroupArgs& a, const Dropper& drop,
                                                const Raw<T, VEC>& rx, const Raw<T, VEC>& rg,
                                                const float (&mu)[VEC], const float (&rs)[VEC],
                                                const float (&ga)[VEC], const float (&be)[VEC],
-                                               uint64_t i, float (&h)[VEC], float (&g)[VEC]) {
-  const uint32_t mask = a.drop.threshold ? drop.mask<VEC>(i) : 0;
+                                               uint32_t mask, float (&h)[VEC],
+                                               float (&g)[VEC]) {
   unpack<T, VEC>(rx, h);
   unpack<T, VEC>(rg, g);
 #pragma unroll

@@ -333,7 +333,8 @@ __device__ __forceinline__ void plane_terms(const GroupArgs& a, const Dropper& d
   fill(rs, rstd);
   fill(ga, weight);
   fill(be, bias);
-  backward_terms<T, VEC>(a, drop, rx, rg, mu, rs, ga, be, i, h, g);
+  const uint32_t mask = a.drop.threshold ? drop.mask<VEC>(i) : 0;
+  backward_terms<T, VEC>(a, drop, rx, rg, mu, rs, ga, be, mask, h, g);
 }
 // grad_x of it, m1 and m2 the means of gamma g and gamma g h
 template <typename T, int VEC>
@@ -362,10 +363,8 @@ struct PlaneSums {
   // the sums of pass `i` over the planes are complete in their threads
   __device__ __forceinline__ void flush(int i) {
     const int lanes = 1 << min(p.tpp, 6);
-    for (int m = 1; m < lanes; m <<= 1) {
-      sg += __shfl_xor(sg, m);
-      sb += __shfl_xor(sb, m);
-    }
+    sg = lanes_sum(sg, lanes);
+    sb = lanes_sum(sb, lanes);
     const int c = i * (BLOCK >> p.tpp) + (threadIdx.x >> p.tpp);
     if (p.tpp > 6) {
       if (threadIdx.x % 64 == 0) s[i][threadIdx.x / 64] = make_float2(sg, sb);
@@ -613,6 +612,15 @@ __device__ __forceinline__ void place(int j, int d, int& start, int& lo) {
   lo = e < d ? e - start : VEC;
 }
 
+// Whether any lane of the wave has elements that are not its own.
+template <int NV>
+__device__ __forceinline__ bool any_partial(const int (&lo)[NV]) {
+  bool partial = false;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) partial |= lo[k] != 0;
+  return __any(partial);
+}
+
 // Sum over a slot's threads, in all of them.  Slots of several waves go through `s`, whose two halves
 // are taken in turn: one barrier a sum.
 template <int TPR, int BLOCK>
@@ -654,27 +662,40 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows(GroupArgs a, int cg, Divider 
       be[k][e] = beta ? beta[start[k] + e] : 0.f;
     }
   }
+  const bool partial = any_partial(lo);
   int flip = 0;
-  // every thread of the work-group goes round as often as the first slot, for the barriers
+  // every thread of the work-group goes round as often as the first slot, for the barriers; the next
+  // row's loads go ahead of this one's sums
   int64_t b = row0;
+  Raw<T, VEC> next[NV];
+  const auto fetch = [&](int64_t row) {
+    const T* p = x + (row < a.batch ? row : a.batch - 1) * a.x_stride;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) next[k] = load_raw<T, VEC, true>(p + start[k]);
+  };
+  fetch(b);
   for (int64_t at = (int64_t)blockIdx.x * kSlots; at < total; at += stride, b += rows) {
     const bool live = b < a.batch;
-    const T* p = x + (live ? b : a.batch - 1) * a.x_stride;
     float f[NV][VEC], sum = 0.f, sq = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      load_pack<T, VEC>(p + start[k], f[k]);
+    for (int k = 0; k < NV; ++k) unpack<T, VEC>(next[k], f[k]);
+    if (at + stride < total) fetch(b + rows);
+    by_mask(partial, [&](auto masked) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) sum += e >= lo[k] ? f[k][e] : 0.f;
-    }
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum += !masked.value || e >= lo[k] ? f[k][e] : 0.f;
+    });
     const float mean = slot_sum<TPR, BLOCK>(sum, s_sum, flip) * inv;
+    by_mask(partial, [&](auto masked) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+      for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        f[k][e] -= mean;
-        sq += e >= lo[k] ? f[k][e] * f[k][e] : 0.f;
-      }
+        for (int e = 0; e < VEC; ++e) {
+          f[k][e] -= mean;
+          sq += !masked.value || e >= lo[k] ? f[k][e] * f[k][e] : 0.f;
+        }
+    });
     const float rstd = rsqrtf(slot_sum<TPR, BLOCK>(sq * inv, s_sum, flip) + a.eps);
     if (!live) continue;
     T* o = y + b * a.y_stride;
@@ -729,6 +750,7 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows_bwd(GroupArgs a, int cg, Divi
       dg[k][e] = db[k][e] = 0.f;
     }
   }
+  const bool partial = any_partial(lo);
   int flip = 0;
   const int64_t step = (int64_t)(gridDim.x / chunks) * deep;
   for (int64_t base = (int64_t)(blockIdx.x / chunks) * deep; base < a.batch; base += step) {
@@ -748,8 +770,9 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows_bwd(GroupArgs a, int cg, Divi
       float mu[VEC], rs[VEC];
       fill(mu, mean);
       fill(rs, rstd);
-      backward_terms<T, VEC>(a, drop, rx[k], rg[k], mu, rs, ga[k], be[k],
-                             (uint64_t)(b * a.channels + start[k]), h[k], v[k]);
+      const uint32_t mask =
+          a.drop.threshold ? drop.mask<VEC>((uint64_t)(b * a.channels + start[k])) : 0;
+      backward_terms<T, VEC>(a, drop, rx[k], rg[k], mu, rs, ga[k], be[k], mask, h[k], v[k]);
       if (WEIGHTS && live) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -757,13 +780,17 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows_bwd(GroupArgs a, int cg, Divi
           db[k][e] += v[k][e];
         }
       }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        v[k][e] *= ga[k][e];
-        s1 += e >= lo[k] ? v[k][e] : 0.f;
-        s2 += e >= lo[k] ? v[k][e] * h[k][e] : 0.f;
-      }
     }
+    by_mask(partial, [&](auto masked) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          v[k][e] *= ga[k][e];
+          s1 += !masked.value || e >= lo[k] ? v[k][e] : 0.f;
+          s2 += !masked.value || e >= lo[k] ? v[k][e] * h[k][e] : 0.f;
+        }
+    });
     s1 = slot_sum<TPR, BLOCK>(s1, s_sum, flip) * inv;
     s2 = slot_sum<TPR, BLOCK>(s2, s_sum, flip) * inv;
     if (!gx || !live) continue;

@@ -15,25 +15,32 @@ struct Tiles {
   int cols, blocks, tc, tr;  // channels of a block, blocks, vectors of a block, rows at a time
   int cg, tiles;             // channels of a group, tiles
   int64_t rows, segments;    // rows of a tile, segments
+  bool paired;               // lanes 2 j and 2 j + 1 have neighbouring vectors of eight aligned elements
   Divider by_tc, by_tr, by_cols, by_cg, by_blocks, by_tiles;
 };
+// rows of a tile for each thread, at least
+constexpr int kLeast = 8;
 template <int VEC>
-Tiles tiles_of(const GroupArgs& a, int least) {
+Tiles tiles_of(const GroupArgs& a) {
   Tiles p;
   p.cg = a.channels / a.groups;
   const int64_t nvec = ceil_div(a.channels, VEC);
   p.blocks = (int)ceil_div(nvec, 32);
   p.tc = (int)ceil_div(nvec, p.blocks);
+  p.paired = VEC == 4 && a.channels % 8 == 0;
+  if (p.paired) p.tc += p.tc % 2;
   p.cols = p.tc * VEC;
   p.blocks = (int)ceil_div(a.channels, p.cols);
   p.tr = kBlock / p.tc;
   p.segments = (int64_t)a.groups + p.blocks;
-  // enough work-groups for the card, with `least` rows to a thread at least.  About 2048: 8 x 256^2 x
-  // 128 bf16 forward 87 us at 512, 79 at 1024 to 4096, 95 at 8192; backward 155, 132, 135, 147, 146.
-  const int64_t want = ceil_div(2048, std::max<int64_t>(1, a.batch * p.blocks));
+  // As many work-groups as the card holds at a time (four a compute unit), with kLeast rows to a
+  // thread at least: a second, short round costs as much as a whole one.  4 x 96^2 x 320 half backward
+  // with dropout 50 us, 58 with 1280 work-groups; 2 x 10^6 x 20 half 93, 108 with 1280, 101 with 2048.
+  const int64_t want =
+      std::max<int64_t>(1, 1024 / std::max<int64_t>(1, a.batch * p.blocks));
   const int64_t tiles =  // (rows of a tile fit 31 bits)
       std::max(ceil_div(a.npts, (int64_t)1 << 30),
-               std::min(ceil_div(a.npts, (int64_t)p.tr * least), want));
+               std::min(ceil_div(a.npts, (int64_t)p.tr * kLeast), want));
   p.rows = std::max<int64_t>(1, ceil_div(a.npts, tiles));
   p.tiles = (int)std::max<int64_t>(1, ceil_div(a.npts, p.rows));
   p.by_tc = Divider(p.tc);
@@ -99,16 +106,19 @@ __device__ __forceinline__ void load_rows(const T* p, int64_t step, int64_t own,
   for (int k = 0; k < K; ++k) raw[k] = load_raw<T, VEC, true>(p + k * step + own);
 }
 
+// The masks of a thread's K rows from element i on, four bits each.
+template <int VEC, int K>
+__device__ __forceinline__ uint32_t row_masks(const GroupArgs& a, const Dropper& drop, int64_t i,
+                                              int64_t step, bool paired) {
+  return a.drop.threshold ? drop.masks<VEC, K>((uint64_t)i, step, paired) : 0;
+}
+
 // Lanes to a segment of at most `width` channels: a power of two, so that the segments take the
 // work-group between them.
 __device__ __forceinline__ int lanes_of(int segs, int width) {
   int l = 64;
   while (l > 1 && (l * segs > kBlock || l / 2 >= width)) l >>= 1;
   return l;
-}
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
-  for (int m = 1; m < lanes; m <<= 1) v += __shfl_xor(v, m);
-  return v;
 }
 // Calls f(segment, its first channel in the block, its width, lane, lanes) in the lanes of each.
 template <typename F>
@@ -194,6 +204,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats_last(GroupArgs a, Tiles p, 
     const auto seen = [&](int i) { return (float)(rounds + (i < more)); };
     float sum = 0.f;
     if (mine) {
+#pragma unroll 4
       for (int i = col.set; i < slots; i += col.sets)
         sum += seen(i) * s_mom[i * p.cols + col.c].x;
       s_set[threadIdx.x] = sum;
@@ -202,14 +213,16 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats_last(GroupArgs a, Tiles p, 
     each_segment(p, q, [&](int s, int from, int wide, int lane, int lanes) {
       float v = 0.f;
       for (int i = 0; i < col.sets; ++i)
+#pragma unroll 4
         for (int k = lane; k < wide; k += lanes) v += s_set[i * p.cols + from + k];
       v = lanes_sum(v, lanes);
-      if (lane == 0) s_mean[s] = v / ((float)q.rows * (float)wide);
+      if (lane == 0) s_mean[s] = v * __builtin_amdgcn_rcpf((float)q.rows * (float)wide);
     });
     __syncthreads();
     if (mine) {
       const float m = s_mean[(int)p.by_cg.of((uint32_t)(q.c0 + col.c)) - q.g0];
       sum = 0.f;
+#pragma unroll 4
       for (int i = col.set; i < slots; i += col.sets) {
         const float2 v = s_mom[i * p.cols + col.c];
         sum += v.y + ((v.x - m) * (seen(i) * inv_m)) * (v.x - m);
@@ -220,6 +233,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats_last(GroupArgs a, Tiles p, 
     each_segment(p, q, [&](int s, int from, int wide, int lane, int lanes) {
       float v = 0.f;
       for (int i = 0; i < col.sets; ++i)
+#pragma unroll 4
         for (int k = lane; k < wide; k += lanes) v += s_set[i * p.cols + from + k];
       v = lanes_sum(v, lanes);
       if (lane == 0)
@@ -359,8 +373,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_apply_last(GroupArgs a, Tiles p, 
     T* to = y + q.b * a.y_stride;
     const int64_t index = q.b * a.npts * a.channels, own = (int64_t)r * a.channels + c;
     const int64_t step = (int64_t)p.tr * a.channels;
-    const auto put = [&](const Raw<T, VEC>& raw, int64_t at) {
-      const uint32_t mask = a.drop.threshold ? drop.mask<VEC>((uint64_t)(index + at + own)) : 0;
+    const auto put = [&](const Raw<T, VEC>& raw, int64_t at, uint32_t mask) {
       float f[VEC];
       unpack<T, VEC>(raw, f);
 #pragma unroll
@@ -374,10 +387,14 @@ __global__ __launch_bounds__(kBlock) void k_gn_apply_last(GroupArgs a, Tiles p, 
         [&](int64_t at) {
           Raw<T, VEC> raw[K];
           load_rows<T, VEC, K>(from + at, step, own, raw);
+          const uint32_t masks = row_masks<VEC, K>(a, drop, index + at + own, step, p.paired);
 #pragma unroll
-          for (int k = 0; k < K; ++k) put(raw[k], at + k * step);
+          for (int k = 0; k < K; ++k) put(raw[k], at + k * step, masks >> 4 * k);
         },
-        [&](int64_t at) { put(load_raw<T, VEC, true>(from + at + own), at); });
+        [&](int64_t at) {
+          const Raw<T, VEC> raw = load_raw<T, VEC, true>(from + at + own);
+          put(raw, at, row_masks<VEC, 1>(a, drop, index + at + own, 0, false));
+        });
   }
 }
 
@@ -406,10 +423,9 @@ __global__ __launch_bounds__(kBlock) void k_gn_sums_last(GroupArgs a, Tiles p, i
       const T* pg = gy + q.b * a.y_stride;
       const int64_t index = q.b * a.npts * a.channels, own = (int64_t)r * a.channels + c;
       const int64_t step = (int64_t)p.tr * a.channels;
-      const auto add = [&](const Raw<T, VEC>& rx, const Raw<T, VEC>& rg, int64_t at) {
+      const auto add = [&](const Raw<T, VEC>& rx, const Raw<T, VEC>& rg, uint32_t mask) {
         float h[VEC], g[VEC];
-        backward_terms<T, VEC>(a, drop, rx, rg, mu, rs, ga, be, (uint64_t)(index + at + own), h,
-                               g);
+        backward_terms<T, VEC>(a, drop, rx, rg, mu, rs, ga, be, mask, h, g);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           sg[e] += g[e] * h[e];
@@ -422,11 +438,14 @@ __global__ __launch_bounds__(kBlock) void k_gn_sums_last(GroupArgs a, Tiles p, i
             Raw<T, VEC> rx[K], rg[K];
             load_rows<T, VEC, K>(px + at, step, own, rx);
             load_rows<T, VEC, K>(pg + at, step, own, rg);
+            const uint32_t masks = row_masks<VEC, K>(a, drop, index + at + own, step, p.paired);
 #pragma unroll
-            for (int k = 0; k < K; ++k) add(rx[k], rg[k], at + k * step);
+            for (int k = 0; k < K; ++k) add(rx[k], rg[k], masks >> 4 * k);
           },
           [&](int64_t at) {
-            add(load_raw<T, VEC, true>(px + at + own), load_raw<T, VEC, true>(pg + at + own), at);
+            const Raw<T, VEC> rx = load_raw<T, VEC, true>(px + at + own);
+            const Raw<T, VEC> rg = load_raw<T, VEC, true>(pg + at + own);
+            add(rx, rg, row_masks<VEC, 1>(a, drop, index + at + own, 0, false));
           });
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
@@ -437,6 +456,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_sums_last(GroupArgs a, Tiles p, i
     const int slots = min(p.tr, q.rows), width = q.c1 - q.c0;
     if (col.set < col.sets && col.c < width) {
       float2 v = make_float2(0.f, 0.f);
+#pragma unroll 4
       for (int i = col.set; i < slots; i += col.sets) {
         v.x += s_sum[i * p.cols + col.c].x;
         v.y += s_sum[i * p.cols + col.c].y;
@@ -497,9 +517,9 @@ __global__ __launch_bounds__(kBlock) void k_gn_grad_last(GroupArgs a, Tiles p, i
     T* to = gx + q.b * a.gx_stride;
     const int64_t index = q.b * a.npts * a.channels, own = (int64_t)r * a.channels + c;
     const int64_t step = (int64_t)p.tr * a.channels;
-    const auto put = [&](const Raw<T, VEC>& rx, const Raw<T, VEC>& rg, int64_t at) {
+    const auto put = [&](const Raw<T, VEC>& rx, const Raw<T, VEC>& rg, int64_t at, uint32_t mask) {
       float h[VEC], g[VEC];
-      backward_terms<T, VEC>(a, drop, rx, rg, mu, rs, ga, be, (uint64_t)(index + at + own), h, g);
+      backward_terms<T, VEC>(a, drop, rx, rg, mu, rs, ga, be, mask, h, g);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) g[e] = rs[e] * fmaf(ga[e], g[e], -fmaf(h[e], m2[e], m1[e]));
       store_own<T, VEC>(to + at + own, g, EVEN ? 0 : lo, stream);
@@ -510,11 +530,14 @@ __global__ __launch_bounds__(kBlock) void k_gn_grad_last(GroupArgs a, Tiles p, i
           Raw<T, VEC> rx[K], rg[K];
           load_rows<T, VEC, K>(px + at, step, own, rx);
           load_rows<T, VEC, K>(pg + at, step, own, rg);
+          const uint32_t masks = row_masks<VEC, K>(a, drop, index + at + own, step, p.paired);
 #pragma unroll
-          for (int k = 0; k < K; ++k) put(rx[k], rg[k], at + k * step);
+          for (int k = 0; k < K; ++k) put(rx[k], rg[k], at + k * step, masks >> 4 * k);
         },
         [&](int64_t at) {
-          put(load_raw<T, VEC, true>(px + at + own), load_raw<T, VEC, true>(pg + at + own), at);
+          const Raw<T, VEC> rx = load_raw<T, VEC, true>(px + at + own);
+          const Raw<T, VEC> rg = load_raw<T, VEC, true>(pg + at + own);
+          put(rx, rg, at, row_masks<VEC, 1>(a, drop, index + at + own, 0, false));
         });
   }
 }
@@ -539,8 +562,6 @@ __global__ __launch_bounds__(kBlock) void k_gn_between_last(GroupArgs a, Tiles p
 constexpr int kVecLast = 4;
 template <typename T, int VEC>
 constexpr int kRowsAhead = VEC * (int)sizeof(T) == 8 ? 8 : 4;
-// rows of a tile for each thread, at least.  In the backward a tile's sums are written and read again.
-constexpr int kLeastFwd = 8, kLeastBwd = 16;
 bool even(const GroupArgs& a) { return a.channels / a.groups % kVecLast == 0; }
 
 template <typename F>
@@ -553,7 +574,7 @@ hipError_t fwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
                float* stats, void* ws, hipStream_t s) {
   pick(a, [&](auto vec) {
     constexpr int V = vec.value, K = kRowsAhead<T, V>;
-    const Tiles p = tiles_of<V>(a, kLeastFwd);
+    const Tiles p = tiles_of<V>(a);
     const int64_t total = a.batch * p.tiles * p.blocks;
     float2* part = static_cast<float2*>(ws);
     hipLaunchKernelGGL((k_gn_stats_last<T, V, K>), grid_of(total), dim3(kBlock), 0, s, a, p, total,
@@ -583,7 +604,7 @@ hipError_t bwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
                hipStream_t s) {
   pick(a, [&](auto vec) {
     constexpr int V = vec.value, K = 4;
-    const Tiles p = tiles_of<V>(a, kLeastBwd);
+    const Tiles p = tiles_of<V>(a);
     const int64_t total = a.batch * p.tiles * p.blocks;
     const Space z(a, a.batch * p.tiles, a.batch * p.segments * p.tiles);
     const Between q = z.between(a, ws, gx != nullptr, ggamma, gbeta);
@@ -606,7 +627,7 @@ hipError_t bwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
 
 size_t group_norm_last_fwd_bytes(const GroupArgs& a) {
   return pick(a, [&](auto vec) {
-    const Tiles p = tiles_of<vec.value>(a, kLeastFwd);
+    const Tiles p = tiles_of<vec.value>(a);
     return up((int64_t)sizeof(float2) * a.batch * p.segments * p.tiles) +
            (joins(p) ? 0 : up((int64_t)sizeof(float) * 2 * a.batch * a.groups));
   });
@@ -614,7 +635,7 @@ size_t group_norm_last_fwd_bytes(const GroupArgs& a) {
 
 size_t group_norm_last_bwd_bytes(const GroupArgs& a) {
   return pick(a, [&](auto vec) {
-    const Tiles p = tiles_of<vec.value>(a, kLeastBwd);
+    const Tiles p = tiles_of<vec.value>(a);
     return Space(a, a.batch * p.tiles, a.batch * p.segments * p.tiles).bytes();
   });
 }
