@@ -248,11 +248,12 @@ auto by_type(int dtype, F&& f) {
   if (dtype == FNO_DTYPE_F32) return f(0.f);
   return dtype == FNO_DTYPE_BF16 ? f((__bf16)0.f) : f((_Float16)0.f);
 }
-// Whether an output goes past the caches (nontemporal stores): where it is larger than the 256 MB
-// cache behind the L2s.
+// Whether an output goes past the caches (nontemporal stores): where it fills half of the 256 MB cache
+// behind the L2s (4 x 64 x 512^2 float32, 268 MB, backward 214 us against 219; 8 x 64 x 512^2 bf16, as
+// large, 242 against 252; below, no difference).
 template <typename T>
 bool stream_out(const GroupArgs& a) {
-  return a.batch * a.channels * a.npts > ((int64_t)256 << 20) / (int64_t)sizeof(T);
+  return a.batch * a.channels * a.npts > ((int64_t)128 << 20) / (int64_t)sizeof(T);
 }
 
 // A backward's workspace: the partial rows, the segments' sums (channels last), the means.

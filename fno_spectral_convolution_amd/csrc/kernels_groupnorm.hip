@@ -197,6 +197,7 @@ __global__ __launch_bounds__(BLOCK) void k_gn_whole(GroupArgs a, Strip p, int64_
 struct Pass {
   Strip p;
   int64_t items;  // work items
+  int joined;     // the first pass's parts of a group
   bool stream;    // the output goes past the caches
 };
 
@@ -271,7 +272,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_apply(GroupArgs a, Pass ps, const
   const Strip& p = ps.p;
   const Dropper drop(a.drop);
   const float inv_m = 1.0f / ((float)p.cg * (float)a.npts);
-  const int n = p.runs * p.parts;
+  const int n = ps.joined;
   for (int64_t w = blockIdx.x; w < ps.items; w += gridDim.x) {
     const Place q = place_of(w, p, a.groups);
     Moments m = {0.f, 0.f, 0.f};
@@ -900,6 +901,23 @@ bool pick_whole(const GroupArgs& a, F&& f) {
 }
 
 template <typename T>
+Pass pass_of(const GroupArgs& a, const Strip& p) {
+  return {p, a.batch * a.groups * p.runs * p.parts, p.runs * p.parts, stream_out<T>(a)};
+}
+// The second pass, with about `strips` strips to a work item: short items run faster than a work-group
+// that goes on from strip to strip (2 x 20 x 128^3 float32 backward, which has nothing to join, 264 us
+// with one, 269 with two, 310 with as many as the first pass has; 8 x 64 x 512^2 float32 forward 279,
+// 264 and 302).
+template <typename T>
+Pass second_of(const GroupArgs& a, const Strip& p, int strips) {
+  Pass q = pass_of<T>(a, p);
+  q.p.parts = (int)std::min<int64_t>(ceil_div(p.strips, strips), 1 << 30);
+  q.p.by_parts = Divider(q.p.parts);
+  q.items = a.batch * a.groups * p.runs * q.p.parts;
+  return q;
+}
+
+template <typename T>
 hipError_t rows_fwd(const GroupArgs& a, const T* x, const float* gamma, const float* beta, T* y,
                     float* stats, hipStream_t s) {
   by_vector<kVec<T>>(a.channels / a.groups, [&](auto vec) {
@@ -909,7 +927,7 @@ hipError_t rows_fwd(const GroupArgs& a, const T* x, const float* gamma, const fl
       // card, or as there are rows
       int64_t unit = a.groups;
       for (int64_t n = kSlots; n % 2 == 0 && unit % 2 == 0; n /= 2) unit /= 2;
-      const int64_t need = ceil_div(a.batch * a.groups, kSlots), most = 2048 * kBlock / kB;
+      const int64_t need = ceil_div(a.batch * a.groups, kSlots), most = 1024 * kBlock / kB;
       const int64_t groups = unit * std::max<int64_t>(1, std::min(ceil_div(need, unit), most / unit));
       hipLaunchKernelGGL((k_gn_rows<T, vec.value, TPR, nv.value, kB>), dim3(groups), dim3(kB), 0, s,
                          a, a.channels / a.groups, Divider(a.groups), groups * kSlots,
@@ -930,11 +948,11 @@ hipError_t first_fwd(const GroupArgs& a, const T* x, const float* gamma, const f
     });
     if (whole) return;
     const Strip p = strip_of<V, K, kBlock>(a);
-    const Pass q = {p, a.batch * a.groups * p.runs * p.parts, stream_out<T>(a)};
+    const Pass q = pass_of<T>(a, p), r = second_of<T>(a, p, 2);
     float4* part = static_cast<float4*>(ws);
     const auto go = [&](auto first, auto second) {
       hipLaunchKernelGGL(first, grid_of(q.items), dim3(kBlock), 0, s, a, q, x, part);
-      hipLaunchKernelGGL(second, grid_of(q.items), dim3(kBlock), 0, s, a, q, x, gamma, beta, part, y,
+      hipLaunchKernelGGL(second, grid_of(r.items), dim3(kBlock), 0, s, a, r, x, gamma, beta, part, y,
                          stats);
     };
     if (p.strips > 1) go(k_gn_stats<T, V, K, true>, k_gn_apply<T, V, K, true>);
@@ -1014,14 +1032,14 @@ hipError_t first_bwd(const GroupArgs& a, const T* x, const float* gamma, const f
     const Strip p = strip_of<V, K, kBlock>(a);
     const Space z(a, a.batch * p.parts, 0);
     const Between t = z.between(a, ws, gx != nullptr, ggamma, gbeta);
-    const Pass q = {p, a.batch * a.groups * p.runs * p.parts, stream_out<T>(a)};
+    const Pass q = pass_of<T>(a, p), r = second_of<T>(a, p, 1);
     const auto go = [&](auto first, auto second) {
       hipLaunchKernelGGL(first, grid_of(q.items), dim3(kBlock), 0, s, a, q, x, gamma, beta, stats, gy,
                          part);
       hipLaunchKernelGGL(k_gn_between, Space::grid(a, t), dim3(kBlock), 0, s, a, t, p.cg, p.parts,
                          Divider(p.cg), gamma);
       if (gx)
-        hipLaunchKernelGGL(second, grid_of(q.items), dim3(kBlock), 0, s, a, q, x, gamma, beta, stats,
+        hipLaunchKernelGGL(second, grid_of(r.items), dim3(kBlock), 0, s, a, r, x, gamma, beta, stats,
                            gy, z.means_at(ws), gx);
     };
     if (p.strips > 1) go(k_gn_sums<T, V, K, true>, k_gn_grad<T, V, K, true>);
