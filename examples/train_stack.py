@@ -1,6 +1,7 @@
-"""Trains a small 2D FNO stack with layer norms on a made-up operator, on one MI355X.
+"""Trains a small 2D FNO stack with norms on a made-up operator, on one MI355X.
 
-    python examples/train_stack.py [--steps N] [--precision f32|bf16|f16]
+    python examples/train_stack.py [--steps N] [--precision f32|bf16|f16] [--norm layer|group]
+                                   [--dropout P]
 
 The data stands for a PDE's solution operator: inputs are Gaussian random fields a, targets GELU(u)
 (what a stack that ends in a GELU can give) of their screened-Poisson solutions
@@ -36,10 +37,11 @@ def batch(wl, step):
     return a, torch.nn.functional.gelu(u)
 
 
-def train(steps=60, precision="f32", lr=1e-2, max_norm=0.1, verbose=True):
+def train(steps=60, precision="f32", lr=1e-2, max_norm=0.1, verbose=True, norm="layer",
+          dropout=0.0):
     """Losses and gradient norms of the run."""
     wl = Workload("example", 90, 4, 20, (64, 64), (12, 12), 3, PRECISIONS[precision], True,
-                  norm=True)
+                  norm=norm, groups=4, dropout=dropout)
     runner = StackRunner(wl)
     opt = AdamW(runner.parameters(), runner.gradients(), lr, max_norm=max_norm)
     losses, norms = [], []
@@ -60,5 +62,7 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=60)
     ap.add_argument("--precision", choices=sorted(PRECISIONS), default="f32")
+    ap.add_argument("--norm", choices=["layer", "group"], default="layer")
+    ap.add_argument("--dropout", type=float, default=0.0)
     args = ap.parse_args()
-    train(args.steps, args.precision)
+    train(args.steps, args.precision, norm=args.norm, dropout=args.dropout)

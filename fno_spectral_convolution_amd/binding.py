@@ -869,6 +869,8 @@ _KINDS = {_torch.float32: FNO_DTYPE_F32, _torch.bfloat16: FNO_DTYPE_BF16,
 _LIST_KINDS = {**_KINDS, _torch.complex64: FNO_DTYPE_F32}  # as pairs of float32
 
 
+NORM_EPS = 1e-5  # of the norms, where a call names none
+
 # The handle of a device's current stream and the current device, without the Stream object and the
 # set-up check of the public calls (0.1 us each against 1.9 and 0.3, next to 3.3 for a launch); the
 # public calls where torch has no such functions.
@@ -951,7 +953,7 @@ def _like_x(t, x, name):
     return t.stride()
 
 
-def layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, out=None, stats=None, want_stats=True):
+def layer_norm_fwd(x, gamma=None, beta=None, eps=NORM_EPS, out=None, stats=None, want_stats=True):
     """Layer norm of a field [B, C, *grid] over its channels at each point ([rows, C]: over each
     row), times gamma plus beta (float32 [C]; None: 1 and 0).  Returns (y, stats); stats, float32
     [2, B, *grid], holds the means and the reciprocal deviations for layer_norm_bwd (None without
@@ -1122,7 +1124,7 @@ def _space(ws, need, x, index):
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def group_norm_fwd(x, groups, gamma=None, beta=None, act=None, eps=1e-5, channels_last=False,
+def group_norm_fwd(x, groups, gamma=None, beta=None, act=None, eps=NORM_EPS, channels_last=False,
                    drop=None, out=None, stats=None, want_stats=True, ws=None):
     """Group norm of a field [B, C, *grid] (channels_last: [B, *grid, C]) over each of `groups` runs of
     C / groups channels and all points of an entry, times gamma plus beta (float32 [C]; None: 1 and

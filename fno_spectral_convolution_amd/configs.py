@@ -30,8 +30,12 @@ class Workload:
     input_kind: str = "grf"       # grf | normal | grf_coords | grf_layered
     tucker_ranks: Optional[Tuple[int, ...]] = None  # Tucker-factorised spectral weights
                                   # (TFNO): ranks R_in, R_out, R_0..R_{d-1}
-    norm: bool = False            # layer norm over the channels between blocks, each point's own:
+    norm: object = False          # between blocks: True / "layer" (layer norm over the channels, each
+                                  # point's own) or "group" (group norm over points and channels):
                                   # block i > 0 reads GELU(norm(z_{i-1}))
+    groups: int = 1               # of the group norm
+    dropout: float = 0.0          # training: what block i > 0 reads is dropped with this probability
+                                  # (without a norm or with a group norm)
     notes: str = ""
 
     @property

@@ -153,14 +153,14 @@ def tucker_params(w, block: int = 0, cin=None, cout=None, modes=None, ranks=None
 
 
 def norm_params(w, block: int = 0):
-    """Weight [C] ~ N(1, 0.1^2) and bias [C] ~ N(0, 0.1^2) of the layer norm before a block."""
+    """Weight [C] ~ N(1, 0.1^2) and bias [C] ~ N(0, 0.1^2) of the norm before a block."""
     g = rng(w.cfg_id, STREAM_NORM, block)
     return 1.0 + normal(g, w.width, 0.1), normal(g, w.width, 0.1)
 
 
 def block_params(w, n_blocks=None):
     """Per-block parameter dicts for ``n_blocks`` blocks: (w, wb, bias), or (core, factors,
-    wb, bias) for workloads with Tucker-factorised spectral weights; with a layer norm between
+    wb, bias) for workloads with Tucker-factorised spectral weights; with a norm between
     blocks also (gamma, beta) for every block but the first."""
     n = w.blocks if n_blocks is None else n_blocks
     out = []

@@ -5,7 +5,8 @@ the spectral blocks (GELU after each), an optional projection head, and for trai
 workloads the MSE loss against a target and the backward through every block (input,
 spectral-weight, bypass-weight and bias gradients).  Workloads with Tucker ranks hold each
 block's spectral weight as a Tucker core and factors (TFNO) and run the Tucker entry points.
-Workloads with ``norm`` take a layer norm over the channels between blocks, with its gradients.
+Workloads with ``norm`` take a layer norm over the channels or a group norm between blocks, with its
+gradients; training workloads with ``dropout`` drop a part of what every block but the first reads.
 Torch provides device memory and the stream; all arithmetic runs in libfno's kernels.
 
 ``StackRunner.parameters()`` and ``gradients()`` list what a step trains and what it returns, in
@@ -61,10 +62,23 @@ class StackRunner:
     computes the loss and the gradient at its pre-activation in one pass (fno_block_fwd_mse)
     and its backward starts from that gradient (fno_block_bwd_preact), so the output field y
     is never written; step() then returns None.  With fuse_loss=False the step writes y and
-    runs the stand-alone loss kernel between the two passes."""
+    runs the stand-alone loss kernel between the two passes.
 
-    def __init__(self, wl, device="cuda", host_inputs=None, fuse_loss=True, last_axis=None):
+    Dropout masks are functions of dropout_seed, the block and `draws`, a count on the device that
+    every step moves on by the number of blocks: a captured step takes new masks at each replay."""
+
+    def __init__(self, wl, device="cuda", host_inputs=None, fuse_loss=True, last_axis=None,
+                 dropout_seed=0):
         import torch
+        if wl.norm not in (False, True, "layer", "group"):
+            raise ValueError(f"norm must be False, True, 'layer' or 'group', not {wl.norm!r}")
+        if wl.norm == "group" and (wl.groups < 1 or wl.width % wl.groups):
+            raise ValueError(f"{wl.groups} groups do not divide {wl.width} channels")
+        self.group_norm = wl.norm == "group"
+        self.dropout = bool(wl.train and wl.dropout and wl.blocks > 1)
+        if self.dropout and wl.norm and not self.group_norm:
+            raise ValueError("dropout goes with a group norm or none: a layer norm's GELU is the "
+                             "next block's own")
         self.torch = torch
         self.wl = wl
         dev = torch.device(device)
@@ -123,8 +137,9 @@ class StackRunner:
                 # block i > 0 reads normed[i]; its norm's backward reads acts[i] and norm_stats[i]
                 self.normed = [None] + [torch.empty(shape, dtype=torch.float32, device=dev)
                                         for _ in range(1, nb)]
+                sides = (wl.groups,) if self.group_norm else tuple(wl.grid)
                 self.norm_stats = [None] + [
-                    torch.empty((2, wl.batch) + tuple(wl.grid), dtype=torch.float32, device=dev)
+                    torch.empty((2, wl.batch) + sides, dtype=torch.float32, device=dev)
                     for _ in range(1, nb)]
             self.mse_ws = torch.empty(max(L.fno_mse_workspace_bytes(self.acts[-1].numel()), 16),
                                       dtype=torch.uint8, device=dev)
@@ -132,6 +147,16 @@ class StackRunner:
             # forward only: two activation buffers used in turn
             self.acts = [torch.empty(shape, dtype=torch.float32, device=dev) for _ in range(2)]
             self.saves = [None] * nb
+        self.norm_ws = None
+        if self.group_norm and nb > 1:
+            a = self.acts[0]
+            n = L._group_shape(a.dtype, a.shape, wl.groups, "gelu", False, a.stride(), a.stride(),
+                               a.stride(), L.NORM_EPS)
+            self.norm_ws = torch.empty(max(n.fwd_bytes, n.bwd_bytes if wl.train else 0, 16),
+                                       dtype=torch.uint8, device=dev)
+        self.draws = torch.zeros(1, dtype=torch.int64, device=dev) if self.dropout else None
+        self.drops = [L.Dropout(wl.dropout, dropout_seed, i, self.draws) if self.dropout and i else
+                      None for i in range(nb)]
         if self.lp is not None:
             out_shape = (wl.batch, wl.proj_out) + tuple(wl.grid)
             self.out = torch.empty(out_shape, dtype=torch.float32, device=dev)
@@ -140,9 +165,13 @@ class StackRunner:
         blocks to the start of the later one: each inner block then keeps only its
         pre-activation z, and its backward reads z and the incoming gradient once instead of
         twice.  The network, its outputs and its gradients are those of the plain stack.  A
-        stack with norms does so always: they go between a block's z and the next one's GELU."""
+        stack with layer norms does so always: they go between a block's z and the next one's GELU.
+        A group norm takes the GELU into its own pass, and the dropout after it; dropout without a
+        norm goes over the blocks' plain outputs."""
         nb = self.wl.blocks
-        if nb == 1 or not (self.wl.train or self.wl.norm):
+        if self.group_norm:
+            return (False, i == nb - 1)
+        if nb == 1 or not (self.wl.train or self.wl.norm) or self.dropout:
             return (False, True)
         return (i > 0, i == nb - 1)
 
@@ -224,15 +253,38 @@ class StackRunner:
                     out += b[k] if k == "factors" else [b[k]]
         return out
 
-    def _norm(self, i, h):
-        """The layer norm in front of block i > 0."""
+    def _between(self, i, h):
+        """From block i - 1's output to block i's input, i > 0: norm and dropout."""
         p = self.params[i]
+        if self.group_norm:
+            out = self.normed[i] if self.wl.train else h
+            L.group_norm_fwd(h, self.wl.groups, p["gamma"], p["beta"], "gelu", drop=self.drops[i],
+                             out=out, stats=self.norm_stats[i] if self.wl.train else None,
+                             want_stats=self.wl.train, ws=self.norm_ws)
+            return out
+        if not self.wl.norm:
+            if self.dropout:
+                L.dropout_fwd(h, self.drops[i], out=h)
+            return h
         if self.wl.train:
             L.layer_norm_fwd(h, p["gamma"], p["beta"], out=self.normed[i],
                              stats=self.norm_stats[i])
             return self.normed[i]
         L.layer_norm_fwd(h, p["gamma"], p["beta"], out=h, want_stats=False)
         return h
+
+    def _between_bwd(self, i, g):
+        """The gradient at block i's input into that at block i - 1's output, in place."""
+        p, out = self.params[i], {"x": g}
+        if self.wl.norm:
+            out.update(gamma=self.grads[i]["gamma"], beta=self.grads[i]["beta"])
+        if self.group_norm:
+            L.group_norm_bwd(self.acts[i], self.wl.groups, p["gamma"], p["beta"], self.norm_stats[i],
+                             g, "gelu", drop=self.drops[i], out=out, ws=self.norm_ws)
+        elif self.wl.norm:
+            L.layer_norm_bwd(self.acts[i], p["gamma"], self.norm_stats[i], g, out=out)
+        elif self.dropout:
+            L.dropout_bwd(g, self.drops[i], out=g)
 
     def _act(self, i):
         return self.acts[i] if self.wl.train else self.acts[i % 2]
@@ -251,8 +303,8 @@ class StackRunner:
         nb = len(self.params)
         for i, p in enumerate(self.params):
             dst = self._act(i + 1)
-            if wl.norm and i > 0:
-                h = self._norm(i, h)
+            if i > 0:
+                h = self._between(i, h)
             if self.fuse_loss and i == nb - 1:
                 # loss and the gradient at the last pre-activation, into g[0]; y is not stored
                 if self.tucker:
@@ -302,12 +354,12 @@ class StackRunner:
                     self.block_plans[i].block_bwd(x_i, p["w"], p["wb"], p["bias"], self.saves[i],
                                                   self.g[gin],
                                                   out={"x": self.g[gout], **self.grads[i]})
-                if wl.norm and i > 0:  # from the gradient at its output to that at its input
-                    L.layer_norm_bwd(self.acts[i], p["gamma"], self.norm_stats[i], self.g[gout],
-                                     out={"x": self.g[gout], "gamma": self.grads[i]["gamma"],
-                                          "beta": self.grads[i]["beta"]})
+                if i > 0:
+                    self._between_bwd(i, self.g[gout])
                 gin = gout
             self.grad_x = self.g[gin]
+            if self.dropout:
+                self.draws += nb
         return h
 
 
