@@ -353,13 +353,12 @@ struct PlaneSums {
   const Strip& p;
   const Place& q;
   float2 (&s)[K][BLOCK / 64];
-  float* row;  // of [2][channels]
-  int channels;
+  float *to_g, *to_b;        // [channels], nullable
   float sg = 0.f, sb = 0.f;  // of the present plane
 
   __device__ __forceinline__ void put(int c, float g, float b) const {
-    row[q.channel + c] = g;
-    row[channels + q.channel + c] = b;
+    if (to_g) to_g[q.channel + c] = g;
+    if (to_b) to_b[q.channel + c] = b;
   }
   // the sums of pass `i` over the planes are complete in their threads
   __device__ __forceinline__ void flush(int i) {
@@ -392,13 +391,15 @@ struct PlaneSums {
   }
 };
 
-// As k_gn_whole; part: rows [batch] of [2][channels], sums of g h and g.
+// As k_gn_whole; to_g and to_b (nullable): sums of g h and g, an entry's `pitch` after the last one's.
 template <typename T, int VEC, int K, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void k_gn_whole_bwd(GroupArgs a, Strip p, int64_t total,
                                                         const T* x, const float* gamma,
                                                         const float* beta, const float* stats,
-                                                        const T* gy, T* gx, float* part) {
+                                                        const T* gy, T* gx, float* to_g,
+                                                        float* to_b, int64_t pitch) {
   __shared__ float2 s_red[BLOCK / 64], s_sum[K][BLOCK / 64];
+  const bool weights = to_g || to_b;
   const Dropper drop(a.drop);
   const int64_t sides = a.batch * a.groups;
   const float inv_m = 1.0f / ((float)p.cg * (float)a.npts);
@@ -410,8 +411,8 @@ __global__ __launch_bounds__(BLOCK) void k_gn_whole_bwd(GroupArgs a, Strip p, in
     it.load(gy + q.b * a.y_stride + q.channel * a.npts, rg);
     const float mean = stats[q.bg], rstd = stats[sides + q.bg];
     const uint64_t index = (uint64_t)((q.b * a.channels + q.channel) * a.npts);
-    PlaneSums<K, BLOCK> sums = {p, q, s_sum, part ? part + q.b * 2 * a.channels : nullptr,
-                                a.channels};
+    PlaneSums<K, BLOCK> sums = {p, q, s_sum, to_g ? to_g + q.b * pitch : nullptr,
+                                to_b ? to_b + q.b * pitch : nullptr};
     float h[K][VEC], g[K][VEC], weight[K], s1 = 0.f, s2 = 0.f;
     int pass = 0, j = 0;
 #pragma unroll
@@ -434,12 +435,12 @@ __global__ __launch_bounds__(BLOCK) void k_gn_whole_bwd(GroupArgs a, Strip p, in
       sums.sg += pg;
       sums.sb += pb;
       if (++j == p.kv) {
-        if (part) sums.flush(pass);
+        if (weights) sums.flush(pass);
         j = 0;
         ++pass;
       }
     }
-    if (part) sums.finish();
+    if (weights) sums.finish();
     if (!gx) continue;
     if (BLOCK > 64) __syncthreads();
     const float2 sum = block_sum<BLOCK / 64>(s1, s2, s_red);
@@ -466,8 +467,8 @@ __global__ __launch_bounds__(kBlock) void k_gn_sums(GroupArgs a, Pass ps, const 
     const T* px = x + q.b * a.x_stride + q.channel * a.npts;
     const T* pg = gy + q.b * a.y_stride + q.channel * a.npts;
     const uint64_t index = (uint64_t)((q.b * a.channels + q.channel) * a.npts);
-    PlaneSums<K, kBlock> sums = {p, q, s_sum, part + (q.b * p.parts + q.s) * 2 * a.channels,
-                                 a.channels};
+    float* row = part + (q.b * p.parts + q.s) * 2 * a.channels;
+    PlaneSums<K, kBlock> sums = {p, q, s_sum, row, row + a.channels};
     if (LONG) {
       const float weight = gamma ? gamma[q.channel] : 1.f, bias = beta ? beta[q.channel] : 0.f;
       long_strips<VEC, K>(
@@ -640,7 +641,8 @@ __device__ __forceinline__ float slot_sum(float v, float (&s)[2][BLOCK / 64], in
 // `stride` slots in the launch: a multiple of the groups, `rows` times as many
 template <typename T, int VEC, int TPR, int NV, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void k_gn_rows(GroupArgs a, int cg, Divider by_groups,
-                                                   int64_t stride, int64_t rows, const T* x,
+                                                   int64_t stride, int64_t rows, bool stream,
+                                                   const T* x,
                                                    const float* gamma, const float* beta, T* y,
                                                    float* stats) {
   constexpr int kSlots = BLOCK / TPR;
@@ -708,7 +710,7 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows(GroupArgs a, int cg, Divider 
       activate(f[k], a.act);
       if (a.drop.threshold)
         drop.apply<VEC>(f[k], drop.mask<VEC>((uint64_t)(b * a.channels + start[k])));
-      store_pack<T, VEC>(o + start[k], f[k]);
+      store_pack<T, VEC>(o + start[k], f[k], stream);
     }
     if (stats && t == 0) {
       const int64_t i = b * a.groups + group;
@@ -719,14 +721,15 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows(GroupArgs a, int cg, Divider 
 }
 
 // A work-group takes `wide` groups (chunk blockIdx.x % chunks of them) of `deep` rows at a time.
-// Their weights' sums stay in registers until its last row and go out as row blockIdx.x / chunks of
-// part, [2][channels] each.
+// Their weights' sums stay in registers until its last row and go out to to_g and to_b (nullable),
+// those of work-group blockIdx.x / chunks `pitch` after the last one's.
 template <typename T, int VEC, int TPR, int NV, int BLOCK, bool WEIGHTS>
 __global__ __launch_bounds__(BLOCK) void k_gn_rows_bwd(GroupArgs a, int cg, Divider by_wide,
-                                                       int wide, int deep, int chunks,
+                                                       int wide, int deep, int chunks, bool stream,
                                                        const T* x, const float* gamma,
                                                        const float* beta, const float* stats,
-                                                       const T* gy, T* gx, float* part) {
+                                                       const T* gy, T* gx, float* to_g,
+                                                       float* to_b, int64_t pitch) {
   constexpr int kCols = TPR * VEC;
   __shared__ float s_sum[2][BLOCK / 64];
   __shared__ float s_cols[WEIGHTS ? BLOCK * VEC : 1];
@@ -754,18 +757,33 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows_bwd(GroupArgs a, int cg, Divi
   const bool partial = any_partial(lo);
   int flip = 0;
   const int64_t step = (int64_t)(gridDim.x / chunks) * deep;
-  for (int64_t base = (int64_t)(blockIdx.x / chunks) * deep; base < a.batch; base += step) {
+  // the next row's loads go ahead of this one's sums
+  Raw<T, VEC> next_x[NV], next_g[NV];
+  float next_mean, next_rstd;
+  const auto fetch = [&](int64_t row) {
+    const int64_t b = mine && row < a.batch ? row : a.batch - 1;
+    next_mean = stats[b * a.groups + g];
+    next_rstd = stats[total + b * a.groups + g];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      next_x[k] = load_raw<T, VEC, true>(x + b * a.x_stride + start[k]);
+      next_g[k] = load_raw<T, VEC, true>(gy + b * a.y_stride + start[k]);
+    }
+  };
+  int64_t base = (int64_t)(blockIdx.x / chunks) * deep;
+  if (base < a.batch) fetch(base + down);
+  for (; base < a.batch; base += step) {
     const bool live = mine && base + down < a.batch;
     const int64_t b = live ? base + down : a.batch - 1;
-    const float mean = stats[b * a.groups + g], rstd = stats[total + b * a.groups + g];
-    const T *px = x + b * a.x_stride, *pg = gy + b * a.y_stride;
+    const float mean = next_mean, rstd = next_rstd;
     float h[NV][VEC], v[NV][VEC], s1 = 0.f, s2 = 0.f;
     Raw<T, VEC> rx[NV], rg[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      rx[k] = load_raw<T, VEC>(px + start[k]);
-      rg[k] = load_raw<T, VEC>(pg + start[k]);
+      rx[k] = next_x[k];
+      rg[k] = next_g[k];
     }
+    if (base + step < a.batch) fetch(base + step + down);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float mu[VEC], rs[VEC];
@@ -801,16 +819,18 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows_bwd(GroupArgs a, int cg, Divi
       if (lo[k] >= VEC) continue;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[k][e] = rstd * (v[k][e] - fmaf(h[k][e], s2, s1));
-      store_pack<T, VEC>(o + start[k], v[k]);
+      store_pack<T, VEC>(o + start[k], v[k], stream);
     }
   }
   if (!WEIGHTS) return;
   // the slots' sums of each column, down their rows
-  part += (int64_t)(blockIdx.x / chunks) * 2 * a.channels + (int64_t)g0 * cg;
+  const int64_t first = (int64_t)(blockIdx.x / chunks) * pitch + (int64_t)g0 * cg;
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
+      float* to = m == 0 ? to_g : to_b;
+      if (!to) continue;
       __syncthreads();
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
@@ -823,7 +843,7 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows_bwd(GroupArgs a, int cg, Divi
         if (r % VEC < low) continue;
         float sum = 0.f;
         for (int d = 0; d < deep; ++d) sum += s_cols[d * wide * kCols + c];
-        part[(int64_t)m * a.channels + i * cg + st + r % VEC] = sum;
+        to[first + i * cg + st + r % VEC] = sum;
       }
     }
 }
@@ -862,8 +882,9 @@ auto pick_rows(int cg, F&& f) {
 }
 
 // The backward's rows: groups and rows that a work-group takes at a time (as many of its slots as
-// can be used, rather more groups, which are neighbours), and its work-groups, which write one
-// partial row each.
+// can be used, rather more groups, which are neighbours), and its work-groups down the batch, which
+// write one partial row each.  One goes down up to four times: it then has the gradients themselves,
+// which spares the workspace and a launch (3.3 us for the host).
 constexpr int kRowsBlock = 1024;
 struct RowsShape {
   int wide, deep, chunks, down;
@@ -882,8 +903,8 @@ RowsShape rows_shape(const GroupArgs& a, int tpr) {
       p.chunks = chunks;
     }
   }
-  p.down = (int)std::min<int64_t>(ceil_div(a.batch, p.deep),
-                                  std::max<int64_t>(1, 256 / p.chunks));
+  const int64_t times = ceil_div(a.batch, p.deep);
+  p.down = times <= 4 ? 1 : (int)std::min<int64_t>(times, std::max<int64_t>(1, 256 / p.chunks));
   return p;
 }
 
@@ -931,7 +952,7 @@ hipError_t rows_fwd(const GroupArgs& a, const T* x, const float* gamma, const fl
       const int64_t groups = unit * std::max<int64_t>(1, std::min(ceil_div(need, unit), most / unit));
       hipLaunchKernelGGL((k_gn_rows<T, vec.value, TPR, nv.value, kB>), dim3(groups), dim3(kB), 0, s,
                          a, a.channels / a.groups, Divider(a.groups), groups * kSlots,
-                         groups * kSlots / a.groups, x, gamma, beta, y, stats);
+                         groups * kSlots / a.groups, stream_out<T>(a), x, gamma, beta, y, stats);
     });
   });
   return hipGetLastError();
@@ -961,6 +982,17 @@ hipError_t first_fwd(const GroupArgs& a, const T* x, const float* gamma, const f
   return hipGetLastError();
 }
 
+// Where the sums for the weights' gradients go: into `rows` partial rows [2][channels], or where there
+// is one row into the gradients themselves.
+struct Partial {
+  float *g = nullptr, *b = nullptr;
+  Partial(const GroupArgs& a, int64_t rows, float* part, float* ggamma, float* gbeta) {
+    if (!ggamma && !gbeta) return;
+    g = rows == 1 ? ggamma : part;
+    b = rows == 1 ? gbeta : part + a.channels;
+  }
+};
+
 template <typename T>
 size_t fwd_bytes(const GroupArgs& a) {
   if (form_of(a) == kRows) return 0;
@@ -979,13 +1011,14 @@ size_t bwd_bytes(const GroupArgs& a) {
   if (form_of(a) == kRows)
     return by_vector<kVec<T>>(a.channels / a.groups, [&](auto vec) {
       return pick_rows<vec.value>(a.channels / a.groups, [&](auto tpr, auto) {
-        return up((int64_t)sizeof(float) * 2 * rows_shape(a, tpr.value).down * a.channels);
+        const int down = rows_shape(a, tpr.value).down;
+        return down == 1 ? (size_t)0 : up((int64_t)sizeof(float) * 2 * down * a.channels);
       });
     });
   return by_vector<kVec<T>>(a.npts, [&](auto vec) {
     constexpr int V = vec.value;
     if (pick_whole<V, kWholeBwd<V>>(a, [](auto, const Strip&) {}))
-      return up((int64_t)sizeof(float) * 2 * a.batch * a.channels);
+      return a.batch == 1 ? (size_t)0 : up((int64_t)sizeof(float) * 2 * a.batch * a.channels);
     return Space(a, a.batch * strip_of<V, kAhead, kBlock>(a).parts, 0).bytes();
   });
 }
@@ -1001,16 +1034,19 @@ hipError_t rows_bwd(const GroupArgs& a, const T* x, const float* gamma, const fl
       constexpr int V = vec.value, TPR = tpr.value, NV = nv.value;
       const RowsShape p = rows_shape(a, TPR);
       parts = p.down;
+      const Partial to(a, parts, part, ggamma, gbeta);
       const auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3(p.chunks * p.down), dim3(kRowsBlock), 0, s, a,
-                           a.channels / a.groups, Divider(p.wide), p.wide, p.deep, p.chunks, x, gamma, beta, stats, gy, gx, part);
+                           a.channels / a.groups, Divider(p.wide), p.wide, p.deep, p.chunks,
+                           stream_out<T>(a), x, gamma, beta, stats, gy, gx, to.g, to.b,
+                           2 * (int64_t)a.channels);
       };
       if (weights) go(k_gn_rows_bwd<T, V, TPR, NV, kRowsBlock, true>);
       else go(k_gn_rows_bwd<T, V, TPR, NV, kRowsBlock, false>);
     });
   });
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !weights) return e;
+  if (e != hipSuccess || !weights || parts == 1) return e;
   return launch_weight_sums(a.channels, parts, part, ggamma, gbeta, s);
 }
 
@@ -1023,10 +1059,11 @@ hipError_t first_bwd(const GroupArgs& a, const T* x, const float* gamma, const f
   bool whole = false;
   by_vector<kVec<T>>(a.npts, [&](auto vec) {
     constexpr int V = vec.value, W = kWholeBwd<V>, K = kAhead;
+    const Partial to(a, a.batch, part, ggamma, gbeta);
     whole = pick_whole<V, W>(a, [&](auto block, const Strip& p) {
       hipLaunchKernelGGL((k_gn_whole_bwd<T, V, W, block.value>), grid_of(a.batch * a.groups),
                          dim3(block.value), 0, s, a, p, a.batch * a.groups, x, gamma, beta, stats, gy,
-                         gx, weights ? part : nullptr);
+                         gx, to.g, to.b, 2 * (int64_t)a.channels);
     });
     if (whole) return;
     const Strip p = strip_of<V, K, kBlock>(a);
@@ -1046,7 +1083,7 @@ hipError_t first_bwd(const GroupArgs& a, const T* x, const float* gamma, const f
     else go(k_gn_sums<T, V, K, false>, k_gn_grad<T, V, K, false>);
   });
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !weights || !whole) return e;
+  if (e != hipSuccess || !weights || !whole || a.batch == 1) return e;
   return launch_weight_sums(a.channels, (int)a.batch, part, ggamma, gbeta, s);
 }
 
