@@ -178,35 +178,24 @@ __device__ __forceinline__ void fill(float (&f)[N], float v) {
 }
 
 // ---- between the backward's passes -----------------------------------------------------------------
-// means [batch * groups]: of gamma g and gamma g h over a group, by the first work-groups of the
-// launch: sums(b, g) are a thread's shares of their sums.  The others add up the partial rows for the
-// weights' gradients, kSumCols columns each.
+// From the first pass's partial rows [2][channels]: the weights' gradients, and for each group the
+// means of gamma g and gamma g h.  In a launch of their own, the first work-groups for the means; where
+// there is little to add up, in the second pass's launch, whose work-groups make the means that they
+// need and are followed by those for the weights.
 constexpr int kSumCols = 16;
 struct Between {
-  int64_t rows;    // partial rows [2][channels]
-  int64_t groups;  // work-groups of the means (0: none wanted)
+  int64_t rows;           // partial rows
+  int64_t groups;         // work-groups before those of the weights
   const float* part;
   float2* means;
   float *ggamma, *gbeta;  // nullable
   Divider by_groups;
+  bool own;               // no launch of their own
 };
-template <typename F>
-__device__ __forceinline__ void between(const GroupArgs& a, const Between& z, F&& sums) {
+// The weights' gradients, kSumCols columns at a time, by the work-groups from z.groups on.
+__device__ __forceinline__ void weight_sums(const GroupArgs& a, const Between& z) {
   constexpr int kSlices = kBlock / kSumCols;
-  __shared__ float2 s_red[kWaves];
   __shared__ float s_col[kSlices][kSumCols];
-  if (blockIdx.x < z.groups) {
-    const int64_t sides = a.batch * a.groups;
-    const float inv = 1.0f / ((float)(a.channels / a.groups) * (float)a.npts);
-    for (int64_t i = blockIdx.x; i < sides; i += z.groups) {
-      const int64_t b = z.by_groups.of(i);
-      const float2 own = sums(b, (int)(i - b * a.groups));
-      __syncthreads();
-      const float2 v = block_sum<kWaves>(own.x, own.y, s_red);
-      if (threadIdx.x == 0) z.means[i] = make_float2(v.x * inv, v.y * inv);
-    }
-    return;
-  }
   const int col = threadIdx.x % kSumCols, slice = threadIdx.x / kSumCols;
   const int64_t width = 2 * (int64_t)a.channels;
   for (int64_t base = (blockIdx.x - z.groups) * kSumCols; base < width;
@@ -224,6 +213,21 @@ __device__ __forceinline__ void between(const GroupArgs& a, const Between& z, F&
       if (out) out[i < a.channels ? i : i - a.channels] = s;
     }
     __syncthreads();
+  }
+}
+// A launch of their own; sums(b, g): a thread's shares of group g's sums.
+template <typename F>
+__device__ __forceinline__ void between(const GroupArgs& a, const Between& z, F&& sums) {
+  __shared__ float2 s_red[kWaves];
+  if (blockIdx.x >= z.groups) return weight_sums(a, z);
+  const int64_t sides = a.batch * a.groups;
+  const float inv = 1.0f / ((float)(a.channels / a.groups) * (float)a.npts);
+  for (int64_t i = blockIdx.x; i < sides; i += z.groups) {
+    const int64_t b = z.by_groups.of(i);
+    const float2 own = sums(b, (int)(i - b * a.groups));
+    __syncthreads();
+    const float2 v = block_sum<kWaves>(own.x, own.y, s_red);
+    if (threadIdx.x == 0) z.means[i] = make_float2(v.x * inv, v.y * inv);
   }
 }
 
@@ -256,6 +260,11 @@ bool stream_out(const GroupArgs& a) {
   return a.batch * a.channels * a.npts > ((int64_t)128 << 20) / (int64_t)sizeof(T);
 }
 
+// Whether a backward's second pass should do for itself what is between the passes: small data, where a
+// launch counts (4 x 20 x 64^2 float32 18 us against 22; 4 x 96^2 x 320 half, three times as large as
+// the limit, 49 against 47).
+inline bool small(const GroupArgs& a) { return a.batch * a.channels * a.npts <= 1 << 22; }
+
 // A backward's workspace: the partial rows, the segments' sums (channels last), the means.
 struct Space {
   int64_t rows;
@@ -271,11 +280,15 @@ struct Space {
   float2* means_at(void* ws) const {
     return reinterpret_cast<float2*>(static_cast<char*>(ws) + part + seg);
   }
-  // what the launch between the passes has to do, and its grid
-  Between between(const GroupArgs& a, void* ws, bool means, float* ggamma, float* gbeta) const {
-    return {rows, means ? std::min<int64_t>(a.batch * a.groups, kMaxGrid) : 0,
-            static_cast<const float*>(ws), means_at(ws), ggamma, gbeta, Divider(a.groups)};
+  // what is between the passes; items: of the second pass, in whose launch it is done where `own`
+  Between between(const GroupArgs& a, void* ws, bool means, float* ggamma, float* gbeta, bool own,
+                  int64_t items) const {
+    own = own && means;
+    const int64_t groups = own ? items : means ? a.batch * a.groups : 0;
+    return {rows, std::min<int64_t>(groups, kMaxGrid), static_cast<const float*>(ws), means_at(ws),
+            ggamma, gbeta, Divider(a.groups), own};
   }
+  // the grid with the weights' work-groups
   static dim3 grid(const GroupArgs& a, const Between& z) {
     const int64_t cols = z.ggamma || z.gbeta ? ceil_div(2 * (int64_t)a.channels, kSumCols) : 0;
     return dim3((unsigned)(z.groups + std::min<int64_t>(cols, kMaxGrid)));

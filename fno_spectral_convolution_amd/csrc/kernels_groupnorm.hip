@@ -453,6 +453,29 @@ __global__ __launch_bounds__(BLOCK) void k_gn_whole_bwd(GroupArgs a, Strip p, in
   }
 }
 
+// A thread's shares of a group's sums of gamma g and gamma g h, from the partial rows.
+struct Sums {
+  int cg, parts;  // channels of a group, partial sums of a plane
+  Divider by_cg;
+  __device__ __forceinline__ float2 of(const GroupArgs& a, const float* part, const float* gamma,
+                                       int64_t b, int64_t g) const {
+    const int64_t first = g * cg;
+    const float* rows = part + b * parts * 2 * a.channels + first;
+    float2 v = make_float2(0.f, 0.f);
+    for (int64_t k = threadIdx.x; k < (int64_t)cg * parts; k += kBlock) {
+      const int64_t j = by_cg.of(k), c = k - j * cg;
+      const float weight = gamma ? gamma[first + c] : 1.f;
+      v.x += weight * rows[(j * 2 + 1) * a.channels + c];
+      v.y += weight * rows[j * 2 * a.channels + c];
+    }
+    return v;
+  }
+};
+__global__ __launch_bounds__(kBlock) void k_gn_between(GroupArgs a, Between z, Sums sums,
+                                                       const float* gamma) {
+  between(a, z, [&](int64_t b, int g) { return sums.of(a, z.part, gamma, b, g); });
+}
+
 // part: rows [batch * parts] of [2][channels], sums of g h and g
 template <typename T, int VEC, int K, bool LONG>
 __global__ __launch_bounds__(kBlock) void k_gn_sums(GroupArgs a, Pass ps, const T* x,
@@ -533,14 +556,27 @@ __global__ __launch_bounds__(kBlock) void k_gn_sums(GroupArgs a, Pass ps, const 
 template <typename T, int VEC, int K, bool LONG>
 __global__ __launch_bounds__(kBlock) void k_gn_grad(GroupArgs a, Pass ps, const T* x,
                                                     const float* gamma, const float* beta,
-                                                    const float* stats, const T* gy,
-                                                    const float2* means, T* gx) {
+                                                    const float* stats, const T* gy, Between z,
+                                                    Sums sums, T* gx) {
+  __shared__ float2 s_red[kWaves];
   const Strip& p = ps.p;
   const Dropper drop(a.drop);
-  for (int64_t w = blockIdx.x; w < ps.items; w += gridDim.x) {
+  if (z.own && blockIdx.x >= z.groups) return weight_sums(a, z);
+  const int64_t stride = z.own ? z.groups : gridDim.x;
+  for (int64_t w = blockIdx.x; w < ps.items; w += stride) {
     const Place q = place_of(w, p, a.groups);
     const float mean = stats[q.bg], rstd = stats[a.batch * a.groups + q.bg];
-    const float m1 = means[q.bg].x, m2 = means[q.bg].y;
+    float2 m;
+    if (z.own) {
+      const float2 v = sums.of(a, z.part, gamma, q.b, q.bg - q.b * a.groups);
+      __syncthreads();
+      m = block_sum<kWaves>(v.x, v.y, s_red);
+      const float inv = 1.0f / ((float)p.cg * (float)a.npts);
+      m = make_float2(m.x * inv, m.y * inv);
+    } else {
+      m = z.means[q.bg];
+    }
+    const float m1 = m.x, m2 = m.y;
     const T* px = x + q.b * a.x_stride + q.channel * a.npts;
     const T* pg = gy + q.b * a.y_stride + q.channel * a.npts;
     T* to = gx + q.b * a.gx_stride + q.channel * a.npts;
@@ -584,22 +620,6 @@ __global__ __launch_bounds__(kBlock) void k_gn_grad(GroupArgs a, Pass ps, const 
       }
     }
   }
-}
-
-__global__ __launch_bounds__(kBlock) void k_gn_between(GroupArgs a, Between z, int cg, int parts,
-                                                       Divider by_cg, const float* gamma) {
-  between(a, z, [&](int64_t b, int g) {
-    const int64_t first = (int64_t)g * cg;
-    const float* rows = z.part + b * parts * 2 * a.channels + first;
-    float2 v = make_float2(0.f, 0.f);
-    for (int64_t k = threadIdx.x; k < (int64_t)cg * parts; k += kBlock) {
-      const int64_t j = by_cg.of(k), c = k - j * cg;
-      const float weight = gamma ? gamma[first + c] : 1.f;
-      v.x += weight * rows[(j * 2 + 1) * a.channels + c];
-      v.y += weight * rows[j * 2 * a.channels + c];
-    }
-    return v;
-  });
 }
 
 // ---- rows: one point ------------------------------------------------------------------------------
@@ -1068,16 +1088,18 @@ hipError_t first_bwd(const GroupArgs& a, const T* x, const float* gamma, const f
     if (whole) return;
     const Strip p = strip_of<V, K, kBlock>(a);
     const Space z(a, a.batch * p.parts, 0);
-    const Between t = z.between(a, ws, gx != nullptr, ggamma, gbeta);
     const Pass q = pass_of<T>(a, p), r = second_of<T>(a, p, 1);
+    const bool own = small(a) && p.cg * p.parts <= 4 * kBlock;
+    const Between t = z.between(a, ws, gx != nullptr, ggamma, gbeta, own, r.items);
+    const Sums sums = {p.cg, p.parts, Divider(p.cg)};
     const auto go = [&](auto first, auto second) {
       hipLaunchKernelGGL(first, grid_of(q.items), dim3(kBlock), 0, s, a, q, x, gamma, beta, stats, gy,
                          part);
-      hipLaunchKernelGGL(k_gn_between, Space::grid(a, t), dim3(kBlock), 0, s, a, t, p.cg, p.parts,
-                         Divider(p.cg), gamma);
+      if (!t.own)
+        hipLaunchKernelGGL(k_gn_between, Space::grid(a, t), dim3(kBlock), 0, s, a, t, sums, gamma);
       if (gx)
-        hipLaunchKernelGGL(second, grid_of(r.items), dim3(kBlock), 0, s, a, r, x, gamma, beta, stats,
-                           gy, z.means_at(ws), gx);
+        hipLaunchKernelGGL(second, t.own ? Space::grid(a, t) : grid_of(r.items), dim3(kBlock), 0, s, a,
+                           r, x, gamma, beta, stats, gy, t, sums, gx);
     };
     if (p.strips > 1) go(k_gn_sums<T, V, K, true>, k_gn_grad<T, V, K, true>);
     else go(k_gn_sums<T, V, K, false>, k_gn_grad<T, V, K, false>);

@@ -51,7 +51,7 @@ Tiles tiles_of(const GroupArgs& a) {
   p.by_tiles = Divider(p.tiles);
   return p;
 }
-// Whether the forward's second pass joins the parts for itself, which saves a launch: few enough for
+// Whether the second pass joins the parts for itself, which saves a launch: few enough for
 // a work-group's threads.
 bool joins(const Tiles& p) {
   const int64_t in_block = std::min<int64_t>(p.cols, (p.cols + p.cg - 1) / p.cg + 1);
@@ -398,6 +398,19 @@ __global__ __launch_bounds__(kBlock) void k_gn_apply_last(GroupArgs a, Tiles p, 
   }
 }
 
+// A lane's share of the sums of gamma g and gamma g h of group g of entry b.
+__device__ __forceinline__ float2 seg_sums(const Tiles& p, const float2* seg, int64_t b, int g,
+                                           int lane, int lanes) {
+  const Span sp = span_of(p, g);
+  const float2* from = parts_of(p, seg, b, g, sp);
+  float2 v = make_float2(0.f, 0.f);
+  for (int k = lane; k < sp.blocks * p.tiles; k += lanes) {
+    v.x += from[k].x;
+    v.y += from[k].y;
+  }
+  return v;
+}
+
 // part: rows [batch * tiles] of [2][channels], sums of g h and g; seg [batch][segments][tiles]: sums
 // of gamma g and gamma g h
 template <typename T, int VEC, int K, bool EVEN>
@@ -496,17 +509,28 @@ __global__ __launch_bounds__(kBlock) void k_gn_grad_last(GroupArgs a, Tiles p, i
                                                          bool stream, const T* x,
                                                          const float* gamma, const float* beta,
                                                          const float* stats, const T* gy,
-                                                         const float2* means, T* gx) {
+                                                         Between z, const float2* seg, T* gx) {
   __shared__ float2 s_st[32 * VEC], s_m[32 * VEC];
   const Dropper drop(a.drop);
-  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+  if (z.own && blockIdx.x >= z.groups) return weight_sums(a, z);
+  const int64_t stride = z.own ? z.groups : gridDim.x;
+  for (int64_t w = blockIdx.x; w < total; w += stride) {
     const Block q = block_of(w, a, p);
     int r, c, lo;
     vector_of<VEC>(q, p, a.channels, r, c, lo);
     __syncthreads();
     given_stats(a, q, stats, s_st);
-    for (int s = threadIdx.x; s < q.segs; s += kBlock)
-      s_m[s] = means[q.b * a.groups + q.g0 + s];
+    if (z.own) {
+      const float inv = 1.0f / ((float)p.cg * (float)a.npts);
+      each_segment(p, q, [&](int s, int, int, int lane, int lanes) {
+        float2 v = seg_sums(p, seg, q.b, q.g0 + s, lane, lanes);
+        v = make_float2(lanes_sum(v.x, lanes) * inv, lanes_sum(v.y, lanes) * inv);
+        if (lane == 0) s_m[s] = v;
+      });
+    } else {
+      for (int s = threadIdx.x; s < q.segs; s += kBlock)
+        s_m[s] = z.means[q.b * a.groups + q.g0 + s];
+    }
     __syncthreads();
     if (lo >= VEC) continue;
     float mu[VEC], rs[VEC], ga[VEC], be[VEC], m1[VEC], m2[VEC];
@@ -544,16 +568,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_grad_last(GroupArgs a, Tiles p, i
 
 __global__ __launch_bounds__(kBlock) void k_gn_between_last(GroupArgs a, Tiles p, Between z,
                                                             const float2* seg) {
-  between(a, z, [&](int64_t b, int g) {
-    const Span sp = span_of(p, g);
-    const float2* from = parts_of(p, seg, b, g, sp);
-    float2 v = make_float2(0.f, 0.f);
-    for (int k = threadIdx.x; k < sp.blocks * p.tiles; k += kBlock) {
-      v.x += from[k].x;
-      v.y += from[k].y;
-    }
-    return v;
-  });
+  between(a, z, [&](int64_t b, int g) { return seg_sums(p, seg, b, g, threadIdx.x, kBlock); });
 }
 
 // ---- launches ------------------------------------------------------------------------------------
@@ -607,15 +622,18 @@ hipError_t bwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
     const Tiles p = tiles_of<V>(a);
     const int64_t total = a.batch * p.tiles * p.blocks;
     const Space z(a, a.batch * p.tiles, a.batch * p.segments * p.tiles);
-    const Between q = z.between(a, ws, gx != nullptr, ggamma, gbeta);
+    const Between q = z.between(a, ws, gx != nullptr, ggamma, gbeta,
+                                joins(p) && small(a), total);
     const auto go = [&](auto first, auto second) {
       hipLaunchKernelGGL(first, grid_of(total), dim3(kBlock), 0, s, a, p, total, x, gamma, beta,
                          stats, gy, static_cast<float*>(ws), z.segments_at(ws));
-      hipLaunchKernelGGL(k_gn_between_last, Space::grid(a, q), dim3(kBlock), 0, s, a, p, q,
-                         z.segments_at(ws));
+      if (!q.own)
+        hipLaunchKernelGGL(k_gn_between_last, Space::grid(a, q), dim3(kBlock), 0, s, a, p, q,
+                           z.segments_at(ws));
       if (gx)
-        hipLaunchKernelGGL(second, grid_of(total), dim3(kBlock), 0, s, a, p, total, stream_out<T>(a),
-                           x, gamma, beta, stats, gy, z.means_at(ws), gx);
+        hipLaunchKernelGGL(second, q.own ? Space::grid(a, q) : grid_of(total), dim3(kBlock), 0, s, a, p,
+                           total, stream_out<T>(a), x, gamma, beta, stats, gy, q, z.segments_at(ws),
+                           gx);
     };
     if (V > 1 && even(a)) go(k_gn_sums_last<T, V, K, V != 1>, k_gn_grad_last<T, V, K, V != 1>);
     else go(k_gn_sums_last<T, V, K, false>, k_gn_grad_last<T, V, K, false>);

@@ -1891,8 +1891,8 @@ fno_status group_args(const fno_group_norm_desc* d, const fno_dropout* drop, fno
     return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: eps must be finite and >= 0");
   if (d->channels >= (int64_t)1 << 30 || d->batch >= (int64_t)1 << 31)
     return fail(FNO_ERR_UNSUPPORTED, "group norm: channels >= 2^30 or batch >= 2^31");
-  // as in the layer norm: every byte offset and the bytes of all elements fit 62 bits
-  const int64_t lim = (int64_t)1 << 60;
+  // every byte offset, the bytes of all elements and those of the workspaces fit 62 bits
+  const int64_t lim = (int64_t)1 << 56;
   int64_t per, all, span;
   const int64_t st = std::max(std::max(d->x_stride, d->y_stride), d->grad_x_stride);
   if (__builtin_mul_overflow(d->channels, d->npts, &per) || per > lim ||

@@ -95,6 +95,7 @@ def test_mask_positions():
     (dict(x_stride=-1), BAD), (dict(eps=-1e-9), BAD), (dict(eps=math.nan), BAD),
     (dict(eps=math.inf), BAD), (dict(npts=1 << 62), BAD), (dict(batch=1 << 30, x_stride=1 << 40), BAD),
     (dict(batch=1 << 30, channels=1 << 20, npts=1 << 20, x_stride=0, y_stride=0), BAD),
+    (dict(batch=1 << 29, channels=1 << 28, npts=1, x_stride=0, y_stride=0, grad_x_stride=0), BAD),
     (dict(channels=1 << 30), L.FNO_ERR_UNSUPPORTED), (dict(batch=1 << 31), L.FNO_ERR_UNSUPPORTED),
 ])
 def test_group_norm_descriptor_refused(kw, status):
@@ -157,6 +158,24 @@ def test_dropout_pointers_refused():
     assert L._lib.fno_dropout_fwd(_ddesc(x_stride=30), drop, P, Q, P, None) == BAD
     assert L._lib.fno_dropout_fwd(_ddesc(residual_stride=30), drop, Q, P, P, None) == BAD
     assert L._lib.fno_dropout_bwd(_ddesc(x_stride=30), drop, P, P, None) == BAD
+
+
+@pytest.mark.parametrize("last", [0, 1])
+@pytest.mark.parametrize("kw", [
+    dict(batch=1 << 26, channels=(1 << 30) - 1, npts=1), dict(batch=1, channels=(1 << 30) - 2, npts=1),
+    dict(batch=(1 << 31) - 1, channels=16, npts=1 << 21), dict(batch=1, channels=1, npts=1 << 56),
+    dict(batch=3, channels=(1 << 30) - 4, npts=1 << 24), dict(batch=1, channels=1 << 26, npts=1 << 30),
+    dict(batch=(1 << 31) - 1, channels=1, npts=2),
+], ids=str)
+@pytest.mark.parametrize("groups", [1, "all"])
+def test_workspaces_of_the_largest_descriptors(kw, last, groups):
+    """Sizes at the limits: the workspaces' layout stays within 64 bits (the sanitizers look on)."""
+    for dtype in (0, 1):
+        d = _desc(dtype=dtype, channels_last=last, groups=kw["channels"] if groups == "all" else 1,
+                  x_stride=0, y_stride=0, grad_x_stride=0, **kw)
+        f, b = ctypes.c_size_t(), ctypes.c_size_t()
+        assert L._lib.fno_group_norm_workspace_bytes(d, ctypes.byref(f), ctypes.byref(b)) == L.FNO_OK
+        assert f.value < 1 << 62 and b.value < 1 << 62
 
 
 def test_without_elements_no_pointers_are_needed():

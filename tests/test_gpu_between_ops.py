@@ -354,6 +354,82 @@ def test_group_norm_tokens(shape, dtype):
     assert all(torch.equal(a[2][n], b[2][n]) for n in a[2])
 
 
+# (last, channels, groups, grid, batch): work-groups of 64, 256 and 1024 threads and beyond, whole
+# vectors and ragged ones, pairs of lanes, one entry and one row, rows around the work-groups' rounds,
+# partial sums joined by the second pass and before it
+EDGES = [(True, c, g, (p,), b) for c, g, p, b in (
+    (8, 2, 70, 3), (16, 4, 300, 2), (24, 1, 33, 1), (40, 10, 129, 3), (64, 8, 4000, 1), (136, 17, 65, 2),
+    (320, 32, 100, 2), (328, 41, 9, 5), (4, 4, 1000, 2), (12, 1, 5000, 1), (132, 3, 77, 1),
+    (1048, 8, 17, 2), (64, 64, 777, 2), (128, 1, 20_000, 2), (264, 2, 16_384, 1))] + \
+    [(False, c, g, (p,), b) for c, g, p, b in (
+        (2, 1, 1024, 1), (2, 1, 1026, 2), (8, 1, 1023, 1), (8, 2, 2048, 3), (8, 2, 2050, 1),
+        (4, 1, 4096, 2), (4, 1, 4098, 1), (8, 1, 4095, 2), (1, 1, 16_384, 1), (1, 1, 16_392, 3),
+        (2, 1, 16_385, 1), (1, 1, 32_768, 2), (1, 1, 32_776, 1), (5, 1, 4100, 2), (300, 2, 8, 2),
+        (40, 1, 520, 1), (9, 3, 20_480, 1), (3, 1, 66_000, 2), (2048, 1, 6, 1), (700, 7, 17, 3))] + \
+    [(False, c, g, (), b) for c, g, b in (
+        (64, 1, 4), (64, 1, 513), (256, 32, 31), (256, 32, 32), (256, 32, 129), (1024, 4, 64),
+        (4096, 2, 5), (8192, 1, 3), (8200, 1, 3), (72, 9, 1000), (17 * 24, 17, 300), (2056, 8, 260))]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("case", EDGES, ids=str)
+def test_group_norm_edges(case, dtype):
+    L = _L()
+    last, channels, groups, grid, batch = case
+    k = EDGES.index(case)
+    act, mask = ACTS[k % 3], ((0.3, 5, 1) if k % 3 != 2 or last else None)
+    announce("group_norm edges", case, dtype, act, mask)
+    x, gamma, beta, gy = _case(k, channels, groups, grid, dtype, last, batch)
+    _, stats, want = _both(L, x, groups, gamma, beta, gy, act, last, mask)
+    drop = None if mask is None else L.Dropout(*mask)
+    args = (x, groups, gamma, beta, stats)
+    for keys in (("x",), ("gamma",), ("beta",)):
+        got = L.group_norm_bwd(*args, gy, act, last, drop, want=keys)
+        assert torch.equal(got[keys[0]], want[keys[0]])
+    over = gy.clone()
+    got = L.group_norm_bwd(*args, over, act, last, drop, out={"x": over})
+    assert all(torch.equal(got[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("dtype,last,field", [
+    (torch.float32, False, (8, 2, (3_000_001,))), (torch.bfloat16, False, (5, 1, (9_000_000,))),
+    (torch.float32, True, (20, 4, (1_200_003,))), (torch.float16, True, (45, 9, (1_100_001,))),
+    (torch.float32, False, (4096, 32, ())), (torch.bfloat16, False, (6150, 6, ()))], ids=str)
+def test_group_norm_outputs_past_the_cache(dtype, last, field):
+    """Outputs over 128 MB, which go past the caches, at odd places too."""
+    L = _L()
+    channels, groups, grid = field
+    batch = 2 if grid else 12_000
+    announce("group_norm large", dtype, last, field)
+    x, gamma, beta, gy = _case(9, channels, groups, grid, dtype, last, batch)
+    assert x.numel() * x.element_size() > 128 << 20
+    n = math.prod(x.shape[1:])
+    mask = (0.2, 9, 3)
+    buf = torch.empty(x.numel() + 64, dtype=dtype, device="cuda")
+    y = buf[1:1 + x.numel()].view(x.shape)
+    _, stats = L.group_norm_fwd(x, groups, gamma, beta, "silu", EPS, last, L.Dropout(*mask), out=y)
+    got = L.group_norm_bwd(x, groups, gamma, beta, stats, gy, "silu", last, L.Dropout(*mask))
+    sums = {}
+    step = 1 if grid else 3000
+    for at in range(0, batch, step):
+        part = slice(at, at + step)
+        f = _factor(x[part].shape, *mask, first=at * n)
+        ref = _Ref(x[part], groups, gamma, beta, "silu", last, f)
+        ref.check_fwd(y[part], stats[:, part])
+        ref.check_bwd(gy[part], {"x": got["x"][part], "gamma": None, "beta": None})
+        up = _split(gy[part], groups, last) * ref.f
+        g = up * _act64(ref.u, "silu")[1]
+        og = up.abs() * (16 * U + 1.2 * ref.off)
+        for k, v, o in (("gamma", g * ref.h, 128 * U * g.abs() * (ref.h.abs() + ref.kappa) + og * ref.h.abs()),
+                        ("beta", g, 128 * U * g.abs() + og)):
+            s = sums.setdefault(k, [0, 0])
+            s[0] = s[0] + v.sum((0, 3)).view(-1)
+            s[1] = s[1] + o.sum((0, 3)).view(-1)
+        del ref, f, up, g, og
+    for k, (v, o) in sums.items():
+        _close("grad_" + k, got[k], v, o)
+
+
 SOME = [(False, (20, 4, (9, 7))), (True, (20, 4, (9, 7))), (False, (6, 2, (12_000,))),
         (True, (45, 9, (300,))), (False, (24, 1, (3,))), (True, (300, 4, (65,))), (False, (96, 4, ())),
         (False, (5000, 2, ())), (False, (33, 3, (40_001,)))]
