@@ -1010,7 +1010,7 @@ class Dropout:
     __slots__ = ("desc", "ptr", "counter", "index")
 
     def __init__(self, p, seed, draw=0, counter=None):
-        if not (0.0 <= p and round(p * 65536) <= 65535):
+        if not (0.0 <= p <= 1.0 and round(p * 65536) <= 65535):
             raise ValueError(f"dropout: p must be in [0, 1) and not round to 1, not {p!r}")
         for name, v in (("seed", seed), ("draw", draw)):
             if v < 0 or v >> 64:
@@ -1153,7 +1153,7 @@ def group_norm_bwd(x, groups, gamma, beta, stats, grad_y, act=None, channels_las
     ws: as in group_norm_fwd."""
     gy_strides = _like_x(grad_y, x, "grad_y")
     o = out or {}
-    gx = o["x"] if "x" in o else         _torch.empty(x.shape, dtype=x.dtype, device=x.device) if "x" in want else None
+    gx = o["x"] if "x" in o else x.new_empty(x.shape) if "x" in want else None
     n = _group_shape(x.dtype, x.shape, groups, act, channels_last, x.stride(), gy_strides,
                      gy_strides if gx is None else _like_x(gx, x, "grad_x"), 0.0)
     index = _on_gpu(x)
