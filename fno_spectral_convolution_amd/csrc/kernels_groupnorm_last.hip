@@ -11,17 +11,20 @@ namespace {
 // tile of rows, tr of them at a time: a thread keeps to its vector's channels.  The part of a group
 // that lies in a block is a segment; group g and block k make segment g + k, so that a group's
 // segments are neighbours (numbers that no pair has stay unused).
-struct Tiles {
-  int cols, blocks, tc, tr;  // channels of a block, blocks, vectors of a block, rows at a time
-  int cg, tiles;             // channels of a group, tiles
-  int64_t rows, segments;    // rows of a tile, segments
-  bool paired;               // lanes 2 j and 2 j + 1 have neighbouring vectors of eight aligned elements
-  Divider by_tc, by_tr, by_cols, by_cg, by_blocks, by_tiles;
+struct Cut {
+  int64_t rows;  // of a tile
+  int tiles;
+  Divider by_tiles;
 };
-// rows of a tile for each thread, at least
-constexpr int kLeast = 8;
+struct Tiles : Cut {
+  int cols, blocks, tc, tr;  // channels of a block, blocks, vectors of a block, rows at a time
+  int cg;                    // channels of a group
+  int64_t segments;
+  bool paired;               // lanes 2 j and 2 j + 1 have neighbouring vectors of eight aligned elements
+  Divider by_tc, by_tr, by_cols, by_cg, by_blocks;
+};
 template <int VEC>
-Tiles tiles_of(const GroupArgs& a) {
+Tiles tiles_of(const GroupArgs& a, int least) {
   Tiles p;
   p.cg = a.channels / a.groups;
   const int64_t nvec = ceil_div(a.channels, VEC);
@@ -33,14 +36,14 @@ Tiles tiles_of(const GroupArgs& a) {
   p.blocks = (int)ceil_div(a.channels, p.cols);
   p.tr = kBlock / p.tc;
   p.segments = (int64_t)a.groups + p.blocks;
-  // As many work-groups as the card holds at a time (four a compute unit), with kLeast rows to a
-  // thread at least: a second, short round costs as much as a whole one.  4 x 96^2 x 320 half backward
+  // As many work-groups as the card holds at a time (four a compute unit), with `least` rows to a
+  // thread or more: a second, short round costs as much as a whole one.  4 x 96^2 x 320 half backward
   // with dropout 50 us, 58 with 1280 work-groups; 2 x 10^6 x 20 half 93, 108 with 1280, 101 with 2048.
   const int64_t want =
       std::max<int64_t>(1, 1024 / std::max<int64_t>(1, a.batch * p.blocks));
   const int64_t tiles =  // (rows of a tile fit 31 bits)
       std::max(ceil_div(a.npts, (int64_t)1 << 30),
-               std::min(ceil_div(a.npts, (int64_t)p.tr * kLeast), want));
+               std::min(ceil_div(a.npts, (int64_t)p.tr * least), want));
   p.rows = std::max<int64_t>(1, ceil_div(a.npts, tiles));
   p.tiles = (int)std::max<int64_t>(1, ceil_div(a.npts, p.rows));
   p.by_tc = Divider(p.tc);
@@ -58,6 +61,19 @@ bool joins(const Tiles& p) {
   const int64_t in_group = std::min<int64_t>(p.blocks, (p.cg + p.cols - 1) / p.cols + 1);
   return in_block * in_group * p.tiles <= 1024;
 }
+
+// The first pass's tiles: four rows to a thread or more, or eight where the second pass can then join
+// the parts.
+template <int VEC>
+Tiles parts_tiles(const GroupArgs& a) {
+  const Tiles p = tiles_of<VEC>(a, 4);
+  if (joins(p)) return p;
+  const Tiles q = tiles_of<VEC>(a, 8);
+  return joins(q) ? q : p;
+}
+// Rows to a thread in the second pass, at least: it has no parts of its own (3 x 4095 x 45 half backward
+// 23 us with four, 26 with eight, 29 with two; both passes).
+constexpr int kLeast = 4;
 
 struct Block {
   int64_t b, row0;     // entry, first row
@@ -88,22 +104,25 @@ __device__ __forceinline__ void vector_of(const Block& q, const Tiles& p, int ch
   lo = r < p.tr && at < channels ? at - c : VEC;
 }
 
-// Rows r, r + tr, ... of a tile, K at a time: all(at), and one(at) for the last ones; `at` is the
-// element that slot 0's row begins with, the same for the whole work-group, so that a thread has one
-// offset of its own for all its rows.
-template <int K, typename All, typename One>
+// Rows r, r + tr, ... of a tile, K at a time: f(at, n, all) with n of them there, all of them where
+// the constant `all` says so; `at` is the element that slot 0's row begins with, the same for the whole
+// work-group, so that a thread has one offset of its own for all its rows.  The last rows are loaded
+// together like the others (2 x 10^6 x 20 half forward 64 us; one by one 69).
+template <int K, typename F>
 __device__ __forceinline__ void tile_rows(const Tiles& p, const Block& q, int r, int channels,
-                                          All&& all, One&& one) {
+                                          F&& f) {
   int i = 0;
-  for (; i + K * p.tr <= q.rows; i += K * p.tr) all((q.row0 + i) * channels);
-  for (; i < q.rows; i += p.tr)
-    if (i + r < q.rows) one((q.row0 + i) * channels);
+  for (; i + K * p.tr <= q.rows; i += K * p.tr) f((q.row0 + i) * channels, K, std::true_type());
+  if (i + r < q.rows)
+    f((q.row0 + i) * channels, (int)p.by_tr.of((uint32_t)(q.rows - i - r - 1)) + 1,
+      std::false_type());
 }
-template <typename T, int VEC, int K>
-__device__ __forceinline__ void load_rows(const T* p, int64_t step, int64_t own,
+template <typename T, int VEC, int K, typename All>
+__device__ __forceinline__ void load_rows(const T* p, int64_t step, int64_t own, int n, All all,
                                           Raw<T, VEC> (&raw)[K]) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) raw[k] = load_raw<T, VEC, true>(p + k * step + own);
+  for (int k = 0; k < K; ++k)
+    if (all.value || k < n) raw[k] = load_raw<T, VEC, true>(p + k * step + own);
 }
 
 // The masks of a thread's K rows from element i on, four bits each.
@@ -113,20 +132,20 @@ __device__ __forceinline__ uint32_t row_masks(const GroupArgs& a, const Dropper&
   return a.drop.threshold ? drop.masks<VEC, K>((uint64_t)i, step, paired) : 0;
 }
 
-// Lanes to a segment of at most `width` channels: a power of two, so that the segments take the
+// log2 of the lanes to a segment of at most `width` channels, so that the segments take the
 // work-group between them.
 __device__ __forceinline__ int lanes_of(int segs, int width) {
-  int l = 64;
-  while (l > 1 && (l * segs > kBlock || l / 2 >= width)) l >>= 1;
+  int l = 6;
+  while (l > 0 && (segs << l > kBlock || 1 << (l - 1) >= width)) --l;
   return l;
 }
 // Calls f(segment, its first channel in the block, its width, lane, lanes) in the lanes of each.
 template <typename F>
 __device__ __forceinline__ void each_segment(const Tiles& p, const Block& q, F&& f) {
-  const int lanes = lanes_of(q.segs, min(p.cg, p.cols)), lane = threadIdx.x & (lanes - 1);
-  for (int s = threadIdx.x / lanes; s < q.segs; s += kBlock / lanes) {
+  const int log = lanes_of(q.segs, min(p.cg, p.cols)), lane = threadIdx.x & ((1 << log) - 1);
+  for (int s = threadIdx.x >> log; s < q.segs; s += kBlock >> log) {
     const int g = q.g0 + s, from = max(q.c0, g * p.cg), to = min(q.c1, (g + 1) * p.cg);
-    f(s, from - q.c0, to - from, lane, lanes);
+    f(s, from - q.c0, to - from, lane, 1 << log);
   }
 }
 // The threads of a block's channels, in sets that share the row slots.
@@ -156,38 +175,29 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats_last(GroupArgs a, Tiles p, 
     if (lo < VEC) {
       const T* from = x + q.b * a.x_stride;
       const int64_t own = (int64_t)r * a.channels + c;
-      const auto add = [&](const auto& raw) {
-        constexpr int N = sizeof(raw) / sizeof(raw[0]);
-        const float all = n + N, share = N * __builtin_amdgcn_rcpf(all);
-        const float between = share * (n * inv_m);
+      tile_rows<K>(p, q, r, a.channels, [&](int64_t at, int more, auto all) {
+        Raw<T, VEC> raw[K] = {};
+        load_rows<T, VEC, K>(from + at, (int64_t)p.tr * a.channels, own, more, all, raw);
+        const float rows = (float)more, seen = n + rows;
+        const float inv = all.value ? 1.0f / K : __builtin_amdgcn_rcpf(rows);
+        const float share = rows * __builtin_amdgcn_rcpf(seen), between = share * (n * inv_m);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           float sum = 0.f, sq = 0.f;
 #pragma unroll
-          for (int k = 0; k < N; ++k) sum += element<T, VEC>(raw[k], e);
-          const float m = sum * (1.0f / N);
+          for (int k = 0; k < K; ++k) sum += element<T, VEC>(raw[k], e);  // (zeros beyond `more`)
+          const float m = sum * inv;
 #pragma unroll
-          for (int k = 0; k < N; ++k) {
+          for (int k = 0; k < K; ++k) {
             const float d = element<T, VEC>(raw[k], e) - m;
-            sq += d * d;
+            sq += all.value || k < more ? d * d : 0.f;
           }
           const float d = m - mean[e];
           mean[e] += d * share;
           var[e] += sq * inv_m + (d * between) * d;
         }
-        n = all;
-      };
-      tile_rows<K>(
-          p, q, r, a.channels,
-          [&](int64_t at) {
-            Raw<T, VEC> raw[K];
-            load_rows<T, VEC, K>(from + at, (int64_t)p.tr * a.channels, own, raw);
-            add(raw);
-          },
-          [&](int64_t at) {
-            const Raw<T, VEC> raw[1] = {load_raw<T, VEC, true>(from + at + own)};
-            add(raw);
-          });
+        n = seen;
+      });
     }
     __syncthreads();
     if (lo < VEC)
@@ -252,31 +262,46 @@ __device__ __forceinline__ Span span_of(const Tiles& p, int g) {
   return {k0, k1 - k0 + 1};
 }
 // The parts of group g of entry b, one a tile for each of its segments.
-__device__ __forceinline__ const float2* parts_of(const Tiles& p, const float2* part, int64_t b,
-                                                  int g, const Span& sp) {
-  return part + (b * p.segments + g + sp.first) * p.tiles;
+__device__ __forceinline__ const float2* parts_of(const Tiles& p, const Cut& cut,
+                                                  const float2* part, int64_t b, int g,
+                                                  const Span& sp) {
+  return part + (b * p.segments + g + sp.first) * cut.tiles;
+}
+// Calls f(i, from[i]) for a lane's share of n parts, four loads ahead.
+template <typename F>
+__device__ __forceinline__ void each_part(const float2* from, int n, int lane, int lanes, F&& f) {
+  for (int i = lane; i < n; i += 4 * lanes) {
+    float2 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u * lanes < n) v[u] = from[i + u * lanes];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u * lanes < n) f(i + u * lanes, v[u]);
+  }
 }
 // Mean and r of group g of entry b from its parts, in `lanes` lanes.
-__device__ __forceinline__ float2 join_parts(const GroupArgs& a, const Tiles& p, const float2* part,
-                                             int64_t b, int g, int lane, int lanes) {
+__device__ __forceinline__ float2 join_parts(const GroupArgs& a, const Tiles& p, const Cut& cut,
+                                             const float2* part, int64_t b, int g, int lane,
+                                             int lanes) {
   const float inv = 1.0f / ((float)p.cg * (float)a.npts);
   const Span sp = span_of(p, g);
-  const float2* from = parts_of(p, part, b, g, sp);
+  const float2* from = parts_of(p, cut, part, b, g, sp);
   const auto share = [&](int i) {  // of the group's entries in part i
-    const int k = (int)p.by_tiles.of((uint32_t)i), block = sp.first + k;
+    const int k = (int)cut.by_tiles.of((uint32_t)i), block = sp.first + k;
     const int width = (int)(min((int64_t)(block + 1) * p.cols, (int64_t)(g + 1) * p.cg) -
                             max((int64_t)block * p.cols, (int64_t)g * p.cg));
-    const int64_t row0 = (i - k * p.tiles) * p.rows;
-    const int64_t rows = p.rows < a.npts - row0 ? p.rows : a.npts - row0;
+    const int64_t row0 = (i - k * cut.tiles) * cut.rows;
+    const int64_t rows = cut.rows < a.npts - row0 ? cut.rows : a.npts - row0;
     return (float)rows * inv * (float)width;
   };
   float mean = 0.f, var = 0.f;
-  for (int i = lane; i < sp.blocks * p.tiles; i += lanes) mean += share(i) * from[i].x;
+  each_part(from, sp.blocks * cut.tiles, lane, lanes,
+            [&](int i, const float2& v) { mean += share(i) * v.x; });
   mean = lanes_sum(mean, lanes);
-  for (int i = lane; i < sp.blocks * p.tiles; i += lanes) {
-    const float2 v = from[i];
+  each_part(from, sp.blocks * cut.tiles, lane, lanes, [&](int i, const float2& v) {
     var += v.y + ((v.x - mean) * share(i)) * (v.x - mean);
-  }
+  });
   return make_float2(mean, rsqrtf(lanes_sum(var, lanes) + a.eps));
 }
 
@@ -288,7 +313,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_finish_last(GroupArgs a, Tiles p,
   for (int64_t i = (int64_t)blockIdx.x * kWaves + threadIdx.x / 64; i < sides;
        i += (int64_t)gridDim.x * kWaves) {
     const int64_t b = by_groups.of(i);
-    const float2 st = join_parts(a, p, part, b, (int)(i - b * a.groups), threadIdx.x % 64, 64);
+    const float2 st = join_parts(a, p, p, part, b, (int)(i - b * a.groups), threadIdx.x % 64, 64);
     if (threadIdx.x % 64 == 0) {
       stats[i] = st.x;
       stats[sides + i] = st.y;
@@ -338,8 +363,8 @@ __device__ __forceinline__ void given_stats(const GroupArgs& a, const Block& q, 
 
 // stats: given (part NULL), or made here from the parts and, nullable, written
 template <typename T, int VEC, int K, bool EVEN>
-__global__ __launch_bounds__(kBlock) void k_gn_apply_last(GroupArgs a, Tiles p, int64_t total,
-                                                          bool stream, const T* x,
+__global__ __launch_bounds__(kBlock) void k_gn_apply_last(GroupArgs a, Tiles p, Cut parts,
+                                                          int64_t total, bool stream, const T* x,
                                                           const float* gamma, const float* beta,
                                                           const float2* part, T* y, float* stats) {
   __shared__ float2 s_st[32 * VEC];
@@ -351,7 +376,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_apply_last(GroupArgs a, Tiles p, 
     __syncthreads();
     if (part) {
       each_segment(p, q, [&](int s, int, int, int lane, int lanes) {
-        const float2 st = join_parts(a, p, part, q.b, q.g0 + s, lane, lanes);
+        const float2 st = join_parts(a, p, parts, part, q.b, q.g0 + s, lane, lanes);
         if (lane != 0) return;
         s_st[s] = st;
         // the block that has the group's first channel
@@ -382,32 +407,27 @@ __global__ __launch_bounds__(kBlock) void k_gn_apply_last(GroupArgs a, Tiles p, 
       if (a.drop.threshold) drop.apply<VEC>(f, mask);
       store_own<T, VEC>(to + at + own, f, EVEN ? 0 : lo, stream);
     };
-    tile_rows<K>(
-        p, q, r, a.channels,
-        [&](int64_t at) {
-          Raw<T, VEC> raw[K];
-          load_rows<T, VEC, K>(from + at, step, own, raw);
-          const uint32_t masks = row_masks<VEC, K>(a, drop, index + at + own, step, p.paired);
+    tile_rows<K>(p, q, r, a.channels, [&](int64_t at, int n, auto all) {
+      Raw<T, VEC> raw[K];
+      load_rows<T, VEC, K>(from + at, step, own, n, all, raw);
+      const uint32_t masks = row_masks<VEC, K>(a, drop, index + at + own, step, p.paired);
 #pragma unroll
-          for (int k = 0; k < K; ++k) put(raw[k], at + k * step, masks >> 4 * k);
-        },
-        [&](int64_t at) {
-          const Raw<T, VEC> raw = load_raw<T, VEC, true>(from + at + own);
-          put(raw, at, row_masks<VEC, 1>(a, drop, index + at + own, 0, false));
-        });
+      for (int k = 0; k < K; ++k)
+        if (all.value || k < n) put(raw[k], at + k * step, masks >> 4 * k);
+    });
   }
 }
 
 // A lane's share of the sums of gamma g and gamma g h of group g of entry b.
-__device__ __forceinline__ float2 seg_sums(const Tiles& p, const float2* seg, int64_t b, int g,
-                                           int lane, int lanes) {
+__device__ __forceinline__ float2 seg_sums(const Tiles& p, const Cut& cut, const float2* seg,
+                                           int64_t b, int g, int lane, int lanes) {
   const Span sp = span_of(p, g);
-  const float2* from = parts_of(p, seg, b, g, sp);
+  const float2* from = parts_of(p, cut, seg, b, g, sp);
   float2 v = make_float2(0.f, 0.f);
-  for (int k = lane; k < sp.blocks * p.tiles; k += lanes) {
-    v.x += from[k].x;
-    v.y += from[k].y;
-  }
+  each_part(from, sp.blocks * cut.tiles, lane, lanes, [&](int, const float2& w) {
+    v.x += w.x;
+    v.y += w.y;
+  });
   return v;
 }
 
@@ -445,21 +465,15 @@ __global__ __launch_bounds__(kBlock) void k_gn_sums_last(GroupArgs a, Tiles p, i
           sb[e] += g[e];
         }
       };
-      tile_rows<K>(
-          p, q, r, a.channels,
-          [&](int64_t at) {
-            Raw<T, VEC> rx[K], rg[K];
-            load_rows<T, VEC, K>(px + at, step, own, rx);
-            load_rows<T, VEC, K>(pg + at, step, own, rg);
-            const uint32_t masks = row_masks<VEC, K>(a, drop, index + at + own, step, p.paired);
+      tile_rows<K>(p, q, r, a.channels, [&](int64_t at, int n, auto all) {
+        Raw<T, VEC> rx[K], rg[K];
+        load_rows<T, VEC, K>(px + at, step, own, n, all, rx);
+        load_rows<T, VEC, K>(pg + at, step, own, n, all, rg);
+        const uint32_t masks = row_masks<VEC, K>(a, drop, index + at + own, step, p.paired);
 #pragma unroll
-            for (int k = 0; k < K; ++k) add(rx[k], rg[k], masks >> 4 * k);
-          },
-          [&](int64_t at) {
-            const Raw<T, VEC> rx = load_raw<T, VEC, true>(px + at + own);
-            const Raw<T, VEC> rg = load_raw<T, VEC, true>(pg + at + own);
-            add(rx, rg, row_masks<VEC, 1>(a, drop, index + at + own, 0, false));
-          });
+        for (int k = 0; k < K; ++k)
+          if (all.value || k < n) add(rx[k], rg[k], masks >> 4 * k);
+      });
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
         if (e >= lo) s_sum[r * p.cols + c + e - q.c0] = make_float2(sg[e], sb[e]);
@@ -505,8 +519,8 @@ __global__ __launch_bounds__(kBlock) void k_gn_sums_last(GroupArgs a, Tiles p, i
 }
 
 template <typename T, int VEC, int K, bool EVEN>
-__global__ __launch_bounds__(kBlock) void k_gn_grad_last(GroupArgs a, Tiles p, int64_t total,
-                                                         bool stream, const T* x,
+__global__ __launch_bounds__(kBlock) void k_gn_grad_last(GroupArgs a, Tiles p, Cut parts,
+                                                         int64_t total, bool stream, const T* x,
                                                          const float* gamma, const float* beta,
                                                          const float* stats, const T* gy,
                                                          Between z, const float2* seg, T* gx) {
@@ -523,7 +537,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_grad_last(GroupArgs a, Tiles p, i
     if (z.own) {
       const float inv = 1.0f / ((float)p.cg * (float)a.npts);
       each_segment(p, q, [&](int s, int, int, int lane, int lanes) {
-        float2 v = seg_sums(p, seg, q.b, q.g0 + s, lane, lanes);
+        float2 v = seg_sums(p, parts, seg, q.b, q.g0 + s, lane, lanes);
         v = make_float2(lanes_sum(v.x, lanes) * inv, lanes_sum(v.y, lanes) * inv);
         if (lane == 0) s_m[s] = v;
       });
@@ -548,27 +562,21 @@ __global__ __launch_bounds__(kBlock) void k_gn_grad_last(GroupArgs a, Tiles p, i
       for (int e = 0; e < VEC; ++e) g[e] = rs[e] * fmaf(ga[e], g[e], -fmaf(h[e], m2[e], m1[e]));
       store_own<T, VEC>(to + at + own, g, EVEN ? 0 : lo, stream);
     };
-    tile_rows<K>(
-        p, q, r, a.channels,
-        [&](int64_t at) {
-          Raw<T, VEC> rx[K], rg[K];
-          load_rows<T, VEC, K>(px + at, step, own, rx);
-          load_rows<T, VEC, K>(pg + at, step, own, rg);
-          const uint32_t masks = row_masks<VEC, K>(a, drop, index + at + own, step, p.paired);
+    tile_rows<K>(p, q, r, a.channels, [&](int64_t at, int n, auto all) {
+      Raw<T, VEC> rx[K], rg[K];
+      load_rows<T, VEC, K>(px + at, step, own, n, all, rx);
+      load_rows<T, VEC, K>(pg + at, step, own, n, all, rg);
+      const uint32_t masks = row_masks<VEC, K>(a, drop, index + at + own, step, p.paired);
 #pragma unroll
-          for (int k = 0; k < K; ++k) put(rx[k], rg[k], at + k * step, masks >> 4 * k);
-        },
-        [&](int64_t at) {
-          const Raw<T, VEC> rx = load_raw<T, VEC, true>(px + at + own);
-          const Raw<T, VEC> rg = load_raw<T, VEC, true>(pg + at + own);
-          put(rx, rg, at, row_masks<VEC, 1>(a, drop, index + at + own, 0, false));
-        });
+      for (int k = 0; k < K; ++k)
+        if (all.value || k < n) put(rx[k], rg[k], at + k * step, masks >> 4 * k);
+    });
   }
 }
 
 __global__ __launch_bounds__(kBlock) void k_gn_between_last(GroupArgs a, Tiles p, Between z,
                                                             const float2* seg) {
-  between(a, z, [&](int64_t b, int g) { return seg_sums(p, seg, b, g, threadIdx.x, kBlock); });
+  between(a, z, [&](int64_t b, int g) { return seg_sums(p, p, seg, b, g, threadIdx.x, kBlock); });
 }
 
 // ---- launches ------------------------------------------------------------------------------------
@@ -589,8 +597,8 @@ hipError_t fwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
                float* stats, void* ws, hipStream_t s) {
   pick(a, [&](auto vec) {
     constexpr int V = vec.value, K = kRowsAhead<T, V>;
-    const Tiles p = tiles_of<V>(a);
-    const int64_t total = a.batch * p.tiles * p.blocks;
+    const Tiles p = parts_tiles<V>(a), r = tiles_of<V>(a, kLeast);
+    const int64_t total = a.batch * p.tiles * p.blocks, items = a.batch * r.tiles * r.blocks;
     float2* part = static_cast<float2*>(ws);
     hipLaunchKernelGGL((k_gn_stats_last<T, V, K>), grid_of(total), dim3(kBlock), 0, s, a, p, total,
                        x, part);
@@ -604,8 +612,8 @@ hipError_t fwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
       part = nullptr;
     }
     const auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid_of(total), dim3(kBlock), 0, s, a, p, total, stream_out<T>(a), x,
-                         gamma, beta, part, y, stats);
+      hipLaunchKernelGGL(kernel, grid_of(items), dim3(kBlock), 0, s, a, r, p, items, stream_out<T>(a),
+                         x, gamma, beta, part, y, stats);
     };
     if (V > 1 && even(a)) go(k_gn_apply_last<T, V, K, V != 1>);
     else go(k_gn_apply_last<T, V, K, false>);
@@ -619,11 +627,11 @@ hipError_t bwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
                hipStream_t s) {
   pick(a, [&](auto vec) {
     constexpr int V = vec.value, K = 4;
-    const Tiles p = tiles_of<V>(a);
-    const int64_t total = a.batch * p.tiles * p.blocks;
+    const Tiles p = parts_tiles<V>(a), r = tiles_of<V>(a, kLeast);
+    const int64_t total = a.batch * p.tiles * p.blocks, items = a.batch * r.tiles * r.blocks;
     const Space z(a, a.batch * p.tiles, a.batch * p.segments * p.tiles);
     const Between q = z.between(a, ws, gx != nullptr, ggamma, gbeta,
-                                joins(p) && small(a), total);
+                                joins(p) && small(a), items);
     const auto go = [&](auto first, auto second) {
       hipLaunchKernelGGL(first, grid_of(total), dim3(kBlock), 0, s, a, p, total, x, gamma, beta,
                          stats, gy, static_cast<float*>(ws), z.segments_at(ws));
@@ -631,9 +639,9 @@ hipError_t bwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
         hipLaunchKernelGGL(k_gn_between_last, Space::grid(a, q), dim3(kBlock), 0, s, a, p, q,
                            z.segments_at(ws));
       if (gx)
-        hipLaunchKernelGGL(second, q.own ? Space::grid(a, q) : grid_of(total), dim3(kBlock), 0, s, a, p,
-                           total, stream_out<T>(a), x, gamma, beta, stats, gy, q, z.segments_at(ws),
-                           gx);
+        hipLaunchKernelGGL(second, q.own ? Space::grid(a, q) : grid_of(items), dim3(kBlock), 0, s, a, r,
+                           p, items, stream_out<T>(a), x, gamma, beta, stats, gy, q,
+                           z.segments_at(ws), gx);
     };
     if (V > 1 && even(a)) go(k_gn_sums_last<T, V, K, V != 1>, k_gn_grad_last<T, V, K, V != 1>);
     else go(k_gn_sums_last<T, V, K, false>, k_gn_grad_last<T, V, K, false>);
@@ -645,7 +653,7 @@ hipError_t bwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
 
 size_t group_norm_last_fwd_bytes(const GroupArgs& a) {
   return pick(a, [&](auto vec) {
-    const Tiles p = tiles_of<vec.value>(a);
+    const Tiles p = parts_tiles<vec.value>(a);
     return up((int64_t)sizeof(float2) * a.batch * p.segments * p.tiles) +
            (joins(p) ? 0 : up((int64_t)sizeof(float) * 2 * a.batch * a.groups));
   });
@@ -653,7 +661,7 @@ size_t group_norm_last_fwd_bytes(const GroupArgs& a) {
 
 size_t group_norm_last_bwd_bytes(const GroupArgs& a) {
   return pick(a, [&](auto vec) {
-    const Tiles p = tiles_of<vec.value>(a);
+    const Tiles p = parts_tiles<vec.value>(a);
     return Space(a, a.batch * p.tiles, a.batch * p.segments * p.tiles).bytes();
   });
 }
