@@ -24,7 +24,7 @@ struct Tiles : Cut {
   Divider by_tc, by_tr, by_cols, by_cg, by_blocks;
 };
 template <int VEC>
-Tiles tiles_of(const GroupArgs& a, int least) {
+Tiles tiles_of(const GroupArgs& a, int least, int most) {
   Tiles p;
   p.cg = a.channels / a.groups;
   const int64_t nvec = ceil_div(a.channels, VEC);
@@ -36,11 +36,10 @@ Tiles tiles_of(const GroupArgs& a, int least) {
   p.blocks = (int)ceil_div(a.channels, p.cols);
   p.tr = kBlock / p.tc;
   p.segments = (int64_t)a.groups + p.blocks;
-  // As many work-groups as the card holds at a time (four a compute unit), with `least` rows to a
-  // thread or more: a second, short round costs as much as a whole one.  4 x 96^2 x 320 half backward
-  // with dropout 50 us, 58 with 1280 work-groups; 2 x 10^6 x 20 half 93, 108 with 1280, 101 with 2048.
+  // `most` work-groups or a few more, with `least` rows to a thread or more: a second, short round costs
+  // as much as a whole one
   const int64_t want =
-      std::max<int64_t>(1, 1024 / std::max<int64_t>(1, a.batch * p.blocks));
+      std::max<int64_t>(1, most / std::max<int64_t>(1, a.batch * p.blocks));
   const int64_t tiles =  // (rows of a tile fit 31 bits)
       std::max(ceil_div(a.npts, (int64_t)1 << 30),
                std::min(ceil_div(a.npts, (int64_t)p.tr * least), want));
@@ -65,12 +64,18 @@ bool joins(const Tiles& p) {
 // The first pass's tiles: four rows to a thread or more, or eight where the second pass can then join
 // the parts.
 template <int VEC>
-Tiles parts_tiles(const GroupArgs& a) {
-  const Tiles p = tiles_of<VEC>(a, 4);
+Tiles parts_tiles(const GroupArgs& a, int most) {
+  const Tiles p = tiles_of<VEC>(a, 4, most);
   if (joins(p)) return p;
-  const Tiles q = tiles_of<VEC>(a, 8);
+  const Tiles q = tiles_of<VEC>(a, 8, most);
   return joins(q) ? q : p;
 }
+// Work-groups of each pass, two, three and four a compute unit.  The first passes end with sums over
+// the work-group: 8 x 256^2 x 128 bf16 moments 24.6 us, 26.8 with 768, 26.9 with 1024; 4 x 96^2 x 320
+// half sums with dropout 21.6, 23.2 with 512, 22.8 with 1024.  The second ones only stream: the same two
+// 48.4 and 25.4 us, with 768 54.2 and 24.4, with 512 60.3 and 27.0; with 1280 both passes of the latter
+// took 8 more.
+constexpr int kMoments = 512, kSums = 768, kSecond = 1024;
 // Rows to a thread in the second pass, at least: it has no parts of its own (3 x 4095 x 45 half backward
 // 23 us with four, 26 with eight, 29 with two; both passes).
 constexpr int kLeast = 4;
@@ -597,7 +602,7 @@ hipError_t fwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
                float* stats, void* ws, hipStream_t s) {
   pick(a, [&](auto vec) {
     constexpr int V = vec.value, K = kRowsAhead<T, V>;
-    const Tiles p = parts_tiles<V>(a), r = tiles_of<V>(a, kLeast);
+    const Tiles p = parts_tiles<V>(a, kMoments), r = tiles_of<V>(a, kLeast, kSecond);
     const int64_t total = a.batch * p.tiles * p.blocks, items = a.batch * r.tiles * r.blocks;
     float2* part = static_cast<float2*>(ws);
     hipLaunchKernelGGL((k_gn_stats_last<T, V, K>), grid_of(total), dim3(kBlock), 0, s, a, p, total,
@@ -627,7 +632,7 @@ hipError_t bwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
                hipStream_t s) {
   pick(a, [&](auto vec) {
     constexpr int V = vec.value, K = 4;
-    const Tiles p = parts_tiles<V>(a), r = tiles_of<V>(a, kLeast);
+    const Tiles p = parts_tiles<V>(a, kSums), r = tiles_of<V>(a, kLeast, kSecond);
     const int64_t total = a.batch * p.tiles * p.blocks, items = a.batch * r.tiles * r.blocks;
     const Space z(a, a.batch * p.tiles, a.batch * p.segments * p.tiles);
     const Between q = z.between(a, ws, gx != nullptr, ggamma, gbeta,
@@ -653,7 +658,7 @@ hipError_t bwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
 
 size_t group_norm_last_fwd_bytes(const GroupArgs& a) {
   return pick(a, [&](auto vec) {
-    const Tiles p = parts_tiles<vec.value>(a);
+    const Tiles p = parts_tiles<vec.value>(a, kMoments);
     return up((int64_t)sizeof(float2) * a.batch * p.segments * p.tiles) +
            (joins(p) ? 0 : up((int64_t)sizeof(float) * 2 * a.batch * a.groups));
   });
@@ -661,7 +666,7 @@ size_t group_norm_last_fwd_bytes(const GroupArgs& a) {
 
 size_t group_norm_last_bwd_bytes(const GroupArgs& a) {
   return pick(a, [&](auto vec) {
-    const Tiles p = parts_tiles<vec.value>(a);
+    const Tiles p = parts_tiles<vec.value>(a, kSums);
     return Space(a, a.batch * p.tiles, a.batch * p.segments * p.tiles).bytes();
   });
 }
