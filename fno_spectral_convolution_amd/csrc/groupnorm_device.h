@@ -11,7 +11,7 @@
 // variance comes from deviations about a mean, never from E[x^2] - E[x]^2: each thread keeps count,
 // mean and squared deviations of what it has seen, and two of these join as
 // M2 = M2_a + M2_b + n_a n_b / (n_a + n_b) (mean_a - mean_b)^2 (Chan, Golub, LeVeque 1979).  Sums are
-// float32 in a fixed order.
+// float32 in a fixed order, without atomics.  Each pass rounds once, where it stores.
 #pragma once
 
 #include <algorithm>

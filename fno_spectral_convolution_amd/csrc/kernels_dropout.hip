@@ -2,6 +2,11 @@
 //
 // A thread takes eight elements at a time, what one block of the generator serves.  The mask goes by
 // the packed index, so that entries that lie apart have the mask of their packed copy.
+//
+// Bound by memory: 134 million bfloat16 elements onto a residual 125 us, 6.5 TB/s; float32 261 (6.2)
+// and without the residual 175 (6.1).  The generator and what makes bits of it are 21 vector
+// instructions an element, about half the time of the bfloat16 pass, and hide behind the loads.  Few
+// elements are the launch: 8 x 1024 bfloat16 2.5 us of kernel in a call of 7.5.
 #include <algorithm>
 
 #include "dropout_device.h"

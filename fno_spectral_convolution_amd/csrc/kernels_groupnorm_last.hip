@@ -1,5 +1,11 @@
 // Group norm of channels-last data [batch][npts][channels] (and of rows of one point that are longer
 // than a work-group holds, the same memory).  groupnorm_device.h has the mathematics.
+//
+// A thread keeps to four channels and goes down the rows, so that its weights, statistics and sums stay
+// in registers.  Two passes: 8 x 256^2 x 128 bfloat16 with SiLU 76.5 us, moments 26 (5.2 TB/s), a launch
+// that joins them 5, output 48 to 54 (5 TB/s); 4 x 96^2 x 320 half with SiLU and dropout backward 46,
+// sums 21, between 5, gradient 25: twelve rows a thread, whose setting out and sums over the work-group
+// are a third of the instructions.
 #include "groupnorm_device.h"
 
 namespace fno {
