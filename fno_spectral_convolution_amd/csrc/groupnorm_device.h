@@ -262,7 +262,7 @@ bool stream_out(const GroupArgs& a) {
 
 // Whether a backward's second pass should do for itself what is between the passes: small data, where a
 // launch counts (4 x 20 x 64^2 float32 18 us against 22; 4 x 96^2 x 320 half, three times as large as
-// the limit, 49 against 47).
+// the limit, loses 2 of 47).
 inline bool small(const GroupArgs& a) { return a.batch * a.channels * a.npts <= 1 << 22; }
 
 // A backward's workspace: the partial rows, the segments' sums (channels last), the means.

@@ -223,3 +223,9 @@ def test_binding_refuses():
         L.Dropout(0.5, 1, counter=torch.zeros(2, dtype=torch.int64))
     with pytest.raises(ValueError, match="int64"):
         L.Dropout(0.5, 1, counter=torch.zeros(1))
+
+
+@pytest.mark.parametrize("p", [math.inf, -math.inf, math.nan, -0.1, 1.0, 1 - 2.0 ** -18, 2.0])
+def test_probabilities_that_are_none(p):
+    with pytest.raises(ValueError, match="p must be in"):
+        L.Dropout(p, 1)
