@@ -1122,6 +1122,11 @@ hipError_t first_bwd(const GroupArgs& a, const T* x, const float* gamma, const f
 
 bool none(const GroupArgs& a) { return a.batch == 0 || a.npts == 0; }
 
+__global__ __launch_bounds__(kBlock) void k_gn_zero(int64_t n, float* p) {
+  for (int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x; i < n; i += (int64_t)gridDim.x * kBlock)
+    p[i] = 0.f;
+}
+
 }  // namespace
 
 size_t group_norm_fwd_bytes(const GroupArgs& a, int dtype) {
@@ -1132,6 +1137,12 @@ size_t group_norm_fwd_bytes(const GroupArgs& a, int dtype) {
 hipError_t launch_group_norm_fwd(const GroupArgs& a, int dtype, const void* x, const float* gamma,
                                  const float* beta, void* y, float* stats, void* ws,
                                  hipStream_t s) {
+  if (none(a)) {
+    const int64_t n = 2 * a.batch * a.groups;
+    if (!stats || n == 0) return hipSuccess;
+    hipLaunchKernelGGL(k_gn_zero, grid_of(ceil_div(n, kBlock)), dim3(kBlock), 0, s, n, stats);
+    return hipGetLastError();
+  }
   const Form form = form_of(a);
   if (form == kLast) return launch_group_norm_last_fwd(a, dtype, x, gamma, beta, y, stats, ws, s);
   return by_type(dtype, [&](auto t) {

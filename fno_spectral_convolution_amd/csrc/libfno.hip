@@ -2115,19 +2115,22 @@ fno_status fno_group_norm_fwd(const fno_group_norm_desc* desc, const fno_dropout
   if (st != FNO_OK) return st;
   if (group_writes_overlap(a, a.y_stride))
     return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: y_stride < channels * npts");
-  if (a.batch == 0 || a.npts == 0) return FNO_OK;
-  const size_t w = dtype_bytes(desc->dtype);
-  REQ_AT(x, "x", w);
-  REQ_AT(y, "y", w);
-  OPT_AT(gamma, "gamma", sizeof(float));
-  OPT_AT(beta, "beta", sizeof(float));
   OPT_AT(stats, "stats", sizeof(float));
-  if (x == y && a.batch > 1 && a.x_stride != a.y_stride)
-    return fail(FNO_ERR_INVALID_ARGUMENT, "group norm in place needs x_stride == y_stride");
-  const size_t need = fno::group_norm_fwd_bytes(a, desc->dtype);
-  if (need > 0) {
-    REQ(ws, "workspace");
-    if (ws_bytes < need) return fail(FNO_ERR_INVALID_ARGUMENT, "workspace too small");
+  const bool none = a.batch == 0 || a.npts == 0;
+  if (a.batch == 0 || (none && !stats)) return FNO_OK;
+  if (!none) {
+    const size_t w = dtype_bytes(desc->dtype);
+    REQ_AT(x, "x", w);
+    REQ_AT(y, "y", w);
+    OPT_AT(gamma, "gamma", sizeof(float));
+    OPT_AT(beta, "beta", sizeof(float));
+    if (x == y && a.batch > 1 && a.x_stride != a.y_stride)
+      return fail(FNO_ERR_INVALID_ARGUMENT, "group norm in place needs x_stride == y_stride");
+    const size_t need = fno::group_norm_fwd_bytes(a, desc->dtype);
+    if (need > 0) {
+      REQ(ws, "workspace");
+      if (ws_bytes < need) return fail(FNO_ERR_INVALID_ARGUMENT, "workspace too small");
+    }
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
   LAUNCH("group_norm_fwd", s,

@@ -123,8 +123,8 @@ fno_status fno_group_norm_workspace_bytes(const fno_group_norm_desc* desc, size_
                                           size_t* bwd);
 
 /* drop NULL: no dropout.  gamma and beta (float32 [channels]) may be NULL: 1 and 0.  stats
- * (nullable) receives float32 [2][batch][groups]: mu, then r, for the backward.  y may be x (the
- * same pointer and stride).  A non-finite x makes its own group of its entry non-finite, where that
+ * (nullable) receives float32 [2][batch][groups]: mu, then r, for the backward (0 and 0 where there
+ * are no points).  y may be x (the same pointer and stride).  A non-finite x makes its own group of its entry non-finite, where that
  * is not dropped, and no other. */
 fno_status fno_group_norm_fwd(const fno_group_norm_desc* desc, const fno_dropout* drop,
                               const void* x, const float* gamma, const float* beta, void* y,
