@@ -92,6 +92,13 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
 struct Moments {
   float n, mean, var;
 };
+// That share of a thread's squared deviations.  Their sum may pass float32's range where the variance
+// does not: scaled() then adds each one up divided, for which the others are spared the instruction.
+template <typename F>
+__device__ __forceinline__ float variance_share(float sq, float inv_m, F&& scaled) {
+  if (__builtin_expect(sq <= 3.402823466e38f, 1)) return sq * inv_m;
+  return scaled();  // (a NaN among them stays)
+}
 __device__ __forceinline__ void join(Moments& a, float n, float mean, float var, float inv_m) {
   const float all = a.n + n, share = n > 0.f ? n * __builtin_amdgcn_rcpf(all) : 0.f;
   const float d = mean - a.mean;

@@ -141,7 +141,18 @@ __device__ __forceinline__ void add_moments(Moments& m, const Raw<T, VEC> (&raw)
       const float d = element<T, VEC>(raw[k], e) - mean;
       sq += e >= lo[k] ? d * d : 0.f;
     }
-  join(m, n, mean, sq * inv_m, inv_m);
+  const float var = variance_share(sq, inv_m, [&] {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float d = element<T, VEC>(raw[k], e) - mean;
+        v += e >= lo[k] ? d * inv_m * d : 0.f;
+      }
+    return v;
+  });
+  join(m, n, mean, var, inv_m);
 }
 
 // y of one vector: x from its group's mean and by = gamma r, at = beta; element i of the field
@@ -187,7 +198,18 @@ __global__ __launch_bounds__(BLOCK) void k_gn_whole(GroupArgs a, Strip p, int64_
         sq += !masked.value || e >= it.lo[k] ? d * d : 0.f;
       }
     });
-    const float rstd = rsqrtf(block_sum<BLOCK / 64>(sq * inv_m, 0.f, s_red[1]).x + a.eps);
+    const float share = variance_share(sq, inv_m, [&] {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = element<T, VEC>(raw[k], e) - mean;
+          v += e >= it.lo[k] ? d * inv_m * d : 0.f;
+        }
+      return v;
+    });
+    const float rstd = rsqrtf(block_sum<BLOCK / 64>(share, 0.f, s_red[1]).x + a.eps);
     if (stats && threadIdx.x == 0) {
       stats[q.bg] = mean;
       stats[a.batch * a.groups + q.bg] = rstd;
@@ -730,7 +752,15 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows(GroupArgs a, int cg, Divider 
           sq += !masked.value || e >= lo[k] ? f[k][e] * f[k][e] : 0.f;
         }
     });
-    const float rstd = rsqrtf(slot_sum<TPR, BLOCK>(sq * inv, s_sum, flip) + a.eps);
+    const float share = variance_share(sq, inv, [&] {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v += e >= lo[k] ? f[k][e] * inv * f[k][e] : 0.f;
+      return v;
+    });
+    const float rstd = rsqrtf(slot_sum<TPR, BLOCK>(share, s_sum, flip) + a.eps);
     if (!live) continue;
     T* o = y + b * a.y_stride;
 #pragma unroll

@@ -192,20 +192,41 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats_last(GroupArgs a, Tiles p, 
         const float rows = (float)more, seen = n + rows;
         const float inv = all.value ? 1.0f / K : __builtin_amdgcn_rcpf(rows);
         const float share = rows * __builtin_amdgcn_rcpf(seen), between = share * (n * inv_m);
+        float m[VEC], sq[VEC], all_sq = 0.f;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          float sum = 0.f, sq = 0.f;
+          float sum = 0.f;
+          sq[e] = 0.f;
 #pragma unroll
           for (int k = 0; k < K; ++k) sum += element<T, VEC>(raw[k], e);  // (zeros beyond `more`)
-          const float m = sum * inv;
+          m[e] = sum * inv;
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            const float d = element<T, VEC>(raw[k], e) - m;
-            sq += all.value || k < more ? d * d : 0.f;
+            const float d = element<T, VEC>(raw[k], e) - m[e];
+            sq[e] += all.value || k < more ? d * d : 0.f;
           }
-          const float d = m - mean[e];
+          all_sq += sq[e];
+        }
+        // (as variance_share, one question for all)
+        if (__builtin_expect(all_sq <= 3.402823466e38f, 1)) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) sq[e] *= inv_m;
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            sq[e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+              const float d = element<T, VEC>(raw[k], e) - m[e];
+              sq[e] += k < more ? d * inv_m * d : 0.f;
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = m[e] - mean[e];
           mean[e] += d * share;
-          var[e] += sq * inv_m + (d * between) * d;
+          var[e] += sq[e] + (d * between) * d;
         }
         n = seen;
       });

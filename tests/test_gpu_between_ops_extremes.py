@@ -32,3 +32,40 @@ def test_statistics_without_points(last):
     L.group_norm_fwd(many, 12, channels_last=last, stats=out[:-1].view(2, 70_001, 12))
     assert not out[:-1].any() and float(out[-1]) == 7.0
     L.group_norm_fwd(many[:0], 12, channels_last=last, stats=out[:0].view(2, 0, 12))
+
+
+# (last, channels, groups, grid, batch): rows, groups in 64, 256 and 1024 threads, two passes with several
+# planes to a strip and several strips to a plane, channels last with and without whole vectors
+FAR = [(False, 4096, 2, (), 5), (False, 8192, 1, (), 3), (False, 20_000, 1, (), 2), (False, 24, 1, (40,), 3),
+       (False, 8, 2, (2048,), 3), (False, 8, 1, (4095,), 2), (False, 20, 1, (3000,), 2),
+       (False, 2, 1, (70_001,), 2), (False, 300, 1, (3,), 2), (True, 64, 8, (777,), 2),
+       (True, 45, 9, (1300,), 2), (True, 4, 4, (9001,), 1), (True, 1, 1, (5003,), 2),
+       (True, 128, 1, (20_000,), 1)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("case", FAR, ids=str)
+def test_deviations_whose_squares_pass_the_range(case, dtype):
+    """A few elements 2.5e19 and more from the rest: their squares, 6e38 and more, are beyond float32, the
+    variance, a share of 1 / m of their sum, is not."""
+    L = _L()
+    last, channels, groups, grid, batch = case
+    announce("group_norm far elements", case, dtype)
+    x, gamma, beta, gy = _case(FAR.index(case), channels, groups, grid, dtype, last, batch)
+    flat = x.view(-1)
+    m = math.prod(grid) * channels // groups
+    for k, value in ((0, 2.5e19), (flat.numel() // 2, -3e19), (flat.numel() - 1, 2e19)):
+        flat[k] = value
+    ref = _Ref(x, groups, gamma, beta, None, last, None)
+    assert m >= 300 and bool(torch.isfinite(ref.rstd.float()).all()) and float(ref.rstd.min()) > 1e-19
+    _, stats, _ = _both(L, x, groups, gamma, beta, gy, None, last, None)
+    assert float(stats[1].min()) > 1e-19
+    # non-finite ones still are: the other groups keep their bits
+    y0, s0 = L.group_norm_fwd(x, groups, gamma, beta, channels_last=last)
+    for value in (math.inf, math.nan):
+        bad = x.clone()
+        bad.view(-1)[0] = value
+        y, s = L.group_norm_fwd(bad, groups, gamma, beta, channels_last=last)
+        own = torch.zeros_like(s0[0], dtype=torch.bool)
+        own[0, 0] = True
+        assert bool(s[1][own].isnan().all()) and torch.equal(s[:, ~own], s0[:, ~own])
