@@ -92,12 +92,22 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
 struct Moments {
   float n, mean, var;
 };
-// That share of a thread's squared deviations.  Their sum may pass float32's range where the variance
-// does not: scaled() then adds each one up divided, for which the others are spared the instruction.
-template <typename F>
-__device__ __forceinline__ float variance_share(float sq, float inv_m, F&& scaled) {
-  if (__builtin_expect(sq <= 3.402823466e38f, 1)) return sq * inv_m;
-  return scaled();  // (a NaN among them stays)
+// Squared deviations may pass float32's range where the variance does not.  sums(divided) adds a
+// thread's up, with the constant `divided` each divided before it is squared: an instruction an element
+// that is spent only where the sum without it came out infinite (or NaN, which it stays).
+template <typename F, typename G>
+__device__ __forceinline__ auto in_range(F&& sums, G&& var) {
+  auto v = sums(std::false_type());
+  if (__builtin_expect(!(var(v) <= 3.402823466e38f), 0)) v = sums(std::true_type());
+  return v;
+}
+template <typename D>
+__device__ __forceinline__ float square(float d, float inv_m, D divided) {
+  return divided.value ? d * inv_m * d : d * d;
+}
+template <typename D>
+__device__ __forceinline__ float share_of(float sq, float inv_m, D divided) {
+  return divided.value ? sq : sq * inv_m;
 }
 __device__ __forceinline__ void join(Moments& a, float n, float mean, float var, float inv_m) {
   const float all = a.n + n, share = n > 0.f ? n * __builtin_amdgcn_rcpf(all) : 0.f;

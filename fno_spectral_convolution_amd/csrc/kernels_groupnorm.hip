@@ -122,9 +122,9 @@ struct Items {
 };
 
 // moments of a thread's vectors, one join for all
-template <typename T, int VEC, int K>
+template <typename T, int VEC, int K, typename D>
 __device__ __forceinline__ void add_moments(Moments& m, const Raw<T, VEC> (&raw)[K],
-                                            const int (&lo)[K], float inv_m) {
+                                            const int (&lo)[K], float inv_m, D divided) {
   float n = 0.f, sum = 0.f, sq = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -139,20 +139,9 @@ __device__ __forceinline__ void add_moments(Moments& m, const Raw<T, VEC> (&raw)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const float d = element<T, VEC>(raw[k], e) - mean;
-      sq += e >= lo[k] ? d * d : 0.f;
+      sq += e >= lo[k] ? square(d, inv_m, divided) : 0.f;
     }
-  const float var = variance_share(sq, inv_m, [&] {
-    float v = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = element<T, VEC>(raw[k], e) - mean;
-        v += e >= lo[k] ? d * inv_m * d : 0.f;
-      }
-    return v;
-  });
-  join(m, n, mean, var, inv_m);
+  join(m, n, mean, share_of(sq, inv_m, divided), inv_m);
 }
 
 // y of one vector: x from its group's mean and by = gamma r, at = beta; element i of the field
@@ -183,7 +172,7 @@ __global__ __launch_bounds__(BLOCK) void k_gn_whole(GroupArgs a, Strip p, int64_
     const Items<VEC, K, BLOCK> it(p, q, a.npts);
     Raw<T, VEC> raw[K] = {};
     it.load(x + q.b * a.x_stride + q.channel * a.npts, raw);
-    float sum = 0.f, sq = 0.f;
+    float sum = 0.f;
     it.each([&](int k, auto masked) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
@@ -191,25 +180,20 @@ __global__ __launch_bounds__(BLOCK) void k_gn_whole(GroupArgs a, Strip p, int64_
     });
     if (BLOCK > 64) __syncthreads();
     const float mean = block_sum<BLOCK / 64>(sum, 0.f, s_red[0]).x * inv_m;
-    it.each([&](int k, auto masked) {
+    const float var = in_range(
+        [&](auto divided) {
+          float sq = 0.f;
+          it.each([&](int k, auto masked) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = element<T, VEC>(raw[k], e) - mean;
-        sq += !masked.value || e >= it.lo[k] ? d * d : 0.f;
-      }
-    });
-    const float share = variance_share(sq, inv_m, [&] {
-      float v = 0.f;
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float d = element<T, VEC>(raw[k], e) - mean;
-          v += e >= it.lo[k] ? d * inv_m * d : 0.f;
-        }
-      return v;
-    });
-    const float rstd = rsqrtf(block_sum<BLOCK / 64>(share, 0.f, s_red[1]).x + a.eps);
+            for (int e = 0; e < VEC; ++e) {
+              const float d = element<T, VEC>(raw[k], e) - mean;
+              sq += !masked.value || e >= it.lo[k] ? square(d, inv_m, divided) : 0.f;
+            }
+          });
+          return share_of(sq, inv_m, divided);
+        },
+        [](float v) { return v; });
+    const float rstd = rsqrtf(block_sum<BLOCK / 64>(var, 0.f, s_red[1]).x + a.eps);
     if (stats && threadIdx.x == 0) {
       stats[q.bg] = mean;
       stats[a.batch * a.groups + q.bg] = rstd;
@@ -271,28 +255,32 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats(GroupArgs a, Pass ps, const
   for (int64_t w = blockIdx.x; w < ps.items; w += gridDim.x) {
     const Place q = place_of(w, p, a.groups);
     const T* from = x + q.b * a.x_stride + q.channel * a.npts;
-    Moments m = {0.f, 0.f, 0.f};
-    if (LONG) {
-      long_strips<VEC, K>(
-          p, q.s, a.npts,
-          [&](int64_t at) {
-            constexpr int none[K] = {};
-            Raw<T, VEC> raw[K];
-            load_strip<T, VEC, K>(from + at, raw);
-            add_moments<T, VEC, K>(m, raw, none, inv_m);
-          },
-          [&](int64_t at, int lo) {
-            const Raw<T, VEC> v[1] = {load_raw<T, VEC>(from + at)};
-            const int own[1] = {lo};
-            add_moments<T, VEC, 1>(m, v, own, inv_m);
-          });
-    } else {
-      const Items<VEC, K, kBlock> it(p, q, a.npts);
-      Raw<T, VEC> raw[K] = {};
-      it.load(from, raw);
-      add_moments<T, VEC, K>(m, raw, it.lo, inv_m);
-    }
-    m = block_moments<kWaves>(m, inv_m, s_red);
+    const auto own = [&](auto divided) {
+      Moments m = {0.f, 0.f, 0.f};
+      if (LONG) {
+        long_strips<VEC, K>(
+            p, q.s, a.npts,
+            [&](int64_t at) {
+              constexpr int none[K] = {};
+              Raw<T, VEC> raw[K];
+              load_strip<T, VEC, K>(from + at, raw);
+              add_moments<T, VEC, K>(m, raw, none, inv_m, divided);
+            },
+            [&](int64_t at, int lo) {
+              const Raw<T, VEC> v[1] = {load_raw<T, VEC>(from + at)};
+              const int own[1] = {lo};
+              add_moments<T, VEC, 1>(m, v, own, inv_m, divided);
+            });
+      } else {
+        const Items<VEC, K, kBlock> it(p, q, a.npts);
+        Raw<T, VEC> raw[K] = {};
+        it.load(from, raw);
+        add_moments<T, VEC, K>(m, raw, it.lo, inv_m, divided);
+      }
+      return m;
+    };
+    const Moments m = block_moments<kWaves>(in_range(own, [](const Moments& v) { return v.var; }),
+                                            inv_m, s_red);
     if (threadIdx.x == 0) part[w] = make_float4(m.n, m.mean, m.var, 0.f);
   }
 }
@@ -732,7 +720,7 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows(GroupArgs a, int cg, Divider 
   fetch(b);
   for (int64_t at = (int64_t)blockIdx.x * kSlots; at < total; at += stride, b += rows) {
     const bool live = b < a.batch;
-    float f[NV][VEC], sum = 0.f, sq = 0.f;
+    float f[NV][VEC], sum = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) unpack<T, VEC>(next[k], f[k]);
     if (at + stride < total) fetch(b + rows);
@@ -743,24 +731,24 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows(GroupArgs a, int cg, Divider 
         for (int e = 0; e < VEC; ++e) sum += !masked.value || e >= lo[k] ? f[k][e] : 0.f;
     });
     const float mean = slot_sum<TPR, BLOCK>(sum, s_sum, flip) * inv;
-    by_mask(partial, [&](auto masked) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          f[k][e] -= mean;
-          sq += !masked.value || e >= lo[k] ? f[k][e] * f[k][e] : 0.f;
-        }
-    });
-    const float share = variance_share(sq, inv, [&] {
-      float v = 0.f;
+      for (int e = 0; e < VEC; ++e) f[k][e] -= mean;
+    const float var = in_range(
+        [&](auto divided) {
+          float sq = 0.f;
+          by_mask(partial, [&](auto masked) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
+            for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v += e >= lo[k] ? f[k][e] * inv * f[k][e] : 0.f;
-      return v;
-    });
-    const float rstd = rsqrtf(slot_sum<TPR, BLOCK>(share, s_sum, flip) + a.eps);
+              for (int e = 0; e < VEC; ++e)
+                sq += !masked.value || e >= lo[k] ? square(f[k][e], inv, divided) : 0.f;
+          });
+          return share_of(sq, inv, divided);
+        },
+        [](float v) { return v; });
+    const float rstd = rsqrtf(slot_sum<TPR, BLOCK>(var, s_sum, flip) + a.eps);
     if (!live) continue;
     T* o = y + b * a.y_stride;
 #pragma unroll

@@ -180,10 +180,14 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats_last(GroupArgs a, Tiles p, 
     const Block q = block_of(w, a, p);
     int r, c, lo;
     vector_of<VEC>(q, p, a.channels, r, c, lo);
-    float n = 0.f, mean[VEC], var[VEC];
-    fill(mean, 0.f);
-    fill(var, 0.f);
-    if (lo < VEC) {
+    struct {
+      float mean[VEC], var[VEC];
+    } m;
+    const auto moments = [&](auto divided) {
+      decltype(m) v;
+      float n = 0.f;
+      fill(v.mean, 0.f);
+      fill(v.var, 0.f);
       const T* from = x + q.b * a.x_stride;
       const int64_t own = (int64_t)r * a.channels + c;
       tile_rows<K>(p, q, r, a.channels, [&](int64_t at, int more, auto all) {
@@ -192,50 +196,37 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats_last(GroupArgs a, Tiles p, 
         const float rows = (float)more, seen = n + rows;
         const float inv = all.value ? 1.0f / K : __builtin_amdgcn_rcpf(rows);
         const float share = rows * __builtin_amdgcn_rcpf(seen), between = share * (n * inv_m);
-        float m[VEC], sq[VEC], all_sq = 0.f;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          float sum = 0.f;
-          sq[e] = 0.f;
+          float sum = 0.f, sq = 0.f;
 #pragma unroll
           for (int k = 0; k < K; ++k) sum += element<T, VEC>(raw[k], e);  // (zeros beyond `more`)
-          m[e] = sum * inv;
+          const float mean = sum * inv;
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            const float d = element<T, VEC>(raw[k], e) - m[e];
-            sq[e] += all.value || k < more ? d * d : 0.f;
+            const float d = element<T, VEC>(raw[k], e) - mean;
+            sq += all.value || k < more ? square(d, inv_m, divided) : 0.f;
           }
-          all_sq += sq[e];
-        }
-        // (as variance_share, one question for all)
-        if (__builtin_expect(all_sq <= 3.402823466e38f, 1)) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) sq[e] *= inv_m;
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            sq[e] = 0.f;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-              const float d = element<T, VEC>(raw[k], e) - m[e];
-              sq[e] += k < more ? d * inv_m * d : 0.f;
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float d = m[e] - mean[e];
-          mean[e] += d * share;
-          var[e] += sq[e] + (d * between) * d;
+          const float d = mean - v.mean[e];
+          v.mean[e] += d * share;
+          v.var[e] += share_of(sq, inv_m, divided) + (d * between) * d;
         }
         n = seen;
       });
-    }
+      return v;
+    };
+    if (lo < VEC)
+      m = in_range(moments, [](const auto& v) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum += v.var[e];
+        return sum;
+      });
     __syncthreads();
     if (lo < VEC)
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
-        if (e >= lo) s_mom[r * p.cols + c + e - q.c0] = make_float2(mean[e], var[e]);
+        if (e >= lo) s_mom[r * p.cols + c + e - q.c0] = make_float2(m.mean[e], m.var[e]);
     __syncthreads();
     // the row slots' moments of a segment: their mean first, then the deviations about it
     const Columns col(p);
