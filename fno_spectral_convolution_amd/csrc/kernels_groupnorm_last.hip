@@ -25,6 +25,7 @@ struct Cut {
 struct Tiles : Cut {
   int cols, blocks, tc, tr;  // channels of a block, blocks, vectors of a block, rows at a time
   int cg;                    // channels of a group
+  int seg_cols, seg_blocks;  // channels of a segment, blocks that a group touches, at most
   int64_t segments;
   bool paired;               // lanes 2 j and 2 j + 1 have neighbouring vectors of eight aligned elements
   Divider by_tc, by_tr, by_cols, by_cg, by_blocks;
@@ -51,6 +52,8 @@ Tiles tiles_of(const GroupArgs& a, int least, int most) {
                std::min(ceil_div(a.npts, (int64_t)p.tr * least), want));
   p.rows = std::max<int64_t>(1, ceil_div(a.npts, tiles));
   p.tiles = (int)std::max<int64_t>(1, ceil_div(a.npts, p.rows));
+  p.seg_cols = std::min(p.cg, p.cols);
+  p.seg_blocks = (int)std::min<int64_t>(p.blocks, ((int64_t)p.cg + p.cols - 1) / p.cols + 1);
   p.by_tc = Divider(p.tc);
   p.by_tr = Divider(p.tr);
   p.by_cols = Divider(p.cols);
@@ -62,9 +65,8 @@ Tiles tiles_of(const GroupArgs& a, int least, int most) {
 // Whether the second pass joins the parts for itself, which saves a launch: few enough for
 // a work-group's threads.
 bool joins(const Tiles& p) {
-  const int64_t in_block = std::min<int64_t>(p.cols, (p.cols + p.cg - 1) / p.cg + 1);
-  const int64_t in_group = std::min<int64_t>(p.blocks, (p.cg + p.cols - 1) / p.cols + 1);
-  return in_block * in_group * p.tiles <= 1024;
+  const int64_t in_block = std::min<int64_t>(p.cols, (p.cols + (int64_t)p.cg - 1) / p.cg + 1);
+  return in_block * p.seg_blocks * p.tiles <= 1024;
 }
 
 // The first pass's tiles: four rows to a thread or more, or eight where the second pass can then join
@@ -143,27 +145,30 @@ __device__ __forceinline__ uint32_t row_masks(const GroupArgs& a, const Dropper&
   return a.drop.threshold ? drop.masks<VEC, K>((uint64_t)i, step, paired) : 0;
 }
 
-// log2 of the lanes to a segment of at most `width` channels, so that the segments take the
+// log2 of the lanes to a segment that has at most `terms` to add up, so that the segments take the
 // work-group between them.
-__device__ __forceinline__ int lanes_of(int segs, int width) {
+__device__ __forceinline__ int lanes_of(int segs, int terms) {
   int l = 6;
-  while (l > 0 && (segs << l > kBlock || 1 << (l - 1) >= width)) --l;
+  while (l > 0 && (segs << l > kBlock || 1 << (l - 1) >= terms)) --l;
   return l;
 }
-// Calls f(segment, its first channel in the block, its width, lane, lanes) in the lanes of each.
+// Calls f(segment, its first channel in the block, its width, lane, lanes) in the lanes of each: for
+// sums over a segment's channels, or over the `terms` parts of its group.
 template <typename F>
-__device__ __forceinline__ void each_segment(const Tiles& p, const Block& q, F&& f) {
-  const int log = lanes_of(q.segs, min(p.cg, p.cols)), lane = threadIdx.x & ((1 << log) - 1);
+__device__ __forceinline__ void each_segment(const Tiles& p, const Block& q, int terms, F&& f) {
+  const int log = lanes_of(q.segs, terms), lane = threadIdx.x & ((1 << log) - 1);
   for (int s = threadIdx.x >> log; s < q.segs; s += kBlock >> log) {
     const int g = q.g0 + s, from = max(q.c0, g * p.cg), to = min(q.c1, (g + 1) * p.cg);
     f(s, from - q.c0, to - from, lane, 1 << log);
   }
 }
-// The threads of a block's channels, in sets that share the row slots.
+// The threads of a block's channels, in sets that share the row slots: no more than sixteen, whose sums
+// each channel's lane then adds up in a row (256 of them for a single channel put the mean of 1.1s off by
+// 42 units of 2^-24; 16 row slots to each of 16 sets are off by 11 at most).
 struct Columns {
   int sets, set, c;  // set >= sets: none
   __device__ __forceinline__ explicit Columns(const Tiles& p) {
-    sets = max(1, min((int)p.by_cols.of((uint32_t)kBlock), p.tr));
+    sets = max(1, min((int)p.by_cols.of((uint32_t)kBlock), min(p.tr, 16)));
     set = (int)p.by_cols.of((uint32_t)threadIdx.x);
     c = threadIdx.x - set * p.cols;
   }
@@ -243,7 +248,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats_last(GroupArgs a, Tiles p, 
       s_set[threadIdx.x] = sum;
     }
     __syncthreads();
-    each_segment(p, q, [&](int s, int from, int wide, int lane, int lanes) {
+    each_segment(p, q, p.seg_cols, [&](int s, int from, int wide, int lane, int lanes) {
       float v = 0.f;
       for (int i = 0; i < col.sets; ++i)
 #pragma unroll 4
@@ -263,7 +268,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats_last(GroupArgs a, Tiles p, 
       s_set[threadIdx.x] = sum;
     }
     __syncthreads();
-    each_segment(p, q, [&](int s, int from, int wide, int lane, int lanes) {
+    each_segment(p, q, p.seg_cols, [&](int s, int from, int wide, int lane, int lanes) {
       float v = 0.f;
       for (int i = 0; i < col.sets; ++i)
 #pragma unroll 4
@@ -398,7 +403,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_apply_last(GroupArgs a, Tiles p, 
     vector_of<VEC>(q, p, a.channels, r, c, lo);
     __syncthreads();
     if (part) {
-      each_segment(p, q, [&](int s, int, int, int lane, int lanes) {
+      each_segment(p, q, p.seg_blocks * parts.tiles, [&](int s, int, int, int lane, int lanes) {
         const float2 st = join_parts(a, p, parts, part, q.b, q.g0 + s, lane, lanes);
         if (lane != 0) return;
         s_st[s] = st;
@@ -527,7 +532,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_sums_last(GroupArgs a, Tiles p, i
       s_set[threadIdx.x] = make_float2(weight * v.y, weight * v.x);
     }
     __syncthreads();
-    each_segment(p, q, [&](int s, int from, int wide, int lane, int lanes) {
+    each_segment(p, q, p.seg_cols, [&](int s, int from, int wide, int lane, int lanes) {
       float u = 0.f, v = 0.f;
       for (int k = lane; k < wide; k += lanes) {
         u += s_set[from + k].x;
@@ -559,7 +564,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_grad_last(GroupArgs a, Tiles p, C
     given_stats(a, q, stats, s_st);
     if (z.own) {
       const float inv = 1.0f / ((float)p.cg * (float)a.npts);
-      each_segment(p, q, [&](int s, int, int, int lane, int lanes) {
+      each_segment(p, q, p.seg_blocks * parts.tiles, [&](int s, int, int, int lane, int lanes) {
         float2 v = seg_sums(p, parts, seg, q.b, q.g0 + s, lane, lanes);
         v = make_float2(lanes_sum(v.x, lanes) * inv, lanes_sum(v.y, lanes) * inv);
         if (lane == 0) s_m[s] = v;

@@ -69,3 +69,24 @@ def test_deviations_whose_squares_pass_the_range(case, dtype):
         own = torch.zeros_like(s0[0], dtype=torch.bool)
         own[0, 0] = True
         assert bool(s[1][own].isnan().all()) and torch.equal(s[:, ~own], s0[:, ~own])
+
+
+# [batch, points, channels], groups, channels last: groups of one or few channels, whose statistics are
+# joined from many parts
+NARROW = [((1, 1 << 20, 1), 1), ((1, 1 << 18, 2), 2), ((2, 65_536, 4), 4), ((1, 65_536, 8), 8),
+          ((2, 16_384, 16), 16), ((1, 300_001, 3), 3), ((1, 70_003, 6), 6), ((3, 30_011, 12), 6)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16], ids=str)
+@pytest.mark.parametrize("shape,groups", NARROW, ids=str)
+def test_narrow_groups_of_many_points(shape, groups, dtype):
+    """Means far from zero and gradients of one sign, joined from hundreds of parts."""
+    L = _L()
+    announce("group_norm narrow", shape, groups, dtype)
+    g = _gen(sum(shape))
+    gamma, beta = 1 + 0.3 * _randn(g, shape[2]), 0.3 * _randn(g, shape[2])
+    for mean, up in ((1700.7, 1.7), (901.3, 0.9), (1.1, 1.1)):
+        x = (mean + _randn(g, *shape)).to(dtype)
+        gy = torch.full(shape, up, device="cuda").to(dtype)
+        _both(L, x, groups, gamma, beta, gy, None, True, None)
+        y, stats, _ = _both(L, torch.full_like(x, mean), groups, gamma, beta, gy, None, True, None)
