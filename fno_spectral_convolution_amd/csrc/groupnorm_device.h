@@ -200,10 +200,14 @@ __device__ __forceinline__ void fill(float (&f)[N], float v) {
 // there is little to add up, in the second pass's launch, whose work-groups make the means that they
 // need and are followed by those for the weights.
 constexpr int kSumCols = 16;
+struct Rows {
+  int64_t n;
+  const float* at;
+};
 struct Between {
-  int64_t rows;           // partial rows
+  Rows sums;              // for the weights
   int64_t groups;         // work-groups before those of the weights
-  const float* part;
+  const float* part;      // the first pass's rows
   float2* means;
   float *ggamma, *gbeta;  // nullable
   Divider by_groups;
@@ -218,10 +222,10 @@ __device__ __forceinline__ void weight_sums(const GroupArgs& a, const Between& z
   for (int64_t base = (blockIdx.x - z.groups) * kSumCols; base < width;
        base += (gridDim.x - z.groups) * kSumCols) {
     const int64_t i = base + col;
-    float s = 0.f;
+    float s = 0.f;  // (chains of up to 128 rows)
     if (i < width)
 #pragma unroll 8
-      for (int64_t k = slice; k < z.rows; k += kSlices) s += z.part[k * width + i];
+      for (int64_t k = slice; k < z.sums.n; k += kSlices) s += z.sums.at[k * width + i];
     s_col[slice][col] = s;
     __syncthreads();
     if (slice == 0 && i < width) {
@@ -282,28 +286,59 @@ bool stream_out(const GroupArgs& a) {
 // the limit, loses 2 of 47).
 inline bool small(const GroupArgs& a) { return a.batch * a.channels * a.npts <= 1 << 22; }
 
-// A backward's workspace: the partial rows, the segments' sums (channels last), the means.
+// Partial rows [2][channels] beyond `most` are folded into sums of `size` neighbours first: their number
+// goes with the batch, and the weights' sums over them have few work-groups, which add up one row after
+// the other in float32 (gradients of one sign came out up to 3000 units of 2^-24 off, and 300000 x 8 x 2
+// float32 backward took 1150 us, now 930; 65536 x 4 x 64 bf16 channels last 1097, now 934).  Up to
+// 2048 the chains are of 128 and the launch would not pay (2000 x 8 x 64 float32 channels last 28 us;
+// 4000 rows 51, 54 without).  About the root of their number to a sum, more where that would leave more
+// than the limit; in float64.
+constexpr int64_t kMostRows = 2048;
+struct Fold {
+  int64_t size, rows;  // rows of a sum, and sums; 1: none
+  explicit Fold(int64_t n, int64_t most = kMostRows) : size(1), rows(n) {
+    if (n <= most) return;
+    while (size * size < n || size * most < n) size *= 2;
+    rows = ceil_div(n, size);
+  }
+  size_t bytes(const GroupArgs& a) const {
+    return size == 1 ? 0 : up((int64_t)sizeof(float) * 2 * rows * a.channels);
+  }
+};
+// the rows to add up in place of n at `part`; `to`: f.bytes() of workspace, f of n rows
+Rows fold_rows(const GroupArgs& a, const Fold& f, int64_t n, const float* part, float* to,
+               hipStream_t s);
+
+// A backward's workspace: the partial rows, what they are folded into, the segments' sums (channels
+// last), the means.
 struct Space {
   int64_t rows;
-  size_t part, seg, means;
+  size_t part, fold, seg, means;
   Space(const GroupArgs& a, int64_t rows, int64_t segments)
       : rows(rows), part(up((int64_t)sizeof(float) * 2 * rows * a.channels)),
-        seg(up((int64_t)sizeof(float2) * segments)),
+        fold(Fold(rows).bytes(a)), seg(up((int64_t)sizeof(float2) * segments)),
         means(up((int64_t)sizeof(float2) * a.batch * a.groups)) {}
-  size_t bytes() const { return part + seg + means; }
+  size_t bytes() const { return part + fold + seg + means; }
   float2* segments_at(void* ws) const {
-    return reinterpret_cast<float2*>(static_cast<char*>(ws) + part);
+    return reinterpret_cast<float2*>(static_cast<char*>(ws) + part + fold);
   }
   float2* means_at(void* ws) const {
-    return reinterpret_cast<float2*>(static_cast<char*>(ws) + part + seg);
+    return reinterpret_cast<float2*>(static_cast<char*>(ws) + part + fold + seg);
   }
   // what is between the passes; items: of the second pass, in whose launch it is done where `own`
   Between between(const GroupArgs& a, void* ws, bool means, float* ggamma, float* gbeta, bool own,
                   int64_t items) const {
     own = own && means;
     const int64_t groups = own ? items : means ? a.batch * a.groups : 0;
-    return {rows, std::min<int64_t>(groups, kMaxGrid), static_cast<const float*>(ws), means_at(ws),
+    const float* part_at = static_cast<const float*>(ws);
+    return {{rows, part_at}, std::min<int64_t>(groups, kMaxGrid), part_at, means_at(ws),
             ggamma, gbeta, Divider(a.groups), own};
+  }
+  // after the first pass: the rows for the weights folded
+  void fold_in(const GroupArgs& a, Between& z, void* ws, hipStream_t s) const {
+    if (fold > 0 && (z.ggamma || z.gbeta))
+      z.sums = fold_rows(a, Fold(rows), rows, z.part,
+                         reinterpret_cast<float*>(static_cast<char*>(ws) + part), s);
   }
   // the grid with the weights' work-groups
   static dim3 grid(const GroupArgs& a, const Between& z) {

@@ -482,16 +482,40 @@ struct Sums {
                                        int64_t b, int64_t g) const {
     const int64_t first = g * cg;
     const float* rows = part + b * parts * 2 * a.channels + first;
-    float2 v = make_float2(0.f, 0.f);
+    double u = 0.0, v = 0.0;  // (a wide group has many)
     for (int64_t k = threadIdx.x; k < (int64_t)cg * parts; k += kBlock) {
       const int64_t j = by_cg.of(k), c = k - j * cg;
       const float weight = gamma ? gamma[first + c] : 1.f;
-      v.x += weight * rows[(j * 2 + 1) * a.channels + c];
-      v.y += weight * rows[j * 2 * a.channels + c];
+      u += weight * rows[(j * 2 + 1) * a.channels + c];
+      v += weight * rows[j * 2 * a.channels + c];
     }
-    return v;
+    return make_float2((float)u, (float)v);
   }
 };
+
+// to [ceil(n / size)][2][channels]: sums of `size` neighbouring rows, kSumCols columns to a work-group
+__global__ __launch_bounds__(kBlock) void k_gn_fold(int64_t width, int64_t n, int64_t size,
+                                                    int64_t columns, int64_t total,
+                                                    const float* part, float* to) {
+  constexpr int kSlices = kBlock / kSumCols;
+  __shared__ double s_col[kSlices][kSumCols];
+  const int col = threadIdx.x % kSumCols, slice = threadIdx.x / kSumCols;
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+    const int64_t row = w / columns, i = (w - row * columns) * kSumCols + col;
+    const int64_t end = (row + 1) * size < n ? (row + 1) * size : n;
+    double s = 0.0;
+    if (i < width)
+#pragma unroll 8
+      for (int64_t k = row * size + slice; k < end; k += kSlices) s += part[k * width + i];
+    s_col[slice][col] = s;
+    __syncthreads();
+    if (slice == 0 && i < width) {
+      for (int u = 1; u < kSlices; ++u) s += s_col[u][col];
+      to[row * width + i] = (float)s;
+    }
+    __syncthreads();
+  }
+}
 __global__ __launch_bounds__(kBlock) void k_gn_between(GroupArgs a, Between z, Sums sums,
                                                        const float* gamma) {
   between(a, z, [&](int64_t b, int g) { return sums.of(a, z.part, gamma, b, g); });
@@ -521,6 +545,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_sums(GroupArgs a, Pass ps, const 
             Raw<T, VEC> rx[K], rg[K];
             load_strip<T, VEC, K>(px + at, rx);
             load_strip<T, VEC, K>(pg + at, rg);
+            float sg = 0.f, sb = 0.f;  // of the strip: short chains
 #pragma unroll
             for (int k = 0; k < K; ++k) {
               float h[VEC], g[VEC];
@@ -528,10 +553,12 @@ __global__ __launch_bounds__(kBlock) void k_gn_sums(GroupArgs a, Pass ps, const 
                                   index + at + k * (kBlock * VEC), h, g);
 #pragma unroll
               for (int e = 0; e < VEC; ++e) {
-                sums.sg += g[e] * h[e];
-                sums.sb += g[e];
+                sg += g[e] * h[e];
+                sb += g[e];
               }
             }
+            sums.sg += sg;
+            sums.sb += sb;
           },
           [&](int64_t at, int lo) {
             float h[VEC], g[VEC];
@@ -933,8 +960,10 @@ auto pick_rows(int cg, F&& f) {
 // The backward's rows: groups and rows that a work-group takes at a time (as many of its slots as
 // can be used, rather more groups, which are neighbours), and its work-groups down the batch, which
 // write one partial row each.  One goes down up to four times: it then has the gradients themselves,
-// which spares the workspace and a launch (3.3 us for the host).
+// which spares the workspace and a launch (3.3 us for the host).  No more than 128 times where it does
+// not: a thread's sums are float32 chains of as many terms.
 constexpr int kRowsBlock = 1024;
+constexpr int64_t kRowsDown = 128;
 struct RowsShape {
   int wide, deep, chunks, down;
 };
@@ -953,7 +982,9 @@ RowsShape rows_shape(const GroupArgs& a, int tpr) {
     }
   }
   const int64_t times = ceil_div(a.batch, p.deep);
-  p.down = times <= 4 ? 1 : (int)std::min<int64_t>(times, std::max<int64_t>(1, 256 / p.chunks));
+  const int64_t down = std::max<int64_t>(std::max(1, 256 / p.chunks),
+                                         std::min(ceil_div(times, kRowsDown), (1 << 21) / (int64_t)p.chunks));
+  p.down = times <= 4 ? 1 : (int)std::min(times, down);
   return p;
 }
 
@@ -1054,20 +1085,33 @@ size_t fwd_bytes(const GroupArgs& a) {
   });
 }
 
+// Workspace of n partial rows alone, and the weights' gradients from them (by a kernel that adds wide
+// rows up in four float32 chains).
+Fold rows_fold(const GroupArgs& a, int64_t n) { return Fold(n, a.channels >= 4096 ? 512 : kMostRows); }
+size_t rows_bytes(const GroupArgs& a, int64_t n) {
+  return n == 1 ? 0 : up((int64_t)sizeof(float) * 2 * n * a.channels) + rows_fold(a, n).bytes(a);
+}
+hipError_t rows_finish(const GroupArgs& a, int64_t n, float* part, float* ggamma, float* gbeta,
+                       hipStream_t s) {
+  float* to = reinterpret_cast<float*>(reinterpret_cast<char*>(part) +
+                                       up((int64_t)sizeof(float) * 2 * n * a.channels));
+  const Rows r = fold_rows(a, rows_fold(a, n), n, part, to, s);
+  return launch_weight_sums(a.channels, (int)r.n, r.at, ggamma, gbeta, s);
+}
+
 template <typename T>
 size_t bwd_bytes(const GroupArgs& a) {
   if (form_of(a) == kLast) return group_norm_last_bwd_bytes(a);
   if (form_of(a) == kRows)
     return by_vector<kVec<T>>(a.channels / a.groups, [&](auto vec) {
       return pick_rows<vec.value>(a.channels / a.groups, [&](auto tpr, auto) {
-        const int down = rows_shape(a, tpr.value).down;
-        return down == 1 ? (size_t)0 : up((int64_t)sizeof(float) * 2 * down * a.channels);
+        return rows_bytes(a, rows_shape(a, tpr.value).down);
       });
     });
   return by_vector<kVec<T>>(a.npts, [&](auto vec) {
     constexpr int V = vec.value;
     if (pick_whole<V, kWholeBwd<V>>(a, [](auto, const Strip&) {}))
-      return a.batch == 1 ? (size_t)0 : up((int64_t)sizeof(float) * 2 * a.batch * a.channels);
+      return rows_bytes(a, a.batch);
     return Space(a, a.batch * strip_of<V, kAhead, kBlock>(a).parts, 0).bytes();
   });
 }
@@ -1096,7 +1140,7 @@ hipError_t rows_bwd(const GroupArgs& a, const T* x, const float* gamma, const fl
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !weights || parts == 1) return e;
-  return launch_weight_sums(a.channels, parts, part, ggamma, gbeta, s);
+  return rows_finish(a, parts, part, ggamma, gbeta, s);
 }
 
 template <typename T>
@@ -1119,11 +1163,12 @@ hipError_t first_bwd(const GroupArgs& a, const T* x, const float* gamma, const f
     const Space z(a, a.batch * p.parts, 0);
     const Pass q = pass_of<T>(a, p), r = second_of<T>(a, p, 1);
     const bool own = small(a) && p.cg * p.parts <= 4 * kBlock;
-    const Between t = z.between(a, ws, gx != nullptr, ggamma, gbeta, own, r.items);
+    Between t = z.between(a, ws, gx != nullptr, ggamma, gbeta, own, r.items);
     const Sums sums = {p.cg, p.parts, Divider(p.cg)};
     const auto go = [&](auto first, auto second) {
       hipLaunchKernelGGL(first, grid_of(q.items), dim3(kBlock), 0, s, a, q, x, gamma, beta, stats, gy,
                          part);
+      z.fold_in(a, t, ws, s);
       if (!t.own)
         hipLaunchKernelGGL(k_gn_between, Space::grid(a, t), dim3(kBlock), 0, s, a, t, sums, gamma);
       if (gx)
@@ -1135,7 +1180,7 @@ hipError_t first_bwd(const GroupArgs& a, const T* x, const float* gamma, const f
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !weights || !whole || a.batch == 1) return e;
-  return launch_weight_sums(a.channels, (int)a.batch, part, ggamma, gbeta, s);
+  return rows_finish(a, a.batch, part, ggamma, gbeta, s);
 }
 
 bool none(const GroupArgs& a) { return a.batch == 0 || a.npts == 0; }
@@ -1146,6 +1191,15 @@ __global__ __launch_bounds__(kBlock) void k_gn_zero(int64_t n, float* p) {
 }
 
 }  // namespace
+
+Rows fold_rows(const GroupArgs& a, const Fold& f, int64_t n, const float* part, float* to,
+               hipStream_t s) {
+  if (f.size == 1) return {n, part};
+  const int64_t width = 2 * (int64_t)a.channels, columns = ceil_div(width, kSumCols);
+  hipLaunchKernelGGL(k_gn_fold, grid_of(f.rows * columns), dim3(kBlock), 0, s, width, n, f.size,
+                     columns, f.rows * columns, part, to);
+  return {f.rows, to};
+}
 
 size_t group_norm_fwd_bytes(const GroupArgs& a, int dtype) {
   if (none(a)) return 0;

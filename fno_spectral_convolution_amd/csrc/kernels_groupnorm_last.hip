@@ -31,7 +31,7 @@ struct Tiles : Cut {
   Divider by_tc, by_tr, by_cols, by_cg, by_blocks;
 };
 template <int VEC>
-Tiles tiles_of(const GroupArgs& a, int least, int most) {
+Tiles tiles_of(const GroupArgs& a, int least, int most, int longest = 1 << 20) {
   Tiles p;
   p.cg = a.channels / a.groups;
   const int64_t nvec = ceil_div(a.channels, VEC);
@@ -43,12 +43,12 @@ Tiles tiles_of(const GroupArgs& a, int least, int most) {
   p.blocks = (int)ceil_div(a.channels, p.cols);
   p.tr = kBlock / p.tc;
   p.segments = (int64_t)a.groups + p.blocks;
-  // `most` work-groups or a few more, with `least` rows to a thread or more: a second, short round costs
-  // as much as a whole one
+  // at most `most` work-groups, with `least` rows to a thread or more: a second, short round costs as
+  // much as a whole one; or as many as leave `longest` rows to a thread
   const int64_t want =
       std::max<int64_t>(1, most / std::max<int64_t>(1, a.batch * p.blocks));
   const int64_t tiles =  // (rows of a tile fit 31 bits)
-      std::max(ceil_div(a.npts, (int64_t)1 << 30),
+      std::max(ceil_div(a.npts, std::min((int64_t)1 << 30, (int64_t)p.tr * longest)),
                std::min(ceil_div(a.npts, (int64_t)p.tr * least), want));
   p.rows = std::max<int64_t>(1, ceil_div(a.npts, tiles));
   p.tiles = (int)std::max<int64_t>(1, ceil_div(a.npts, p.rows));
@@ -72,10 +72,10 @@ bool joins(const Tiles& p) {
 // The first pass's tiles: four rows to a thread or more, or eight where the second pass can then join
 // the parts.
 template <int VEC>
-Tiles parts_tiles(const GroupArgs& a, int most) {
-  const Tiles p = tiles_of<VEC>(a, 4, most);
+Tiles parts_tiles(const GroupArgs& a, int most, int longest = 1 << 20) {
+  const Tiles p = tiles_of<VEC>(a, 4, most, longest);
   if (joins(p)) return p;
-  const Tiles q = tiles_of<VEC>(a, 8, most);
+  const Tiles q = tiles_of<VEC>(a, 8, most, longest);
   return joins(q) ? q : p;
 }
 // Work-groups of each pass, two, three and four a compute unit.  The first passes end with sums over
@@ -87,6 +87,8 @@ constexpr int kMoments = 512, kSums = 768, kSecond = 1024;
 // Rows to a thread in the second pass, at least: it has no parts of its own (3 x 4095 x 45 half backward
 // 23 us with four, 26 with eight, 29 with two; both passes).
 constexpr int kLeast = 4;
+// And in the sums at most, four of which make one term of a thread's float32 chain.
+constexpr int kLongest = 512;
 
 struct Block {
   int64_t b, row0;     // entry, first row
@@ -451,12 +453,12 @@ __device__ __forceinline__ float2 seg_sums(const Tiles& p, const Cut& cut, const
                                            int64_t b, int g, int lane, int lanes) {
   const Span sp = span_of(p, g);
   const float2* from = parts_of(p, cut, seg, b, g, sp);
-  float2 v = make_float2(0.f, 0.f);
+  double u = 0.0, v = 0.0;
   each_part(from, sp.blocks * cut.tiles, lane, lanes, [&](int, const float2& w) {
-    v.x += w.x;
-    v.y += w.y;
+    u += w.x;
+    v += w.y;
   });
-  return v;
+  return make_float2((float)u, (float)v);
 }
 
 // part: rows [batch * tiles] of [2][channels], sums of g h and g; seg [batch][segments][tiles]: sums
@@ -484,23 +486,28 @@ __global__ __launch_bounds__(kBlock) void k_gn_sums_last(GroupArgs a, Tiles p, i
       const T* pg = gy + q.b * a.y_stride;
       const int64_t index = q.b * a.npts * a.channels, own = (int64_t)r * a.channels + c;
       const int64_t step = (int64_t)p.tr * a.channels;
-      const auto add = [&](const Raw<T, VEC>& rx, const Raw<T, VEC>& rg, uint32_t mask) {
-        float h[VEC], g[VEC];
-        backward_terms<T, VEC>(a, drop, rx, rg, mu, rs, ga, be, mask, h, g);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          sg[e] += g[e] * h[e];
-          sb[e] += g[e];
-        }
-      };
       tile_rows<K>(p, q, r, a.channels, [&](int64_t at, int n, auto all) {
         Raw<T, VEC> rx[K], rg[K];
         load_rows<T, VEC, K>(px + at, step, own, n, all, rx);
         load_rows<T, VEC, K>(pg + at, step, own, n, all, rg);
         const uint32_t masks = row_masks<VEC, K>(a, drop, index + at + own, step, p.paired);
+        float tg[VEC], tb[VEC];  // of these rows (the first is always there)
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-          if (all.value || k < n) add(rx[k], rg[k], masks >> 4 * k);
+        for (int k = 0; k < K; ++k) {
+          if (!all.value && k >= n) continue;
+          float h[VEC], g[VEC];
+          backward_terms<T, VEC>(a, drop, rx[k], rg[k], mu, rs, ga, be, masks >> 4 * k, h, g);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            tg[e] = k == 0 ? g[e] * h[e] : fmaf(g[e], h[e], tg[e]);
+            tb[e] = k == 0 ? g[e] : tb[e] + g[e];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          sg[e] += tg[e];
+          sb[e] += tb[e];
+        }
       });
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
@@ -655,14 +662,15 @@ hipError_t bwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
                hipStream_t s) {
   pick(a, [&](auto vec) {
     constexpr int V = vec.value, K = 4;
-    const Tiles p = parts_tiles<V>(a, kSums), r = tiles_of<V>(a, kLeast, kSecond);
+    const Tiles p = parts_tiles<V>(a, kSums, kLongest), r = tiles_of<V>(a, kLeast, kSecond);
     const int64_t total = a.batch * p.tiles * p.blocks, items = a.batch * r.tiles * r.blocks;
     const Space z(a, a.batch * p.tiles, a.batch * p.segments * p.tiles);
-    const Between q = z.between(a, ws, gx != nullptr, ggamma, gbeta,
+    Between q = z.between(a, ws, gx != nullptr, ggamma, gbeta,
                                 joins(p) && small(a), items);
     const auto go = [&](auto first, auto second) {
       hipLaunchKernelGGL(first, grid_of(total), dim3(kBlock), 0, s, a, p, total, x, gamma, beta,
                          stats, gy, static_cast<float*>(ws), z.segments_at(ws));
+      z.fold_in(a, q, ws, s);
       if (!q.own)
         hipLaunchKernelGGL(k_gn_between_last, Space::grid(a, q), dim3(kBlock), 0, s, a, p, q,
                            z.segments_at(ws));
@@ -689,7 +697,7 @@ size_t group_norm_last_fwd_bytes(const GroupArgs& a) {
 
 size_t group_norm_last_bwd_bytes(const GroupArgs& a) {
   return pick(a, [&](auto vec) {
-    const Tiles p = parts_tiles<vec.value>(a, kSums);
+    const Tiles p = parts_tiles<vec.value>(a, kSums, kLongest);
     return Space(a, a.batch * p.tiles, a.batch * p.segments * p.tiles).bytes();
   });
 }

@@ -90,3 +90,46 @@ def test_narrow_groups_of_many_points(shape, groups, dtype):
         gy = torch.full(shape, up, device="cuda").to(dtype)
         _both(L, x, groups, gamma, beta, gy, None, True, None)
         y, stats, _ = _both(L, torch.full_like(x, mean), groups, gamma, beta, gy, None, True, None)
+
+
+# (last, channels, groups, grid, batch, dtype): many entries, or long runs of points, to a channel
+MANY = [(True, 64, 8, (4,), 65_536, 0), (True, 8, 2, (2,), 300_000, 0), (True, 6, 3, (3,), 40_000, 0),
+        (True, 1, 1, (2,), 1 << 21, 0), (False, 8, 4, (2,), 300_000, 0), (False, 20, 5, (6,), 90_001, 0),
+        (False, 2, 1, (12_000,), 3000, 0), (False, 4, 1, (), 1 << 25, 0), (False, 20, 4, (), 1 << 22, 0),
+        (False, 1030, 1, (3,), 4100, 0), (True, 8, 2, (2,), 300_000, 1), (False, 8, 4, (2,), 300_000, 2),
+        (False, 1, 1, (1 << 22,), 100, 0), (True, 4, 1, (1 << 18,), 800, 0)]
+
+
+@pytest.mark.parametrize("up", [1.1, 0.9])
+@pytest.mark.parametrize("case", MANY, ids=str)
+def test_weight_gradients_of_many_rows(case, up):
+    """Gradients of one sign and one size, over as many rows as a batch has: float32's rounding errors
+    then add up in one direction."""
+    L = _L()
+    last, channels, groups, grid, batch, kind = case
+    dtype = TYPES[kind]
+    announce("group_norm many rows", case, up)
+    g = _gen(batch + channels)
+    shape = (batch,) + grid + (channels,) if last else (batch, channels) + grid
+    x = torch.empty(shape, dtype=dtype, device="cuda")
+    step = max(1, (1 << 24) // math.prod(shape[1:]))
+    for at in range(0, batch, step):
+        x[at:at + step] = _randn(g, *x[at:at + step].shape)
+    gamma, beta = 1 + 0.3 * _randn(g, channels), 0.3 * _randn(g, channels)
+    gy = torch.full(shape, up, device="cuda").to(dtype)
+    _, stats = L.group_norm_fwd(x, groups, gamma, beta, None, EPS, last)
+    got = L.group_norm_bwd(x, groups, gamma, beta, stats, gy, None, last, want=("gamma", "beta"))
+    both = L.group_norm_bwd(x, groups, gamma, beta, stats, gy, None, last)
+    assert torch.equal(both["gamma"], got["gamma"]) and torch.equal(both["beta"], got["beta"])
+    sums = [0, 0, 0, 0]
+    for at in range(0, batch, step):
+        part = slice(at, at + step)
+        ref = _Ref(x[part], groups, gamma, beta, None, last, None)
+        if at == 0 or at + step >= batch:
+            ref.check_bwd(gy[part], {"x": both["x"][part], "gamma": None, "beta": None})
+        v = _split(gy[part], groups, last)
+        for i, t in enumerate((v * ref.h, 128 * U * v * (ref.h.abs() + ref.kappa) + 2 * U * v * ref.h.abs(),
+                               v, 130 * U * v)):
+            sums[i] = sums[i] + t.sum((0, 3)).view(-1)
+    _close("grad_gamma", got["gamma"], sums[0], sums[1])
+    _close("grad_beta", got["beta"], sums[2], sums[3])
