@@ -1778,13 +1778,15 @@ bool known_dtype(int32_t d) {
     if (ptr) REQ_AT(ptr, name, bytes); \
   } while (0)
 
-fno_status norm_args(const fno_layer_norm_desc* d, fno::NormArgs* a) {
+// `backward`: of a call that has a grad_x; the others do not look at its stride
+fno_status norm_args(const fno_layer_norm_desc* d, fno::NormArgs* a, bool backward) {
   if (!d) return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm descriptor is NULL");
   if (!known_dtype(d->dtype)) return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: unknown dtype");
   if (d->reserved != 0) return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: reserved must be 0");
   if (d->batch < 0 || d->npts < 0 || d->channels < 1)
     return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: batch, npts >= 0 and channels >= 1");
-  if (d->x_stride < 0 || d->y_stride < 0 || d->grad_x_stride < 0)
+  const int64_t gx_stride = backward ? d->grad_x_stride : 0;
+  if (d->x_stride < 0 || d->y_stride < 0 || gx_stride < 0)
     return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: strides must be >= 0");
   if (!(d->eps >= 0.0) || !std::isfinite(d->eps))
     return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: eps must be finite and >= 0");
@@ -1794,7 +1796,7 @@ fno_status norm_args(const fno_layer_norm_desc* d, fno::NormArgs* a) {
   // of 0 keep offsets below those)
   const int64_t lim = (int64_t)1 << 60;
   int64_t per, rows, all, span;
-  const int64_t st = std::max(std::max(d->x_stride, d->y_stride), d->grad_x_stride);
+  const int64_t st = std::max(std::max(d->x_stride, d->y_stride), gx_stride);
   if (__builtin_mul_overflow(d->channels, d->npts, &per) || per > lim ||
       __builtin_mul_overflow(d->batch, d->npts, &rows) || rows > lim ||
       __builtin_mul_overflow(rows, d->channels, &all) || all > lim ||
@@ -1805,7 +1807,7 @@ fno_status norm_args(const fno_layer_norm_desc* d, fno::NormArgs* a) {
   a->channels = (int)d->channels;
   a->x_stride = d->x_stride;
   a->y_stride = d->y_stride;
-  a->gx_stride = d->grad_x_stride;
+  a->gx_stride = gx_stride;
   a->eps = (float)d->eps;
   return FNO_OK;
 }
@@ -1872,7 +1874,8 @@ fno_status dropout(const char* name, const fno_dropout_desc* d, const fno_dropou
   return FNO_OK;
 }
 
-fno_status group_args(const fno_group_norm_desc* d, const fno_dropout* drop, fno::GroupArgs* a) {
+fno_status group_args(const fno_group_norm_desc* d, const fno_dropout* drop, fno::GroupArgs* a,
+                      bool backward) {
   if (!d) return fail(FNO_ERR_INVALID_ARGUMENT, "group norm descriptor is NULL");
   if (!known_dtype(d->dtype)) return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: unknown dtype");
   if (d->reserved != 0) return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: reserved must be 0");
@@ -1885,7 +1888,8 @@ fno_status group_args(const fno_group_norm_desc* d, const fno_dropout* drop, fno
     return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: batch, npts >= 0 and channels >= 1");
   if (d->groups < 1 || d->channels % d->groups != 0)
     return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: groups must divide channels");
-  if (d->x_stride < 0 || d->y_stride < 0 || d->grad_x_stride < 0)
+  const int64_t gx_stride = backward ? d->grad_x_stride : 0;
+  if (d->x_stride < 0 || d->y_stride < 0 || gx_stride < 0)
     return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: strides must be >= 0");
   if (!(d->eps >= 0.0) || !std::isfinite(d->eps))
     return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: eps must be finite and >= 0");
@@ -1894,7 +1898,7 @@ fno_status group_args(const fno_group_norm_desc* d, const fno_dropout* drop, fno
   // every byte offset, the bytes of all elements and those of the workspaces fit 62 bits
   const int64_t lim = (int64_t)1 << 56;
   int64_t per, all, span;
-  const int64_t st = std::max(std::max(d->x_stride, d->y_stride), d->grad_x_stride);
+  const int64_t st = std::max(std::max(d->x_stride, d->y_stride), gx_stride);
   if (__builtin_mul_overflow(d->channels, d->npts, &per) || per > lim ||
       __builtin_mul_overflow(d->batch, per, &all) || all > lim ||
       __builtin_mul_overflow(d->batch, st, &span) || span > lim)
@@ -1907,7 +1911,7 @@ fno_status group_args(const fno_group_norm_desc* d, const fno_dropout* drop, fno
   a->act = d->activation;
   a->x_stride = d->x_stride;
   a->y_stride = d->y_stride;
-  a->gx_stride = d->grad_x_stride;
+  a->gx_stride = gx_stride;
   a->eps = (float)d->eps;
   return drop_args(drop, &a->drop);
 }
@@ -2022,7 +2026,7 @@ extern "C" {
 fno_status fno_layer_norm_fwd(const fno_layer_norm_desc* desc, const void* x, const float* gamma,
                               const float* beta, void* y, float* stats, void* stream) {
   fno::NormArgs a;
-  fno_status st = norm_args(desc, &a);
+  fno_status st = norm_args(desc, &a, false);
   if (st != FNO_OK) return st;
   if (norm_writes_overlap(a, a.y_stride))
     return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: y_stride < channels * npts");
@@ -2044,7 +2048,7 @@ fno_status fno_layer_norm_fwd(const fno_layer_norm_desc* desc, const void* x, co
 fno_status fno_layer_norm_workspace_bytes(const fno_layer_norm_desc* desc, size_t* bytes) {
   if (!bytes) return fail(FNO_ERR_INVALID_ARGUMENT, "bytes is NULL");
   fno::NormArgs a;
-  fno_status st = norm_args(desc, &a);
+  fno_status st = norm_args(desc, &a, true);
   if (st != FNO_OK) return st;
   *bytes = norm_workspace(a, desc->dtype);
   return FNO_OK;
@@ -2055,7 +2059,7 @@ fno_status fno_layer_norm_bwd(const fno_layer_norm_desc* desc, const void* x, co
                               float* grad_gamma, float* grad_beta, void* ws, size_t ws_bytes,
                               void* stream) {
   fno::NormArgs a;
-  fno_status st = norm_args(desc, &a);
+  fno_status st = norm_args(desc, &a, true);
   if (st != FNO_OK) return st;
   if (grad_x && norm_writes_overlap(a, a.gx_stride))
     return fail(FNO_ERR_INVALID_ARGUMENT, "layer norm: grad_x_stride < channels * npts");
@@ -2100,7 +2104,7 @@ fno_status fno_dropout_bwd(const fno_dropout_desc* desc, const fno_dropout* drop
 fno_status fno_group_norm_workspace_bytes(const fno_group_norm_desc* desc, size_t* fwd,
                                           size_t* bwd) {
   fno::GroupArgs a;
-  const fno_status st = group_args(desc, nullptr, &a);
+  const fno_status st = group_args(desc, nullptr, &a, false);
   if (st != FNO_OK) return st;
   if (fwd) *fwd = fno::group_norm_fwd_bytes(a, desc->dtype);
   if (bwd) *bwd = fno::group_norm_bwd_bytes(a, desc->dtype);
@@ -2111,7 +2115,7 @@ fno_status fno_group_norm_fwd(const fno_group_norm_desc* desc, const fno_dropout
                               const void* x, const float* gamma, const float* beta, void* y,
                               float* stats, void* ws, size_t ws_bytes, void* stream) {
   fno::GroupArgs a;
-  const fno_status st = group_args(desc, drop, &a);
+  const fno_status st = group_args(desc, drop, &a, false);
   if (st != FNO_OK) return st;
   if (group_writes_overlap(a, a.y_stride))
     return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: y_stride < channels * npts");
@@ -2144,7 +2148,7 @@ fno_status fno_group_norm_bwd(const fno_group_norm_desc* desc, const fno_dropout
                               float* grad_gamma, float* grad_beta, void* ws, size_t ws_bytes,
                               void* stream) {
   fno::GroupArgs a;
-  const fno_status st = group_args(desc, drop, &a);
+  const fno_status st = group_args(desc, drop, &a, true);
   if (st != FNO_OK) return st;
   if (grad_x && group_writes_overlap(a, a.gx_stride))
     return fail(FNO_ERR_INVALID_ARGUMENT, "group norm: grad_x_stride < channels * npts");

@@ -118,7 +118,7 @@ typedef struct fno_group_norm_desc {
 } fno_group_norm_desc;
 
 /* Bytes of workspace of the two calls on this descriptor (either may be 0, its workspace then
- * NULL; fwd and bwd nullable). */
+ * NULL; fwd and bwd nullable).  Does not look at grad_x_stride either. */
 fno_status fno_group_norm_workspace_bytes(const fno_group_norm_desc* desc, size_t* fwd,
                                           size_t* bwd);
 
