@@ -58,12 +58,11 @@ Strip strip_of(const GroupArgs& a) {
   return p;
 }
 
-// Where a work item's strip begins: its entry, group and channels, and the first point.
+// Where a work item's strip begins: its entry, group and channels.
 struct Place {
   int64_t b, bg, s;  // entry, entry and group, strip (or part) of the plane
   int run;
   int64_t channel;   // of its first plane, in the field
-  int64_t point;     // of strip s in the plane
 };
 __device__ __forceinline__ Place place_of(int64_t w, const Strip& p, int groups) {
   Place q;
@@ -73,11 +72,11 @@ __device__ __forceinline__ Place place_of(int64_t w, const Strip& p, int groups)
   q.run = (int)(lines - q.bg * p.runs);
   q.b = p.by_groups.of(q.bg);
   q.channel = (q.bg - q.b * groups) * p.cg + (int64_t)q.run * p.planes;
-  q.point = 0;
   return q;
 }
 
-// A thread's vectors of a strip.
+// A thread's vectors of a strip of whole planes (p.strips = 1: a plane has no more points than a
+// work-group holds).
 template <int VEC, int K, int BLOCK>
 struct Items {
   int row[K];  // plane, from the strip's first
@@ -87,16 +86,16 @@ struct Items {
     const int t = threadIdx.x & ((1 << p.tpp) - 1), slot = threadIdx.x >> p.tpp;
     const int slots = BLOCK >> p.tpp;
     const int planes = min(p.planes, p.cg - q.run * p.planes);
-    const int left = (int)min(npts - q.point, (int64_t)1 << 30);  // of the plane, from here
+    const int points = (int)npts;
     int pass = 0, j = 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int e = (t + (j << p.tpp)) * VEC, start = min(e, left - VEC);
+      const int e = (t + (j << p.tpp)) * VEC, start = min(e, points - VEC);
       row[k] = pass * slots + slot;
-      const bool there = row[k] < planes && e < left;
+      const bool there = row[k] < planes && e < points;
       lo[k] = there ? e - start : VEC;
       if (!there) row[k] = 0;
-      off[k] = there ? row[k] * (int)min(npts, (int64_t)1 << 30) + start : 0;
+      off[k] = there ? row[k] * points + start : 0;
       if (++j == p.kv) j = 0, ++pass;
     }
   }

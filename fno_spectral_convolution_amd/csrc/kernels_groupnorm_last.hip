@@ -527,7 +527,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_sums_last(GroupArgs a, Tiles p, i
     }
     __syncthreads();
     float* row = part + (q.b * p.tiles + q.tile) * 2 * a.channels + q.c0;
-    if ((int)threadIdx.x < width) {  // (a block has at most 256 channels)
+    if ((int)threadIdx.x < width) {  // (a block has at most 128 channels)
       float2 v = s_set[threadIdx.x];
       for (int i = 1; i < col.sets; ++i) {
         v.x += s_set[i * p.cols + threadIdx.x].x;
