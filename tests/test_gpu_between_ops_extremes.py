@@ -11,7 +11,7 @@ import pytest
 import torch
 
 from tests.gpu_helpers import announce
-from tests.test_gpu_between_ops import (ACTS, EPS, TYPES, U, _act64, _both, _case, _close, _factor, _gen,
+from tests.test_gpu_between_ops import (EPS, TYPES, U, _act64, _both, _case, _close, _factor, _gen,
                                         _L, _randn, _Ref, _split)
 
 pytestmark = pytest.mark.gpu
@@ -133,3 +133,70 @@ def test_weight_gradients_of_many_rows(case, up):
             sums[i] = sums[i] + t.sum((0, 3)).view(-1)
     _close("grad_gamma", got["gamma"], sums[0], sums[1])
     _close("grad_beta", got["beta"], sums[2], sums[3])
+
+
+# (last, channels, groups, grid, batch): more than 2^20 work items in one pass or both, of work-groups of
+# 64, 256 and 1024 threads, of two passes with several planes to a strip, and channels last
+LOOPS = [(False, 8, 4, (2,), 300_001), (False, 128, 1, (3,), (1 << 20) + 3), (False, 300, 1, (3,), (1 << 20) + 3),
+         (False, 1030, 1, (3,), 215_000), (True, 4, 2, (2,), (1 << 20) + 5), (True, 6, 3, (3,), (1 << 20) + 5),
+         (True, 8, 2, (2,), (1 << 20) + 5), (True, 3, 1, (2,), (1 << 20) + 5)]
+
+
+@pytest.mark.parametrize("act,mask", [(None, None), ("silu", (0.3, 5, 1))], ids=["plain", "silu-dropout"])
+@pytest.mark.parametrize("case", LOOPS, ids=str)
+def test_more_work_items_than_work_groups(case, act, mask):
+    """Work-groups that go on to a second item, with the shared memory of the first."""
+    L = _L()
+    last, channels, groups, grid, batch = case
+    dtype = torch.float32 if channels < 100 else torch.bfloat16
+    announce("group_norm loops", case, act, mask)
+    g = _gen(batch + channels)
+    shape = (batch,) + grid + (channels,) if last else (batch, channels) + grid
+    n = math.prod(shape[1:])
+    x, gy = (torch.empty(shape, dtype=dtype, device="cuda") for _ in range(2))
+    step = max(1, (1 << 25) // n)
+    for at in range(0, batch, step):
+        x[at:at + step] = 0.7 + _randn(g, *x[at:at + step].shape)
+        gy[at:at + step] = 0.5 + _randn(g, *x[at:at + step].shape)
+    gamma, beta = 1 + 0.3 * _randn(g, channels), 0.3 * _randn(g, channels)
+    drop = None if mask is None else L.Dropout(*mask)
+    y, stats = L.group_norm_fwd(x, groups, gamma, beta, act, EPS, last, drop)
+    got = L.group_norm_bwd(x, groups, gamma, beta, stats, gy, act, last, drop)
+    sums = {}
+    for at in range(0, batch, step):
+        part = slice(at, at + step)
+        f = None if mask is None else _factor(x[part].shape, *mask, first=at * n)
+        ref = _Ref(x[part], groups, gamma, beta, act, last, f)
+        ref.check_fwd(y[part], stats[:, part])
+        ref.check_bwd(gy[part], {"x": got["x"][part], "gamma": None, "beta": None})
+        up = _split(gy[part], groups, last) * ref.f
+        v = up * _act64(ref.u, act)[1]
+        off = 2 * U * v.abs() if act is None else up.abs() * (16 * U + 1.2 * ref.off)
+        for k, t, o in (("gamma", v * ref.h, 128 * U * v.abs() * (ref.h.abs() + ref.kappa)
+                         + off * ref.h.abs()), ("beta", v, 128 * U * v.abs() + off)):
+            s = sums.setdefault(k, [0, 0])
+            s[0] = s[0] + t.sum((0, 3)).view(-1)
+            s[1] = s[1] + o.sum((0, 3)).view(-1)
+    for k, (t, o) in sums.items():
+        _close("grad_" + k, got[k], t, o)
+
+
+def test_more_strips_than_work_groups():
+    """Planes of a strip and a little more, as many as make over 2^20 work items of each pass.  The entries
+    are one entry in memory, so that all their outputs are the same bits."""
+    L = _L()
+    announce("group_norm loops of strips")
+    g = _gen(77)
+    for channels, batch in ((9, 116_600), (5, 104_900)):
+        x = (_randn(g, 1, channels, 4100) + 0.7).expand(batch, -1, -1)
+        gy = (_randn(g, 1, channels, 4100) + 0.5).expand(batch, -1, -1)
+        gamma, beta = 1 + 0.3 * _randn(g, channels), 0.3 * _randn(g, channels)
+        y, stats = L.group_norm_fwd(x, 1, gamma, beta, "gelu")
+        ref = _Ref(x[:1], 1, gamma, beta, "gelu", False, None)
+        ref.check_fwd(y[:1], stats[:, :1])
+        assert bool((stats == stats[:, :1]).all())
+        assert all(bool((y[at:at + 4096] == y[:1]).all()) for at in range(0, batch, 4096))
+        got = L.group_norm_bwd(x, 1, gamma, beta, stats, gy, "gelu", out={"x": y})
+        ref.check_bwd(gy[:1], {"x": got["x"][:1], "gamma": None, "beta": None})
+        assert all(bool((y[at:at + 4096] == y[:1]).all()) for at in range(0, batch, 4096))
+        del y, got
