@@ -622,6 +622,18 @@ template <typename T, int VEC>
 constexpr int kRowsAhead = VEC * (int)sizeof(T) == 8 ? 8 : 4;
 bool even(const GroupArgs& a) { return a.channels / a.groups % kVecLast == 0; }
 
+// Whether an output goes past the caches: where it is large, and the work-groups' rows begin and end near
+// whole lines.  Others are left to the cache to put together.  Forward and backward with the streaming
+// stores over without, 134 to 400 MB: rows of 256 bytes 149 us over 155 and 245 over 253, of 96 159 over
+// 162 and 265 over 274, but of 90 (45 half) 248 over 232 and 411 over 387, of 40 268 over 251 and 426 over
+// 418; 64 bf16 from 32 bytes into a line 186 over 175 and 296 over 290.  (Planes and rows of tokens gain
+// at any alignment: 20 x 600001 float32 212 over 218 and 334 over 361.)
+template <typename T>
+bool stream_rows(const GroupArgs& a, const T* to, int64_t stride) {
+  return stream_out<T>(a) && a.channels * sizeof(T) % 32 == 0 &&
+         reinterpret_cast<uintptr_t>(to) % 64 == 0 && (a.batch == 1 || stride * sizeof(T) % 64 == 0);
+}
+
 template <typename F>
 auto pick(const GroupArgs& a, F&& f) {
   return by_vector<kVecLast>(a.channels, f);
@@ -647,8 +659,8 @@ hipError_t fwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
       part = nullptr;
     }
     const auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid_of(items), dim3(kBlock), 0, s, a, r, p, items, stream_out<T>(a),
-                         x, gamma, beta, part, y, stats);
+      hipLaunchKernelGGL(kernel, grid_of(items), dim3(kBlock), 0, s, a, r, p, items,
+                         stream_rows(a, y, a.y_stride), x, gamma, beta, part, y, stats);
     };
     if (V > 1 && even(a)) go(k_gn_apply_last<T, V, K, V != 1>);
     else go(k_gn_apply_last<T, V, K, false>);
@@ -676,8 +688,8 @@ hipError_t bwd(const GroupArgs& a, const T* x, const float* gamma, const float* 
                            z.segments_at(ws));
       if (gx)
         hipLaunchKernelGGL(second, q.own ? Space::grid(a, q) : grid_of(items), dim3(kBlock), 0, s, a, r,
-                           p, items, stream_out<T>(a), x, gamma, beta, stats, gy, q,
-                           z.segments_at(ws), gx);
+                           p, items, stream_rows(a, gx, a.gx_stride), x, gamma, beta, stats, gy,
+                           q, z.segments_at(ws), gx);
     };
     if (V > 1 && even(a)) go(k_gn_sums_last<T, V, K, V != 1>, k_gn_grad_last<T, V, K, V != 1>);
     else go(k_gn_sums_last<T, V, K, false>, k_gn_grad_last<T, V, K, false>);
