@@ -31,7 +31,7 @@ struct Tiles : Cut {
   Divider by_tc, by_tr, by_cols, by_cg, by_blocks;
 };
 template <int VEC>
-Tiles tiles_of(const GroupArgs& a, int least, int most, int longest = 1 << 20) {
+Tiles tiles_of(const GroupArgs& a, int least, int most, int longest = 1 << 22) {
   Tiles p;
   p.cg = a.channels / a.groups;
   const int64_t nvec = ceil_div(a.channels, VEC);
@@ -44,11 +44,12 @@ Tiles tiles_of(const GroupArgs& a, int least, int most, int longest = 1 << 20) {
   p.tr = kBlock / p.tc;
   p.segments = (int64_t)a.groups + p.blocks;
   // at most `most` work-groups, with `least` rows to a thread or more: a second, short round costs as
-  // much as a whole one; or as many as leave `longest` rows to a thread
+  // much as a whole one; or as many as leave `longest` rows to a thread, up to a million
   const int64_t want =
       std::max<int64_t>(1, most / std::max<int64_t>(1, a.batch * p.blocks));
   const int64_t tiles =  // (rows of a tile fit 31 bits)
-      std::max(ceil_div(a.npts, std::min((int64_t)1 << 30, (int64_t)p.tr * longest)),
+      std::max(std::max(ceil_div(a.npts, (int64_t)1 << 30),
+                        std::min<int64_t>(ceil_div(a.npts, (int64_t)p.tr * longest), 1 << 20)),
                std::min(ceil_div(a.npts, (int64_t)p.tr * least), want));
   p.rows = std::max<int64_t>(1, ceil_div(a.npts, tiles));
   p.tiles = (int)std::max<int64_t>(1, ceil_div(a.npts, p.rows));
@@ -72,7 +73,7 @@ bool joins(const Tiles& p) {
 // The first pass's tiles: four rows to a thread or more, or eight where the second pass can then join
 // the parts.
 template <int VEC>
-Tiles parts_tiles(const GroupArgs& a, int most, int longest = 1 << 20) {
+Tiles parts_tiles(const GroupArgs& a, int most, int longest = 1 << 22) {
   const Tiles p = tiles_of<VEC>(a, 4, most, longest);
   if (joins(p)) return p;
   const Tiles q = tiles_of<VEC>(a, 8, most, longest);

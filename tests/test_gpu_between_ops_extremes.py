@@ -135,6 +135,12 @@ def test_weight_gradients_of_many_rows(case, up):
     _close("grad_beta", got["beta"], sums[2], sums[3])
 
 
+@pytest.mark.parametrize("case", [(False, 4, 1, (), 1 << 26, 1), (False, 4096, 32, (), 200_000, 1)], ids=str)
+def test_weight_gradients_of_many_tokens(case):
+    """More partial rows of tokens than are added up at a time."""
+    test_weight_gradients_of_many_rows(case, 1.1)
+
+
 # (last, channels, groups, grid, batch): more than 2^20 work items in one pass or both, of work-groups of
 # 64, 256 and 1024 threads, of two passes with several planes to a strip, and channels last
 LOOPS = [(False, 8, 4, (2,), 300_001), (False, 128, 1, (3,), (1 << 20) + 3), (False, 300, 1, (3,), (1 << 20) + 3),

@@ -30,3 +30,20 @@ def test_forward_does_not_look_at_grad_x_stride(stride):
         sizes.append((f.value, b.value))
     assert sizes[0] == sizes[1] and min(sizes[0]) > 0
     assert L._lib.fno_layer_norm_workspace_bytes(train._desc(grad_x_stride=stride), ctypes.byref(b)) == BAD
+
+
+@pytest.mark.parametrize("last", [0, 1])
+@pytest.mark.parametrize("channels", [1, 3, 64, 320])
+def test_workspaces_grow_with_the_points(channels, last):
+    """Up to the largest descriptor: no count in a workspace's layout wraps."""
+    sizes = [(0, 0)]
+    for k in range(31, 57):
+        if channels << k > 1 << 56:
+            break
+        d = between._desc(channels=channels, groups=1, npts=1 << k, batch=1, channels_last=last,
+                          x_stride=0, y_stride=0, grad_x_stride=0)
+        f, b = ctypes.c_size_t(), ctypes.c_size_t()
+        assert L._lib.fno_group_norm_workspace_bytes(d, ctypes.byref(f), ctypes.byref(b)) == L.FNO_OK
+        assert f.value >= sizes[-1][0] and b.value >= sizes[-1][1], k
+        sizes.append((f.value, b.value))
+    assert len(sizes) > 15
