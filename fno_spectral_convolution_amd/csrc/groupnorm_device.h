@@ -11,7 +11,8 @@
 // variance comes from deviations about a mean, never from E[x^2] - E[x]^2: each thread keeps count,
 // mean and squared deviations of what it has seen, and two of these join as
 // M2 = M2_a + M2_b + n_a n_b / (n_a + n_b) (mean_a - mean_b)^2 (Chan, Golub, LeVeque 1979).  Sums are
-// float32 in a fixed order, without atomics.  Each pass rounds once, where it stores.
+// float32 in a fixed order, without atomics, of chains that stay short whatever the sizes: a chain of n
+// like terms may be off by n / 3 units of 2^-24.  Each pass rounds once, where it stores.
 #pragma once
 
 #include <algorithm>
@@ -274,8 +275,9 @@ auto by_type(int dtype, F&& f) {
   return dtype == FNO_DTYPE_BF16 ? f((__bf16)0.f) : f((_Float16)0.f);
 }
 // Whether an output goes past the caches (nontemporal stores): where it fills half of the 256 MB cache
-// behind the L2s (4 x 64 x 512^2 float32, 268 MB, backward 214 us against 219; 8 x 64 x 512^2 bf16, as
-// large, 242 against 252; below, no difference).
+// behind the L2s (4 x 64 x 512^2 float32, 268 MB, with GELU forward 136 us against 140 and backward 216
+// against 224; 8 x 64 x 512^2 bf16, as large, 152 against 154 and 249 against 259, with dropout as well
+// 165 against 167 and the same 305; below, no difference).
 template <typename T>
 bool stream_out(const GroupArgs& a) {
   return a.batch * a.channels * a.npts > ((int64_t)128 << 20) / (int64_t)sizeof(T);

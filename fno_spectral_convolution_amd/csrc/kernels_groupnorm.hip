@@ -6,11 +6,12 @@
 // 4096 in 32 heads forward 45 us float32 (6.0 TB/s) and 31 bfloat16, backward bfloat16 43 and 5 for the
 // weights' sums.  Larger groups are read twice, statistics first: work-groups that wait for each other
 // within a launch could not share the card with a second call that does the same.  Both passes run at
-// the memory's rate, which reads out of the 256 MB cache do not exceed: 8 x 64 x 512^2 float32 with GELU
-// and dropout 264 us forward (moments 91, output 197 traced one by one; 6.1 TB/s with the second
-// reading), 2 x 20 x 128^3 float32 with GELU backward 265 (103 and 164; 6.3 TB/s).  Half data with GELU
-// and dropout are near the vector units' rate (8 x 64 x 512^2 bfloat16 backward 319: some 41
-// instructions an element in each pass).
+// the memory's rate, which reads out of the 256 MB cache do not exceed: 8 x 64 x 512^2 float32 267 us
+// forward (moments 91, output 195 traced one by one; 6.0 TB/s with the second reading), with GELU and
+// dropout the same, although these keep the vector units over 80% busy in the output pass;
+// 2 x 20 x 128^3 float32 with GELU backward 265 (102 and 161; 6.3 TB/s).  Half data with GELU and dropout
+// are at the vector units' rate: 8 x 64 x 512^2 bfloat16 forward 165, without either 148; backward 305
+// (some 41 instructions an element in each pass), with GELU alone 249, without either 212.
 #include "groupnorm_device.h"
 
 namespace fno {

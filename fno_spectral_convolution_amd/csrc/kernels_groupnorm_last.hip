@@ -2,10 +2,12 @@
 // than a work-group holds, the same memory).  groupnorm_device.h has the mathematics.
 //
 // A thread keeps to four channels and goes down the rows, so that its weights, statistics and sums stay
-// in registers.  Two passes: 8 x 256^2 x 128 bfloat16 with SiLU 76.5 us, moments 26 (5.2 TB/s), a launch
-// that joins them 5, output 48 to 54 (5 TB/s); 4 x 96^2 x 320 half with SiLU and dropout backward 46,
-// sums 21, between 5, gradient 25: twelve rows a thread, whose setting out and sums over the work-group
-// are a third of the instructions.
+// in registers.  Two passes: 8 x 256^2 x 128 bfloat16 with SiLU 76.5 us, moments 25 (5.4 TB/s), a launch
+// that joins them 5, output 48 to 54 (5 TB/s), the same in float32 49, 5 and 108, backward 102, 5 and
+// 161 (all 5 TB/s and more); 4 x 96^2 x 320 half with SiLU and dropout backward 47, sums 21, between 5,
+// gradient 25: twelve rows a thread, whose setting out and sums over the work-group are a third of the
+// instructions.  There neither the memory (3.2 and 3.7 TB/s) nor the vector units (55 to 70% busy) are
+// full: four and five waves a SIMD, with 80 to 90 scalar registers of the arguments kept in vector ones.
 #include "groupnorm_device.h"
 
 namespace fno {

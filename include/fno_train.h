@@ -114,7 +114,7 @@ typedef struct fno_group_norm_desc {
   int64_t x_stride;       /* of x                                                */
   int64_t y_stride;       /* of y (forward), of grad_y (backward)                */
   int64_t grad_x_stride;  /* of grad_x (the forward does not look at it)         */
-  double eps;             /* finite, >= 0                                        */
+  double eps;             /* finite, >= 0; added as a float32                    */
 } fno_group_norm_desc;
 
 /* Bytes of workspace of the two calls on this descriptor (either may be 0, its workspace then
