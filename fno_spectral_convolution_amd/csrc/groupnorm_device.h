@@ -16,6 +16,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "dropout_device.h"
@@ -93,23 +94,26 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
 struct Moments {
   float n, mean, var;
 };
-// Squared deviations may pass float32's range where the variance does not.  sums(divided) adds a
-// thread's up, with the constant `divided` each divided before it is squared: an instruction an element
-// that is spent only where the sum without it came out infinite (or NaN, which it stays).
-template <typename F, typename G>
-__device__ __forceinline__ auto in_range(F&& sums, G&& var) {
-  auto v = sums(std::false_type());
-  if (__builtin_expect(!(var(v) <= 3.402823466e38f), 0)) v = sums(std::true_type());
-  return v;
-}
-template <typename D>
-__device__ __forceinline__ float square(float d, float inv_m, D divided) {
-  return divided.value ? d * inv_m * d : d * d;
-}
-template <typename D>
-__device__ __forceinline__ float share_of(float sq, float inv_m, D divided) {
-  return divided.value ? sq : sq * inv_m;
-}
+// Squared deviations and their sum may pass float32's range where the variance does not.  They are taken
+// of deviations times `down`, a power of two with down^2 <= 1 / m, so that their sum stays below the
+// variance; times `up`, below 4, it is the sum divided by m.  Neither rounds.  Made by the host: a
+// division and the steps after it were 2% of a call of many small groups.
+struct Scale {
+  float inv_m, down, up, back;  // 1 / m; back = 1 / down
+  Scale() = default;
+  explicit Scale(const GroupArgs& a)
+      : inv_m(1.0f / ((float)(a.channels / a.groups) * (float)a.npts)) {
+    int exponent;
+    std::frexp(inv_m, &exponent);  // 1 / m >= 2^(exponent - 1)
+    const int half = (2 - exponent) / 2;
+    down = std::ldexp(1.f, -half);
+    back = std::ldexp(1.f, half);
+    up = std::ldexp(inv_m, 2 * half);
+  }
+  __device__ __forceinline__ float deviation(float x, float mean) const {
+    return fmaf(x, down, -mean * down);
+  }
+};
 __device__ __forceinline__ void join(Moments& a, float n, float mean, float var, float inv_m) {
   const float all = a.n + n, share = n > 0.f ? n * __builtin_amdgcn_rcpf(all) : 0.f;
   const float d = mean - a.mean;

@@ -30,6 +30,7 @@ struct Strip {
   int tpp, kv, planes;    // log2 of the threads to a plane, vectors of a thread in it, planes
   int cg, runs, parts;    // channels of a group, strips along them, partial sums of a plane
   Divider by_parts, by_runs, by_groups;
+  Scale scale;
 };
 template <int VEC, int K, int BLOCK>
 Strip strip_of(const GroupArgs& a) {
@@ -56,6 +57,7 @@ Strip strip_of(const GroupArgs& a) {
   p.by_parts = Divider(p.parts);
   p.by_runs = Divider(p.runs);
   p.by_groups = Divider(a.groups);
+  p.scale = Scale(a);
   return p;
 }
 
@@ -122,9 +124,9 @@ struct Items {
 };
 
 // moments of a thread's vectors, one join for all
-template <typename T, int VEC, int K, typename D>
+template <typename T, int VEC, int K>
 __device__ __forceinline__ void add_moments(Moments& m, const Raw<T, VEC> (&raw)[K],
-                                            const int (&lo)[K], float inv_m, D divided) {
+                                            const int (&lo)[K], float inv_m, const Scale& scale) {
   float n = 0.f, sum = 0.f, sq = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -138,10 +140,10 @@ __device__ __forceinline__ void add_moments(Moments& m, const Raw<T, VEC> (&raw)
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const float d = element<T, VEC>(raw[k], e) - mean;
-      sq += e >= lo[k] ? square(d, inv_m, divided) : 0.f;
+      const float d = scale.deviation(element<T, VEC>(raw[k], e), mean);
+      sq += e >= lo[k] ? d * d : 0.f;
     }
-  join(m, n, mean, share_of(sq, inv_m, divided), inv_m);
+  join(m, n, mean, sq * scale.up, inv_m);
 }
 
 // y of one vector: x from its group's mean and by = gamma r, at = beta; element i of the field
@@ -166,7 +168,8 @@ __global__ __launch_bounds__(BLOCK) void k_gn_whole(GroupArgs a, Strip p, int64_
                                                     float* stats) {
   __shared__ float2 s_red[2][BLOCK / 64];
   const Dropper drop(a.drop);
-  const float inv_m = 1.0f / ((float)p.cg * (float)a.npts);
+  const Scale scale = p.scale;
+  const float inv_m = scale.inv_m;
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
     const Place q = place_of(w, p, a.groups);
     const Items<VEC, K, BLOCK> it(p, q, a.npts);
@@ -180,20 +183,15 @@ __global__ __launch_bounds__(BLOCK) void k_gn_whole(GroupArgs a, Strip p, int64_
     });
     if (BLOCK > 64) __syncthreads();
     const float mean = block_sum<BLOCK / 64>(sum, 0.f, s_red[0]).x * inv_m;
-    const float var = in_range(
-        [&](auto divided) {
-          float sq = 0.f;
-          it.each([&](int k, auto masked) {
+    float sq = 0.f;
+    it.each([&](int k, auto masked) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const float d = element<T, VEC>(raw[k], e) - mean;
-              sq += !masked.value || e >= it.lo[k] ? square(d, inv_m, divided) : 0.f;
-            }
-          });
-          return share_of(sq, inv_m, divided);
-        },
-        [](float v) { return v; });
-    const float rstd = rsqrtf(block_sum<BLOCK / 64>(var, 0.f, s_red[1]).x + a.eps);
+      for (int e = 0; e < VEC; ++e) {
+        const float d = scale.deviation(element<T, VEC>(raw[k], e), mean);
+        sq += !masked.value || e >= it.lo[k] ? d * d : 0.f;
+      }
+    });
+    const float rstd = rsqrtf(block_sum<BLOCK / 64>(sq * scale.up, 0.f, s_red[1]).x + a.eps);
     if (stats && threadIdx.x == 0) {
       stats[q.bg] = mean;
       stats[a.batch * a.groups + q.bg] = rstd;
@@ -251,36 +249,33 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats(GroupArgs a, Pass ps, const
                                                      float4* part) {
   __shared__ float2 s_red[2][kWaves];
   const Strip& p = ps.p;
-  const float inv_m = 1.0f / ((float)p.cg * (float)a.npts);
+  const Scale scale = p.scale;
+  const float inv_m = scale.inv_m;
   for (int64_t w = blockIdx.x; w < ps.items; w += gridDim.x) {
     const Place q = place_of(w, p, a.groups);
     const T* from = x + q.b * a.x_stride + q.channel * a.npts;
-    const auto own = [&](auto divided) {
-      Moments m = {0.f, 0.f, 0.f};
-      if (LONG) {
-        long_strips<VEC, K>(
-            p, q.s, a.npts,
-            [&](int64_t at) {
-              constexpr int none[K] = {};
-              Raw<T, VEC> raw[K];
-              load_strip<T, VEC, K>(from + at, raw);
-              add_moments<T, VEC, K>(m, raw, none, inv_m, divided);
-            },
-            [&](int64_t at, int lo) {
-              const Raw<T, VEC> v[1] = {load_raw<T, VEC>(from + at)};
-              const int own[1] = {lo};
-              add_moments<T, VEC, 1>(m, v, own, inv_m, divided);
-            });
-      } else {
-        const Items<VEC, K, kBlock> it(p, q, a.npts);
-        Raw<T, VEC> raw[K] = {};
-        it.load(from, raw);
-        add_moments<T, VEC, K>(m, raw, it.lo, inv_m, divided);
-      }
-      return m;
-    };
-    const Moments m = block_moments<kWaves>(in_range(own, [](const Moments& v) { return v.var; }),
-                                            inv_m, s_red);
+    Moments m = {0.f, 0.f, 0.f};
+    if (LONG) {
+      long_strips<VEC, K>(
+          p, q.s, a.npts,
+          [&](int64_t at) {
+            constexpr int none[K] = {};
+            Raw<T, VEC> raw[K];
+            load_strip<T, VEC, K>(from + at, raw);
+            add_moments<T, VEC, K>(m, raw, none, inv_m, scale);
+          },
+          [&](int64_t at, int lo) {
+            const Raw<T, VEC> v[1] = {load_raw<T, VEC>(from + at)};
+            const int own[1] = {lo};
+            add_moments<T, VEC, 1>(m, v, own, inv_m, scale);
+          });
+    } else {
+      const Items<VEC, K, kBlock> it(p, q, a.npts);
+      Raw<T, VEC> raw[K] = {};
+      it.load(from, raw);
+      add_moments<T, VEC, K>(m, raw, it.lo, inv_m, scale);
+    }
+    m = block_moments<kWaves>(m, inv_m, s_red);
     if (threadIdx.x == 0) part[w] = make_float4(m.n, m.mean, m.var, 0.f);
   }
 }
@@ -292,7 +287,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_apply(GroupArgs a, Pass ps, const
   __shared__ float2 s_red[2][kWaves];
   const Strip& p = ps.p;
   const Dropper drop(a.drop);
-  const float inv_m = 1.0f / ((float)p.cg * (float)a.npts);
+  const float inv_m = p.scale.inv_m;
   const int n = ps.joined;
   for (int64_t w = blockIdx.x; w < ps.items; w += gridDim.x) {
     const Place q = place_of(w, p, a.groups);
@@ -423,7 +418,7 @@ __global__ __launch_bounds__(BLOCK) void k_gn_whole_bwd(GroupArgs a, Strip p, in
   const bool weights = to_g || to_b;
   const Dropper drop(a.drop);
   const int64_t sides = a.batch * a.groups;
-  const float inv_m = 1.0f / ((float)p.cg * (float)a.npts);
+  const float inv_m = p.scale.inv_m;
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
     const Place q = place_of(w, p, a.groups);
     const Items<VEC, K, BLOCK> it(p, q, a.npts);
@@ -619,7 +614,7 @@ __global__ __launch_bounds__(kBlock) void k_gn_grad(GroupArgs a, Pass ps, const 
       const float2 v = sums.of(a, z.part, gamma, q.b, q.bg - q.b * a.groups);
       __syncthreads();
       m = block_sum<kWaves>(v.x, v.y, s_red);
-      const float inv = 1.0f / ((float)p.cg * (float)a.npts);
+      const float inv = p.scale.inv_m;
       m = make_float2(m.x * inv, m.y * inv);
     } else {
       m = z.means[q.bg];
@@ -709,7 +704,7 @@ __device__ __forceinline__ float slot_sum(float v, float (&s)[2][BLOCK / 64], in
 // `stride` slots in the launch: a multiple of the groups, `rows` times as many
 template <typename T, int VEC, int TPR, int NV, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void k_gn_rows(GroupArgs a, int cg, Divider by_groups,
-                                                   int64_t stride, int64_t rows, bool stream,
+                                                   Scale scale, int64_t stride, int64_t rows, bool stream,
                                                    const T* x,
                                                    const float* gamma, const float* beta, T* y,
                                                    float* stats) {
@@ -717,7 +712,7 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows(GroupArgs a, int cg, Divider 
   __shared__ float s_sum[2][BLOCK / 64];
   const Dropper drop(a.drop);
   const int t = threadIdx.x % TPR;
-  const float inv = 1.0f / (float)cg;
+  const float inv = scale.inv_m;
   const int64_t total = a.batch * a.groups, slot = (int64_t)blockIdx.x * kSlots + threadIdx.x / TPR;
   const int64_t row0 = by_groups.of(slot);
   const int group = (int)(slot - row0 * a.groups), first = group * cg;
@@ -747,7 +742,7 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows(GroupArgs a, int cg, Divider 
   fetch(b);
   for (int64_t at = (int64_t)blockIdx.x * kSlots; at < total; at += stride, b += rows) {
     const bool live = b < a.batch;
-    float f[NV][VEC], sum = 0.f;
+    float f[NV][VEC], sum = 0.f, sq = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) unpack<T, VEC>(next[k], f[k]);
     if (at + stride < total) fetch(b + rows);
@@ -758,31 +753,24 @@ __global__ __launch_bounds__(BLOCK) void k_gn_rows(GroupArgs a, int cg, Divider 
         for (int e = 0; e < VEC; ++e) sum += !masked.value || e >= lo[k] ? f[k][e] : 0.f;
     });
     const float mean = slot_sum<TPR, BLOCK>(sum, s_sum, flip) * inv;
+    by_mask(partial, [&](auto masked) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+      for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) f[k][e] -= mean;
-    const float var = in_range(
-        [&](auto divided) {
-          float sq = 0.f;
-          by_mask(partial, [&](auto masked) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-              for (int e = 0; e < VEC; ++e)
-                sq += !masked.value || e >= lo[k] ? square(f[k][e], inv, divided) : 0.f;
-          });
-          return share_of(sq, inv, divided);
-        },
-        [](float v) { return v; });
-    const float rstd = rsqrtf(slot_sum<TPR, BLOCK>(var, s_sum, flip) + a.eps);
+        for (int e = 0; e < VEC; ++e) {
+          f[k][e] = scale.deviation(f[k][e], mean);
+          sq += !masked.value || e >= lo[k] ? f[k][e] * f[k][e] : 0.f;
+        }
+    });
+    const float rstd = rsqrtf(slot_sum<TPR, BLOCK>(sq * scale.up, s_sum, flip) + a.eps);
     if (!live) continue;
+    const float by = rstd * scale.back;
     T* o = y + b * a.y_stride;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if (lo[k] >= VEC) continue;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) f[k][e] = fmaf(f[k][e] * rstd, ga[k][e], be[k][e]);
+      for (int e = 0; e < VEC; ++e) f[k][e] = fmaf(f[k][e] * by, ga[k][e], be[k][e]);
       activate(f[k], a.act);
       if (a.drop.threshold)
         drop.apply<VEC>(f[k], drop.mask<VEC>((uint64_t)(b * a.channels + start[k])));
@@ -1031,7 +1019,7 @@ hipError_t rows_fwd(const GroupArgs& a, const T* x, const float* gamma, const fl
       const int64_t need = ceil_div(a.batch * a.groups, kSlots), most = 1024 * kBlock / kB;
       const int64_t groups = unit * std::max<int64_t>(1, std::min(ceil_div(need, unit), most / unit));
       hipLaunchKernelGGL((k_gn_rows<T, vec.value, TPR, nv.value, kB>), dim3(groups), dim3(kB), 0, s,
-                         a, a.channels / a.groups, Divider(a.groups), groups * kSlots,
+                         a, a.channels / a.groups, Divider(a.groups), Scale(a), groups * kSlots,
                          groups * kSlots / a.groups, stream_out<T>(a), x, gamma, beta, y, stats);
     });
   });

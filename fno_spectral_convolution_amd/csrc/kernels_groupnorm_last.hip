@@ -31,6 +31,7 @@ struct Tiles : Cut {
   int64_t segments;
   bool paired;               // lanes 2 j and 2 j + 1 have neighbouring vectors of eight aligned elements
   Divider by_tc, by_tr, by_cols, by_cg, by_blocks;
+  Scale scale;
 };
 template <int VEC>
 Tiles tiles_of(const GroupArgs& a, int least, int most, int longest = 1 << 22) {
@@ -63,6 +64,7 @@ Tiles tiles_of(const GroupArgs& a, int least, int most, int longest = 1 << 22) {
   p.by_cg = Divider(p.cg);
   p.by_blocks = Divider(p.blocks);
   p.by_tiles = Divider(p.tiles);
+  p.scale = Scale(a);
   return p;
 }
 // Whether the second pass joins the parts for itself, which saves a launch: few enough for
@@ -185,19 +187,16 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats_last(GroupArgs a, Tiles p, 
                                                           const T* x, float2* part) {
   __shared__ float2 s_mom[kBlock * VEC];  // [tr][cols]
   __shared__ float s_set[kBlock], s_mean[32 * VEC];
-  const float inv_m = 1.0f / ((float)p.cg * (float)a.npts);
+  const Scale scale = p.scale;
+  const float inv_m = scale.inv_m;
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
     const Block q = block_of(w, a, p);
     int r, c, lo;
     vector_of<VEC>(q, p, a.channels, r, c, lo);
-    struct {
-      float mean[VEC], var[VEC];
-    } m;
-    const auto moments = [&](auto divided) {
-      decltype(m) v;
-      float n = 0.f;
-      fill(v.mean, 0.f);
-      fill(v.var, 0.f);
+    float n = 0.f, mean[VEC], var[VEC];
+    fill(mean, 0.f);
+    fill(var, 0.f);
+    if (lo < VEC) {
       const T* from = x + q.b * a.x_stride;
       const int64_t own = (int64_t)r * a.channels + c;
       tile_rows<K>(p, q, r, a.channels, [&](int64_t at, int more, auto all) {
@@ -211,32 +210,24 @@ __global__ __launch_bounds__(kBlock) void k_gn_stats_last(GroupArgs a, Tiles p, 
           float sum = 0.f, sq = 0.f;
 #pragma unroll
           for (int k = 0; k < K; ++k) sum += element<T, VEC>(raw[k], e);  // (zeros beyond `more`)
-          const float mean = sum * inv;
+          const float m = sum * inv;
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            const float d = element<T, VEC>(raw[k], e) - mean;
-            sq += all.value || k < more ? square(d, inv_m, divided) : 0.f;
+            const float d = scale.deviation(element<T, VEC>(raw[k], e), m);
+            sq += all.value || k < more ? d * d : 0.f;
           }
-          const float d = mean - v.mean[e];
-          v.mean[e] += d * share;
-          v.var[e] += share_of(sq, inv_m, divided) + (d * between) * d;
+          const float d = m - mean[e];
+          mean[e] += d * share;
+          var[e] += sq * scale.up + (d * between) * d;
         }
         n = seen;
       });
-      return v;
-    };
-    if (lo < VEC)
-      m = in_range(moments, [](const auto& v) {
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) sum += v.var[e];
-        return sum;
-      });
+    }
     __syncthreads();
     if (lo < VEC)
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
-        if (e >= lo) s_mom[r * p.cols + c + e - q.c0] = make_float2(m.mean[e], m.var[e]);
+        if (e >= lo) s_mom[r * p.cols + c + e - q.c0] = make_float2(mean[e], var[e]);
     __syncthreads();
     // the row slots' moments of a segment: their mean first, then the deviations about it
     const Columns col(p);
